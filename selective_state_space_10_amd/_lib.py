@@ -17,6 +17,19 @@ EXPORTS = ("ssm_abi_version", "ssm_status_string", "ssm_last_error", "ssm_scan_c
            "ssm_scan_bwd_conv_workspace_bytes", "ssm_scan_bwd_conv", "ssm_scan_fwd_plan",
            "ssm_scan_fwd_noalloc", "ssm_affine_scan")
 
+# every symbol include/ssm_block.h declares
+BLOCK_EXPORTS = ("ssm_block_abi_version", "ssm_decay_attn_fwd_workspace_bytes",
+                 "ssm_decay_attn_fwd", "ssm_decay_attn_bwd_workspace_bytes", "ssm_decay_attn_bwd",
+                 "ssm_decay_attn_update", "ssm_residual_norm_fwd",
+                 "ssm_residual_norm_bwd_workspace_bytes", "ssm_residual_norm_bwd",
+                 "ssm_gated_norm_fwd", "ssm_gated_norm_bwd_workspace_bytes", "ssm_gated_norm_bwd")
+
+
+class View4(ctypes.Structure):
+    """ssm_view4: a (batch, step, head, element) tensor's pointer and strides."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_batch", ctypes.c_int64),
+                ("stride_step", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
 
 class FwdPlan(ctypes.Structure):
     """ssm_fwd_plan: kernel (0 all-purpose, 1 wave-specialised), channels per
@@ -90,6 +103,32 @@ def load() -> ctypes.CDLL:
     lib.ssm_scan_fwd_noalloc.argtypes = [I64] * 4 + [INT] + [P] * 8 + [INT] + [P] * 5 + [INT]
     lib.ssm_scan_fwd_plan.restype = INT
     lib.ssm_scan_fwd_plan.argtypes = [I64] * 4 + [INT, INT, INT, ctypes.POINTER(FwdPlan)]
+    F, V = ctypes.c_float, ctypes.POINTER(View4)
+    lib.ssm_block_abi_version.restype = INT
+    lib.ssm_block_abi_version.argtypes = []
+    for name in ("ssm_decay_attn_fwd", "ssm_decay_attn_bwd"):
+        getattr(lib, name + "_workspace_bytes").restype = I64
+        getattr(lib, name + "_workspace_bytes").argtypes = [I64] * 6 + [INT]
+        getattr(lib, name).restype = INT
+    lib.ssm_decay_attn_fwd.argtypes = [I64] * 6 + [INT, V, V, V, P, INT, F] + [P] * 4 + [I64, P]
+    lib.ssm_decay_attn_bwd.argtypes = [I64] * 6 + [INT, V, V, V, P, INT, F, P, V] + [P] * 7 \
+        + [I64, P]
+    lib.ssm_decay_attn_update.restype = INT
+    lib.ssm_decay_attn_update.argtypes = [I64] * 5 + [INT, P, V, V, V, P, INT, F, P, P]
+    lib.ssm_residual_norm_fwd.restype = INT
+    lib.ssm_residual_norm_fwd.argtypes = [I64, I64, INT, INT, P, I64, P, P, P, F, P, P, P, P]
+    lib.ssm_residual_norm_bwd_workspace_bytes.restype = I64
+    lib.ssm_residual_norm_bwd_workspace_bytes.argtypes = [I64, I64]
+    lib.ssm_residual_norm_bwd.restype = INT
+    lib.ssm_residual_norm_bwd.argtypes = [I64, I64, INT, INT] + [P] * 6 + [I64] + [P] * 6 \
+        + [I64, P]
+    lib.ssm_gated_norm_fwd.restype = INT
+    lib.ssm_gated_norm_fwd.argtypes = [I64] * 3 + [INT, P, I64, P, I64, P, F, INT, P, P, P]
+    lib.ssm_gated_norm_bwd_workspace_bytes.restype = I64
+    lib.ssm_gated_norm_bwd_workspace_bytes.argtypes = [I64] * 3
+    lib.ssm_gated_norm_bwd.restype = INT
+    lib.ssm_gated_norm_bwd.argtypes = [I64] * 3 + [INT, P, P, I64, P, I64, P, P, INT] + [P] * 4 \
+        + [I64, P]
     _lib = lib
     return lib
 

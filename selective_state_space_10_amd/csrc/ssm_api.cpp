@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "../../include/ssm_scan.h"
+#include "api_error.hpp"
 #include "kernels.hpp"
 
 namespace {
@@ -73,6 +74,22 @@ int hip_status(hipError_t e, const char *what) {
 }
 
 }  // namespace
+
+namespace ssm {
+
+void api_clear_error() { g_last_error[0] = 0; }
+
+int api_fail(int status, const char *fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+  va_end(ap);
+  return status;
+}
+
+int api_hip_status(hipError_t e, const char *what) { return hip_status(e, what); }
+
+}  // namespace ssm
 
 extern "C" {
 
