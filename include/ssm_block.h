@@ -61,7 +61,8 @@ typedef struct ssm_view4 {
  *   state_final: the same shape, NULL = not wanted
  *   o:         (batch, seqlen, heads, dv) contiguous, io_dtype
  *
- * Sizes: batch, seqlen >= 1; 1 <= heads <= 65536; dk, dv multiples of 8 from 8 to 256.
+ * Sizes: batch, seqlen >= 1; 1 <= heads <= 65536; batch * heads <= 2^26; dk, dv
+ * multiples of 8 from 8 to 256; heads * dk, heads * dv and step strides <= 2^23.
  * A NaN or an infinity at one step reaches no earlier step.
  */
 int64_t ssm_decay_attn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,

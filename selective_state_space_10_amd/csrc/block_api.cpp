@@ -16,6 +16,7 @@ namespace {
 constexpr int64_t kMaxElems = (int64_t)1 << 40;      // of one tensor
 constexpr int64_t kMaxBatchHeads = (int64_t)1 << 26; // workgroups of one launch stay below 2^31
 constexpr int64_t kMaxRow = 16384;
+constexpr int64_t kMaxStep = (int64_t)1 << 23;       // elements from one step to the next
 
 bool product_ok(int64_t a, int64_t b, int64_t *out) {
   if (b > kMaxElems / a) return false;
@@ -40,6 +41,8 @@ int check_attn(int64_t batch, int64_t seqlen, int64_t heads, int64_t key_heads, 
   if (heads > 65536) return api_fail(SSM_ERR_UNSUPPORTED, "heads=%lld exceeds 65536", (long long)heads);
   if (batch > kMaxBatchHeads / heads)
     return api_fail(SSM_ERR_UNSUPPORTED, "batch * heads exceeds 2^26 (batch=%lld heads=%lld)", (long long)batch, (long long)heads);
+  if (heads * (dk > dv ? dk : dv) > kMaxStep)  // offsets inside a chunk of 64 steps are 32-bit bytes
+    return api_fail(SSM_ERR_UNSUPPORTED, "heads * max(dk, dv) exceeds 2^23");
   int64_t n;
   if (!product_ok(batch * heads, seqlen, &n) || !product_ok(n, dk > dv ? dk : dv, &n))
     return api_fail(SSM_ERR_BAD_SHAPE, "tensors of more than 2^40 elements");
@@ -54,6 +57,7 @@ int check_view(const char *name, const ssm_view4 *v, int io_dtype) {
     if (s < 0 || s > kMaxElems) return api_fail(SSM_ERR_BAD_SHAPE, "%s has stride %lld", name, (long long)s);
     if (s * es % 16 != 0) return api_fail(SSM_ERR_ALIGNMENT, "%s has stride %lld, not a multiple of 16 bytes", name, (long long)s);
   }
+  if (v->stride_step > kMaxStep) return api_fail(SSM_ERR_UNSUPPORTED, "%s has a step stride over 2^23 elements", name);
   if (((uintptr_t)v->ptr & 15u) != 0) return api_fail(SSM_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
   return SSM_OK;
 }

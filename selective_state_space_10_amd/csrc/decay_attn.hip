@@ -27,54 +27,69 @@ struct Split {
   int64_t seg_len;
 };
 
-Split split_of(int64_t L) { return {1, L}; }
+int cols_of(int64_t dc) { return da_waves(dc) * 16; }
+int64_t slices_of(int64_t dc) { return (dc + cols_of(dc) - 1) / cols_of(dc); }
 
-struct FwdPlanDa {
-  Split sp;
-  int64_t nslice, tile;
-};
+int64_t compute_units() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v < 1) v = 256;
+    return v;
+  }();
+  return n;
+}
+
+// A sequence is split where batch rows, heads and slices do not fill the card:
+// into so many segments that every CU has the workgroups that its LDS holds, of
+// at least kMinSegment steps.  Measured, bf16, forward: 8 x 2048, 16 heads of
+// 128: 188 us in one piece, 118 us in 2, 111 us in 4, 149 us in 8 segments;
+// 1 x 32768, 40 heads of 128: 2.7 ms in one piece, 552 us in 32, 738 us in 128;
+// 3 x 1111, 8 heads of 72 x 96, fp32: 204 us in one piece, 81 us in 5, 54 us in 9.
+constexpr int64_t kMinSegment = 64;
+Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc) {
+  const int64_t wgs = bh * slices_of(dc), want = compute_units() * (padded(da) > 128 ? 1 : da_waves(dc) == 8 ? 2 : 3);
+  int64_t n = (want + wgs - 1) / wgs;
+  if (n > L / kMinSegment) n = L / kMinSegment;
+  if (n <= 1) return {1, L};
+  const int64_t len = ((L + n - 1) / n + 63) / 64 * 64;
+  return {(int)((L + len - 1) / len), len};
+}
+
+// From how many segments on the states before them are computed once, by a
+// kernel of its own, and not by every workgroup from the end states before it
+// (32 segments of 40 heads of 128: 552 us against 597 us; 4 segments of the
+// 8 x 2048 shape: no difference beyond the launch).
+constexpr int kCombineFrom = 5;
 
 }  // namespace
 
-// The decays' gradient from the dot products of the main pass:
-//   dg_t = sum_{r >= t in the segment} (q_r . dq_r - k_r . dk_r) + <exp(g) S, R> at the segment's end,
-// where S and R are the states that both directions carry over that boundary:
-// what crosses t is the products of pairs around t, and starting the sum at
-// every segment's end keeps rounding from adding up over the sequence.  (The
-// dot products leave out pairs with no decay between, decay_attn.hpp.)  One
-// workgroup per segment; the running sum is fp64.
+// The decays' gradient from the dot products of the main passes:
+//   dg_t = sum_{r >= t up to the next edge} (q_r . dq_r - k_r . dk_r) + <exp(g) S, R> at that edge,
+// where S and R are the states that both directions carry over it: what crosses
+// t is the products of pairs around t.  (The dot products leave out pairs with
+// no decay between, decay_attn.hpp.)  Edges bound the length over which rounding
+// adds up.  One workgroup per edge; the running sum is fp64.
 struct DaDecayGrad {
-  const float *dots_q, *dots_k;   // (parts, BH, L)
-  const float *edge_q, *edge_k;   // NULL = no boundary terms
+  const float *dots_q, *dots_k;   // (slices, BH, L)
+  const float *edge_dot;          // (parts, BH, nblock)
   const float *g;
-  int64_t g_b, g_t, L, seg_len, edge_size;
-  int H, BH, nseg, parts, last_edge;
+  int64_t g_b, g_t, L;
+  int H, BH, nblock, edge_len, last_edge, slices, parts;
   float *out;       // (B, L, H), or NULL
-  float *sums;      // (BH, nseg) sums over the segment, or NULL
+  float *sums;      // (BH, nblock) sums over the steps before an edge, or NULL
 };
 
 __global__ void __launch_bounds__(256) decay_grad_kernel(DaDecayGrad a) {
   __shared__ double wsum[4];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int bh = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
+  const int bh = blockIdx.x / a.nblock, blk = blockIdx.x % a.nblock;
   const int h = bh % a.H;
   const int64_t b = bh / a.H;
-  const int64_t t0 = seg * a.seg_len, t1 = min(a.L, t0 + a.seg_len);
+  const int64_t t0 = (int64_t)blk * a.edge_len, t1 = min(a.L, t0 + a.edge_len);
   const float *pg = a.g + b * a.g_b + h;
-  auto block_sum = [&](double v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    __syncthreads();
-    if (lane == 0) wsum[w] = v;
-    __syncthreads();
-    return wsum[0] + wsum[1] + wsum[2] + wsum[3];
-  };
   double carry = 0.0;
-  if (a.edge_q && (seg + 1 < a.nseg || a.last_edge)) {
-    const int64_t o = ((int64_t)bh * (a.nseg + 1) + seg + 1) * a.edge_size;
-    double v = 0.0;
-    for (int64_t i = threadIdx.x; i < a.edge_size; i += 256) v += (double)a.edge_q[o + i] * a.edge_k[o + i];
-    carry = block_sum(v);
+  if (blk + 1 < a.nblock || a.last_edge) {
+    for (int p = 0; p < a.parts; ++p) carry += a.edge_dot[((int64_t)p * a.BH + bh) * a.nblock + blk];
     if (t1 < a.L) carry *= fast_exp2(decay_log2(pg[t1 * a.g_t]));
   }
   double total = 0.0;
@@ -83,15 +98,11 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DaDecayGrad a) {
     const int64_t t = hi - 1 - threadIdx.x;
     double v = 0.0;
     if (t >= t0)
-      for (int p = 0; p < a.parts; ++p) {
+      for (int p = 0; p < a.slices; ++p) {
         const int64_t o = ((int64_t)p * a.BH + bh) * a.L + t;
         v += (double)a.dots_q[o] - (double)a.dots_k[o];
       }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_up(v, d, 64);
-      if (lane >= d) v += o;
-    }
+    v = wave_sum_scan(v);
     __syncthreads();
     if (lane == 63) wsum[w] = v;
     __syncthreads();
@@ -106,18 +117,64 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DaDecayGrad a) {
     }
   }
   if (a.sums) {
-    total = block_sum(total);
-    if (threadIdx.x == 0) a.sums[blockIdx.x] = (float)total;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) total += __shfl_xor(total, d, 64);
+    __syncthreads();
+    if (lane == 0) wsum[w] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) a.sums[blockIdx.x] = (float)(wsum[0] + wsum[1] + wsum[2] + wsum[3]);
   }
 }
 
-// One decay per head: the sum over batch rows and segments.
-__global__ void __launch_bounds__(64) decay_grad_heads_kernel(const float *sums, int B, int H, int nseg, float *out) {
+// The states before every segment from the end states of the ones before it
+// (in place): one thread per 4 elements, in the order of the recurrence.
+__global__ void __launch_bounds__(256) combine_kernel(DaArgs a, int da_padded, int cols) {
+  const DaRole &R = a.role[blockIdx.y];
+  const int64_t tile4 = (int64_t)da_padded * cols / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= tile4 * a.nslice * a.BH) return;
+  const int64_t bh = i / (tile4 * a.nslice), x = i % (tile4 * a.nslice);
+  f32x4 cur = {0, 0, 0, 0};
+  if (R.state_in) {
+    // element of the tile as decay_attn_kernel lays it out: waves, row tiles, lanes
+    const int slice = (int)(x / tile4), y = (int)(x % tile4), lane = y & 63, dt = (y >> 6) % (da_padded / 16), w = (y >> 6) / (da_padded / 16);
+    const int row = dt * 16 + (lane >> 4) * 4, col = slice * cols + w * 16 + (lane & 15), da = (int)a.da, dc = (int)a.dc;
+    const float *s = R.state_in + bh * da * dc;
+    for (int r = 0; r < 4; ++r)
+      if (row + r < da && col < dc) cur[r] = s[R.state_in_t ? col * da + row + r : (row + r) * dc + col];
+  }
+  const int64_t step = tile4 * a.nslice;
+  f32x4 *p = (f32x4 *)R.loc + bh * a.nseg * step + x;
+  const float *tot = R.tot + bh * a.nseg;
+  const int first = R.reverse ? a.nseg - 1 : 0, dir = R.reverse ? -1 : 1;
+  int j = 0;
+  constexpr int U = 8;  // loads under way
+  for (; j + U < a.nseg; j += U) {
+    f32x4 l[U];
+    float e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) l[u] = p[(first + dir * (j + u)) * step], e[u] = tot[first + dir * (j + u)];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      p[(first + dir * (j + u)) * step] = cur;
+      cur = cur * e[u] + l[u];
+    }
+  }
+  for (; j < a.nseg; ++j) {
+    f32x4 l = cur;
+    float e = 0.0f;
+    if (j + 1 < a.nseg) l = p[(first + dir * j) * step], e = tot[first + dir * j];
+    p[(first + dir * j) * step] = cur;
+    cur = cur * e + l;
+  }
+}
+
+// One decay per head: the sum over batch rows and steps.
+__global__ void __launch_bounds__(64) decay_grad_heads_kernel(const float *sums, int B, int H, int nblock, float *out) {
   const int h = blockIdx.x * 64 + threadIdx.x;
   if (h >= H) return;
   double v = 0.0;
   for (int b = 0; b < B; ++b)
-    for (int s = 0; s < nseg; ++s) v += sums[((int64_t)b * H + h) * nseg + s];
+    for (int s = 0; s < nblock; ++s) v += sums[((int64_t)b * H + h) * nblock + s];
   out[h] = (float)v;
 }
 
@@ -138,20 +195,37 @@ __global__ void __launch_bounds__(256) shared_heads_kernel(const float *part, in
 
 namespace {
 
-hipError_t launch_kernel(const DaArgs &a, int io_dtype, bool precise, bool state_only, hipStream_t s) {
-  return io_dtype == 0 ? launch_decay_attn_f32(a, padded(a.da), precise, state_only, s)
-                       : launch_decay_attn_bf16(a, padded(a.da), precise, state_only, s);
+hipError_t launch_kernel(const DaArgs &a, int io_dtype, bool dots, bool state_only, hipStream_t s) {
+  return io_dtype == 0 ? launch_decay_attn_f32(a, padded(a.da), dots, state_only, s)
+                       : launch_decay_attn_bf16(a, padded(a.da), dots, state_only, s);
 }
 
-DaArgs base_args(const DecayAttnArgs &a, int64_t da, int64_t dc, Split sp) {
+// Both passes of a set of roles.
+hipError_t launch_passes(const DaArgs &a, int io_dtype, bool dots, hipStream_t s) {
+  hipError_t e;
+  if (a.nseg > 1) {
+    if ((e = launch_kernel(a, io_dtype, false, true, s)) != hipSuccess) return e;
+    if (a.combined) {
+      const int64_t n = (int64_t)padded(a.da) * cols_of(a.dc) / 4 * a.nslice * a.BH;
+      hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((n + 255) / 256), a.nroles), dim3(256), 0, s, a, padded(a.da), cols_of(a.dc));
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  }
+  return launch_kernel(a, io_dtype, dots, false, s);
+}
+
+DaArgs base_args(const DecayAttnArgs &a, int64_t da, int64_t dc) {
+  const Split sp = split_of(a.L, a.B * a.H, da, dc);
   DaArgs r{};
+  r.combined = sp.nseg >= kCombineFrom;
   r.L = a.L, r.da = da, r.dc = dc, r.g = a.g, r.g_b = a.g_b, r.g_t = a.g_t;
+  r.nroles = 1;
   r.H = (int)a.H, r.BH = (int)(a.B * a.H), r.nseg = sp.nseg, r.seg_len = sp.seg_len;
-  r.nslice = (int)((dc + kDaCols - 1) / kDaCols);
+  r.nslice = (int)slices_of(dc);
   return r;
 }
 
-int64_t edge_size(int64_t da, int64_t dc) { return (int64_t)padded(da) * kDaCols * ((dc + kDaCols - 1) / kDaCols); }
+int64_t edge_size(int64_t da, int64_t dc) { return padded(da) * cols_of(dc) * slices_of(dc); }
 
 void take_segments(Carve &c, DaRole &r, const DaArgs &a) {
   if (a.nseg == 1) return;
@@ -160,8 +234,7 @@ void take_segments(Carve &c, DaRole &r, const DaArgs &a) {
 }
 
 DaArgs fwd_args(const DecayAttnArgs &a, Carve &c) {
-  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L));
-  r.nroles = 1;
+  DaArgs r = base_args(a, a.dk, a.dv);
   DaRole &o = r.role[0];
   o.a = a.q, o.b = a.k, o.c = a.v;
   o.out = a.o;
@@ -171,19 +244,28 @@ DaArgs fwd_args(const DecayAttnArgs &a, Carve &c) {
   return r;
 }
 
+// Steps between two edges: the shortest power of two for which writing and
+// reading the states there (8 bytes per element) stays within an eighth of the
+// bytes that the three passes read and write per step (8 rows of each kind).
+int edge_len_of(const DecayAttnArgs &a, int es) {
+  const int64_t state = 8 * padded(a.dv) * cols_of(a.dk) * slices_of(a.dk), step = es * (a.dk + a.dv);
+  int e = 64;
+  while (e < 1024 && state > (int64_t)e * step) e *= 2;
+  return e;
+}
+
 struct BwdSet {
-  DaArgs qk, v;          // dq and dk (state dv x dk), dv (state dk x dv)
+  DaArgs q, k, v;        // dq and dk: state dv x dk; dv: state dk x dv
   float *dq_part, *dk_part, *sums;
-  bool want_g, edges;
+  bool want_g;
 };
 
-BwdSet bwd_args(const DecayAttnArgs &a, bool want_g, Carve &c) {
+BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
   BwdSet r{};
-  const Split sp = split_of(a.L);
+  const int edge_len = edge_len_of(a, io_dtype == 0 ? 4 : 2);
   r.want_g = want_g;
-  r.qk = base_args(a, a.dv, a.dk, sp), r.v = base_args(a, a.dk, a.dv, sp);
-  r.qk.nroles = 2, r.v.nroles = 1;
-  DaRole &q = r.qk.role[0], &k = r.qk.role[1], &v = r.v.role[0];
+  r.q = r.k = base_args(a, a.dv, a.dk), r.v = base_args(a, a.dk, a.dv);
+  DaRole &q = r.q.role[0], &k = r.k.role[0], &v = r.v.role[0];
   q.a = a.dout, q.b = a.v, q.c = a.k, q.e = a.q;
   k.a = a.v, k.b = a.dout, k.c = a.q, k.e = a.k;
   v.a = a.k, v.b = a.q, v.c = a.dout;
@@ -192,21 +274,22 @@ BwdSet bwd_args(const DecayAttnArgs &a, bool want_g, Carve &c) {
   q.state_in = a.state0, q.state_in_t = 1, k.state_in_t = 1;
   v.state_out = a.dstate0;
   q.out = a.dq, k.out = a.dk_out, v.out = a.dv_out;
-  take_segments(c, q, r.qk), take_segments(c, k, r.qk), take_segments(c, v, r.v);
+  take_segments(c, q, r.q), take_segments(c, k, r.k), take_segments(c, v, r.v);
   if (a.G < a.H) {
     const int64_t n = a.B * a.L * a.H * a.dk;
     q.out = r.dq_part = c.take<float>(n), k.out = r.dk_part = c.take<float>(n);
     q.out_f32 = k.out_f32 = 1;
   }
   if (want_g) {
-    const int64_t n = a.B * a.H * a.L * r.qk.nslice * kDaWaves;
+    const int64_t n = a.B * a.H * a.L * r.q.nslice;
     q.dots = c.take<float>(n), k.dots = c.take<float>(n);
-    // taken whether dstate_final is given or not: the workspace's size goes by the shape
-    const int64_t m = a.B * a.H * (sp.nseg + 1) * edge_size(a.dv, a.dk);
-    float *eq = c.take<float>(m), *ek = c.take<float>(m);
-    r.edges = sp.nseg > 1 || a.dstate_final;
-    if (r.edges) q.edge = eq, k.edge = ek;
-    r.sums = c.take<float>(a.B * a.H * sp.nseg);
+    // an edge after the last step is there whether dstate_final is given or not: the size goes by the shape
+    const int inner = (int)((a.L - 1) / edge_len);
+    r.q.edge_shift = r.k.edge_shift = __builtin_ctz(edge_len);
+    r.q.nedge = r.k.nedge = inner + 1, r.q.last_edge = r.k.last_edge = a.dstate_final != nullptr;
+    q.edge = k.edge = c.take<float>(a.B * a.H * (inner + 1) * edge_size(a.dv, a.dk));
+    q.edge_dot = c.take<float>(a.B * a.H * (inner + 1) * r.q.nslice * da_waves(a.dk));
+    r.sums = c.take<float>(a.B * a.H * (inner + 1));
   }
   return r;
 }
@@ -219,44 +302,37 @@ int64_t decay_attn_fwd_workspace_bytes(const DecayAttnArgs &a, int) {
   return c.used;
 }
 
-int64_t decay_attn_bwd_workspace_bytes(const DecayAttnArgs &a, int) {
+int64_t decay_attn_bwd_workspace_bytes(const DecayAttnArgs &a, int io_dtype) {
   Carve c{nullptr};
-  bwd_args(a, true, c);
+  bwd_args(a, io_dtype, true, c);
   return c.used;
 }
 
 hipError_t launch_decay_attn_fwd(const DecayAttnArgs &a, int io_dtype, hipStream_t s) {
   Carve c{(char *)a.workspace};
-  const DaArgs r = fwd_args(a, c);
-  if (r.nseg > 1) {
-    const hipError_t e = launch_kernel(r, io_dtype, false, true, s);
-    if (e != hipSuccess) return e;
-  }
-  return launch_kernel(r, io_dtype, false, false, s);
+  return launch_passes(fwd_args(a, c), io_dtype, false, s);
 }
 
 hipError_t launch_decay_attn_bwd(const DecayAttnArgs &a, int io_dtype, hipStream_t s) {
   Carve c{(char *)a.workspace};
-  const BwdSet r = bwd_args(a, a.dlog_decay != nullptr, c);
+  const BwdSet r = bwd_args(a, io_dtype, a.dlog_decay != nullptr, c);
   hipError_t e;
-  if (r.qk.nseg > 1) {
-    if ((e = launch_kernel(r.qk, io_dtype, false, true, s)) != hipSuccess) return e;
-    if ((e = launch_kernel(r.v, io_dtype, false, true, s)) != hipSuccess) return e;
-  }
-  if ((e = launch_kernel(r.qk, io_dtype, r.want_g, false, s)) != hipSuccess) return e;
-  if ((e = launch_kernel(r.v, io_dtype, false, false, s)) != hipSuccess) return e;
+  // backward in time first: it writes the states that the forward pass dots at edges
+  for (const DaArgs *p : {&r.k, &r.v, &r.q})
+    if ((e = launch_passes(*p, io_dtype, r.want_g && p != &r.v, s)) != hipSuccess) return e;
   if (r.want_g) {
     DaDecayGrad d{};
-    d.dots_q = r.qk.role[0].dots, d.dots_k = r.qk.role[1].dots;
-    d.edge_q = r.qk.role[0].edge, d.edge_k = r.qk.role[1].edge;
-    d.g = a.g, d.g_b = a.g_b, d.g_t = a.g_t, d.L = a.L, d.seg_len = r.qk.seg_len, d.edge_size = edge_size(a.dv, a.dk);
-    d.H = (int)a.H, d.BH = (int)(a.B * a.H), d.nseg = r.qk.nseg, d.parts = r.qk.nslice * kDaWaves, d.last_edge = a.dstate_final != nullptr;
+    d.dots_q = r.q.role[0].dots, d.dots_k = r.k.role[0].dots, d.edge_dot = r.q.role[0].edge_dot;
+    d.g = a.g, d.g_b = a.g_b, d.g_t = a.g_t, d.L = a.L;
+    d.H = (int)a.H, d.BH = (int)(a.B * a.H), d.edge_len = 1 << r.q.edge_shift;
+    d.nblock = r.q.nedge, d.last_edge = r.q.last_edge;
+    d.slices = r.q.nslice, d.parts = r.q.nslice * da_waves(a.dk);
     const bool heads = a.g_t == 0;
     d.out = heads ? nullptr : a.dlog_decay, d.sums = heads ? r.sums : nullptr;
-    hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(d.BH * d.nseg)), dim3(256), 0, s, d);
+    hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(d.BH * d.nblock)), dim3(256), 0, s, d);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (heads) {
-      hipLaunchKernelGGL(decay_grad_heads_kernel, dim3((unsigned)((a.H + 63) / 64)), dim3(64), 0, s, r.sums, (int)a.B, (int)a.H, d.nseg, a.dlog_decay);
+      hipLaunchKernelGGL(decay_grad_heads_kernel, dim3((unsigned)((a.H + 63) / 64)), dim3(64), 0, s, r.sums, (int)a.B, (int)a.H, d.nblock, a.dlog_decay);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }

@@ -45,10 +45,10 @@ struct DaRole {
   const float *state_in; // (B, H, da, dc), or (B, H, dc, da) if state_in_t; NULL = 0
   int state_in_t;
   float *state_out;      // (B, H, da, dc), NULL = not wanted
-  float *dots;           // (slices * waves, B * H, L) partial sums of out . e, or NULL
-  float *loc, *tot;      // segments: end states from zero, total decays
-  float *edge;           // states at segment boundaries, (B * H, nseg + 1, slices, tile), or NULL;
-                         // forward in time the last one without the last step's own term
+  float *dots;           // (slices, B * H, L) partial sums of out . e, or NULL
+  float *loc, *tot;      // segments: end states from zero (or, combined, the states before them), total decays
+  float *edge;           // states at edges (below), (B * H, edges, slices, tile), or NULL
+  float *edge_dot;       // forward in time: <S, R> at edges, (slices * waves, B * H, edges)
 };
 
 struct DaArgs {
@@ -56,8 +56,14 @@ struct DaArgs {
   const float *g;
   int64_t g_b, g_t;
   int H, BH, nseg, nslice, nroles;
+  int combined;          // loc holds the states before the segments
   int64_t seg_len;       // a multiple of the chunk
-  DaRole role[3];
+  // An edge lies before every step E, 2 E, ..., E = 2^edge_shift; edge i - 1 before
+  // step i * E, the last one (if last_edge) after the last step.  The
+  // backward direction writes its states R there, the forward one dots its own
+  // with them: the decays' gradient starts from them (decay_attn.hip).
+  int edge_shift, nedge, last_edge;
+  DaRole role[2];
 };
 
 // Matrix fragments of 32 along the contracted dimension and 16 along the
@@ -65,6 +71,19 @@ struct DaArgs {
 // 4 (l / 16) + r and 16 + 4 (l / 16) + r, r = 0..3.  This order makes the
 // accumulators of a 16 x 16 product (row 4 (l / 16) + r, column l % 16) usable
 // as the next product's operand without moving data between lanes.
+//
+// In LDS, matrices read only as rows hold the 8 bf16 values of a fragment side
+// by side (32-blocks as [l / 16][half][r], pos()); one that is also read by
+// columns keeps its order.  Rows are padded so that reads meet no bank
+// conflicts; measured clocks per fragment (8 waves of one workgroup) by row
+// stride modulo 256 bytes:
+//                                             +16 bytes   +32
+//   bf16 row, side by side, ds_read_b128          8.0     4.1
+//   bf16 row in order, 2 x ds_read_b64            4.8     8.1   (ds_read2_b64: 16, 32)
+//   bf16 column in order, 2 x ds_read_b64_tr      8.1     4.8
+//   bf16 column, side by side, the same          16.1     8.1
+//   fp32 row, 2 x ds_read_b128                   16.1     8.2
+//   fp32 column, 8 x ds_read_b32                 18.4    32.4
 template <typename T>
 struct Mx;
 
@@ -72,31 +91,44 @@ template <>
 struct Mx<bf16> {
   typedef uint4 Frag;
   static constexpr int kChunk = 64;
-  static constexpr int kPad = 8;  // row padding in elements: rows start 4 banks apart
-  // Rows along the contracted dimension are stored so that the 8 values of a
-  // fragment are adjacent: 32-blocks as [l / 16][half][r].
-  static __device__ __forceinline__ int pos(int k) { return (k & ~31) | ((k & 12) << 1) | ((k & 16) >> 2) | (k & 3); }
+  static constexpr int kPadRow = 16, kPadCol = 16;  // elements, for matrices read by rows alone or by columns too
+  static __device__ __forceinline__ constexpr int pos(int k) { return (k & ~31) | ((k & 12) << 1) | ((k & 16) >> 2) | (k & 3); }
   static __device__ __forceinline__ Frag rowfrag(const bf16 *m, int stride, int row0, int k0) {
     const int l = threadIdx.x & 63;
     return *(const uint4 *)(m + (row0 + (l & 15)) * stride + k0 + (l >> 4) * 8);
   }
-  // transposed: contracted along rows; cols are col0 .. col0 + 15, given as the
-  // storage offset of each group of four (off(j), j = l % 4)
+  // a row whose 16-byte units are permuted by x
+  static __device__ __forceinline__ int swizzled(int k, int x) { return pos(k) ^ (x * 8); }
+  static __device__ __forceinline__ Frag rowfrag_swizzled(const bf16 *row, int k0, int x) {
+    const int l = threadIdx.x & 63;
+    return *(const uint4 *)(row + ((k0 + (l >> 4) * 8) ^ (x * 8)));
+  }
+  // from a matrix in order: two reads, volatile so that they do not become one ds_read2_b64
+  static __device__ __forceinline__ Frag rowfrag_inorder(const bf16 *m, int stride, int row0, int k0) {
+    typedef __attribute__((address_space(3))) const volatile uint64_t lds_u64;
+    const int l = threadIdx.x & 63;
+    lds_u64 *p = (lds_u64 *)(m + (row0 + (l & 15)) * stride + k0 + (l >> 4) * 4);
+    const uint2 x = __builtin_bit_cast(uint2, (uint64_t)p[0]), y = __builtin_bit_cast(uint2, (uint64_t)p[4]);
+    return make_uint4(x.x, x.y, y.x, y.y);
+  }
+  // 16 bytes of a row (elements k .. k + 7), side by side
+  static __device__ __forceinline__ void put_row(bf16 *row, int k, uint4 v) {
+    *(uint2 *)(row + pos(k)) = make_uint2(v.x, v.y);
+    *(uint2 *)(row + pos(k) + 8) = make_uint2(v.z, v.w);
+  }
+  // transposed: contracted along rows, column col0 + l % 16.  The transposing
+  // read gives lane i of 16 column i of a block of 4 rows x 16 columns, of
+  // which it addresses row i / 4, columns 4 (i % 4) ...
   static __device__ __forceinline__ uint2 tr4(const bf16 *p) {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p)));
   }
-  static __device__ __forceinline__ Frag colfrag(const bf16 *m, int stride, int row0, int off) {
+  static __device__ __forceinline__ Frag colfrag(const bf16 *m, int stride, int row0, int col0) {
     const int l = threadIdx.x & 63;
-    const bf16 *p = m + (row0 + (l >> 4) * 4 + ((l >> 2) & 3)) * stride + off;
+    const bf16 *p = m + (row0 + (l >> 4) * 4 + ((l >> 2) & 3)) * stride + col0 + (l & 3) * 4;
     const uint2 x = tr4(p), y = tr4(p + 16 * stride);
     return make_uint4(x.x, x.y, y.x, y.y);
   }
-  static __device__ __forceinline__ int coloff_perm(int ct) {  // columns 16 ct .. of a permuted row
-    const int j = threadIdx.x & 3;
-    return (ct >> 1) * 32 + j * 8 + (ct & 1) * 4;
-  }
-  static __device__ __forceinline__ int coloff(int col0) { return col0 + (threadIdx.x & 3) * 4; }
   static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   }
@@ -132,7 +164,7 @@ struct Mx<bf16> {
 #pragma unroll
     for (int n = 0; n < N; ++n) o[n] = make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
   }
-  // four values along the contracted dimension, in N pieces `plane` elements apart
+  // four adjacent values, in N pieces `plane` elements apart
   template <int N>
   static __device__ __forceinline__ void put4(bf16 *p, int plane, const float (&x)[4]) {
     uint32_t a[N], b[N];
@@ -141,18 +173,21 @@ struct Mx<bf16> {
 #pragma unroll
     for (int n = 0; n < N; ++n) *(uint2 *)(p + n * plane) = make_uint2(a[n], b[n]);
   }
-  // 16 bytes of a row (elements k .. k + 7) into permuted order
-  static __device__ __forceinline__ void put_perm(bf16 *row, int k, uint4 v) {
-    const int o = pos(k);
-    *(uint2 *)(row + o) = make_uint2(v.x, v.y);
-    *(uint2 *)(row + o + 8) = make_uint2(v.z, v.w);
-  }
-  static __device__ __forceinline__ bool nonfinite(uint4 v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool bad = false;
+  static __device__ __forceinline__ void store4(void *p, f32x4 v) { *(uint2 *)p = make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3])); }
+  // zeros in place of NaN and infinities
+  static __device__ __forceinline__ Frag finite(Frag f) {
+    uint32_t w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
-    return bad;
+    for (int i = 0; i < 4; ++i) {
+      if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+      if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // sign bits of the result are set where an exponent is all ones
+  static __device__ __forceinline__ uint32_t nonfinite(uint4 v) {
+    constexpr uint32_t m = 0x7f807f80u, one = 0x00800080u;
+    return (((v.x & m) + one) | ((v.y & m) + one) | ((v.z & m) + one) | ((v.w & m) + one)) & 0x80008000u;
   }
 };
 
@@ -162,23 +197,28 @@ struct Mx<float> {
     f32x4 a, b;
   };
   static constexpr int kChunk = 32;
-  static constexpr int kPad = 4;
-  static __device__ __forceinline__ int pos(int k) { return k; }
+  static constexpr int kPadRow = 8, kPadCol = 4;
+  static __device__ __forceinline__ constexpr int pos(int k) { return k; }
+  static __device__ __forceinline__ void put_row(float *row, int k, uint4 v) { *(uint4 *)(row + k) = v; }
+  static __device__ __forceinline__ Frag rowfrag_inorder(const float *m, int stride, int row0, int k0) { return rowfrag(m, stride, row0, k0); }
+  static __device__ __forceinline__ int swizzled(int k, int x) { return k ^ (x * 4); }
+  static __device__ __forceinline__ Frag rowfrag_swizzled(const float *row, int k0, int x) {
+    const int l = threadIdx.x & 63, k = k0 + (l >> 4) * 4;
+    return Frag{*(const f32x4 *)(row + (k ^ (x * 4))), *(const f32x4 *)(row + ((k + 16) ^ (x * 4)))};
+  }
   static __device__ __forceinline__ Frag rowfrag(const float *m, int stride, int row0, int k0) {
     const int l = threadIdx.x & 63;
     const float *p = m + (row0 + (l & 15)) * stride + k0 + (l >> 4) * 4;
     return Frag{*(const f32x4 *)p, *(const f32x4 *)(p + 16)};
   }
-  static __device__ __forceinline__ Frag colfrag(const float *m, int stride, int row0, int off) {
+  static __device__ __forceinline__ Frag colfrag(const float *m, int stride, int row0, int col0) {
     const int l = threadIdx.x & 63;
-    const float *p = m + (row0 + (l >> 4) * 4) * stride + off;
+    const float *p = m + (row0 + (l >> 4) * 4) * stride + col0 + (l & 15);
     Frag f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) f.a[r] = p[r * stride], f.b[r] = p[(16 + r) * stride];
     return f;
   }
-  static __device__ __forceinline__ int coloff_perm(int ct) { return ct * 16 + (threadIdx.x & 15); }
-  static __device__ __forceinline__ int coloff(int col0) { return col0 + (threadIdx.x & 15); }
   static __device__ __forceinline__ f32x4 mma(const Frag &a, const Frag &b, f32x4 c) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[r], b.a[r], c, 0, 0, 0);
@@ -201,75 +241,141 @@ struct Mx<float> {
     static_assert(N == 1, "fp32 operands are whole");
     *(float4 *)p = make_float4(x[0], x[1], x[2], x[3]);
   }
-  static __device__ __forceinline__ void put_perm(float *row, int k, uint4 v) { *(uint4 *)(row + k) = v; }
-  static __device__ __forceinline__ bool nonfinite(uint4 v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool bad = false;
+  static __device__ __forceinline__ void store4(void *p, f32x4 v) { *(f32x4 *)p = v; }
+  static __device__ __forceinline__ Frag finite(Frag f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7f800000u) == 0x7f800000u;
-    return bad;
+    for (int r = 0; r < 4; ++r) {
+      if ((__float_as_uint(f.a[r]) & 0x7f800000u) == 0x7f800000u) f.a[r] = 0.0f;
+      if ((__float_as_uint(f.b[r]) & 0x7f800000u) == 0x7f800000u) f.b[r] = 0.0f;
+    }
+    return f;
+  }
+  static __device__ __forceinline__ uint32_t nonfinite(uint4 v) {
+    constexpr uint32_t m = 0x7f800000u, one = 0x00800000u;
+    return (((v.x & m) + one) | ((v.y & m) + one) | ((v.z & m) + one) | ((v.w & m) + one)) & 0x80000000u;
   }
 };
 
+// The value, opaque to the compiler: what is computed from it stays where it is
+// written and holds no registers over a loop (a spill there would cost a wait
+// for all loads under way).
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // A (ROWS, COLS) tile on its way from global memory to LDS, 16 bytes at a time.
+// Offsets within a tile are 32-bit, from a base that is the same for all lanes.
 template <typename T, int ROWS, int COLS, int NT>
 struct TileRegs {
   static constexpr int EPP = 16 / (int)sizeof(T), PPR = COLS / EPP, N = (ROWS * PPR + NT - 1) / NT, RSTEP = NT / PPR;
   static_assert(PPR <= NT && NT % PPR == 0, "whole rows per step");
   uint4 r[N];
-  // row0: first row's first element; rows, cols: how many there are (rows >= 1, cols >= 1)
-  __device__ __forceinline__ void load(const T *row0, int64_t st, int rows, int cols) {
-    const int row = threadIdx.x / PPR, col = (threadIdx.x % PPR) * EPP;
-    const T *p = row0 + row * st + col;
+  // row0: the first row; st: bytes from row to row; rows, cols: how many there are (both >= 1)
+  __device__ __forceinline__ void load(const char *row0, uint32_t st, int rows, int cols) {
+    const int tid = here(threadIdx.x), row = tid / PPR, col = (tid % PPR) * EPP;
+    const uint32_t c = col < cols ? col * (uint32_t)sizeof(T) : 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool ok = row + i * RSTEP < rows && col < cols;
-      r[i] = *(const uint4 *)(ok ? p + (int64_t)(i * RSTEP) * st : row0);
-    }
+    for (int i = 0; i < N; ++i) r[i] = *(const uint4 *)(row0 + ((uint32_t)min(row + i * RSTEP, rows - 1) * st + c));
   }
-  // f(row, col, piece) for every piece of the tile, zeros outside rows x cols
-  template <typename F>
-  __device__ __forceinline__ void each(int rows, int cols, F f) const {
-    const int row = threadIdx.x / PPR, col = (threadIdx.x % PPR) * EPP;
+  // Puts the tile into LDS rows `stride` elements apart, zeros outside
+  // rows x cols, in reverse order of rows if rev.  CHECK: first[col] becomes the
+  // first row of a column with a NaN or an infinity, and *any nonzero.
+  // ROWS_ONLY: side by side for row fragments.
+  template <bool ROWS_ONLY, bool CHECK>
+  __device__ __forceinline__ void put(T *lds, int stride, int rows, int cols, bool rev, int *first = nullptr, int *any = nullptr) const {
+    const int tid = here(threadIdx.x), row = tid / PPR, col = (tid % PPR) * EPP;
+    auto one = [&](int lr, uint4 v) {
+      if (ROWS_ONLY)
+        Mx<T>::put_row(lds + lr * stride, col, v);
+      else
+        *(uint4 *)(lds + lr * stride + col) = v;
+      if (CHECK && Mx<T>::nonfinite(v)) {
+        *any = 1;
+        for (int j = 0; j < EPP; ++j)
+          if (!(fabsf(load_io(lds + lr * stride + col, j)) < INFINITY)) atomicMin(first + col + j, lr);
+      }
+    };
+    if (rows == ROWS && cols == COLS && N * NT == ROWS * PPR) {  // the same for all lanes
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int rr = row + i * RSTEP;
-      if (N * NT == ROWS * PPR || rr < ROWS) {
-        const bool ok = rr < rows && col < cols;
-        f(rr, col, ok ? r[i] : make_uint4(0, 0, 0, 0));
+      for (int i = 0; i < N; ++i) one(rev ? ROWS - 1 - row - i * RSTEP : row + i * RSTEP, r[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int rr = row + i * RSTEP;
+        const bool in = rr < rows;
+        if (N * NT == ROWS * PPR || rr < ROWS) one(rev && in ? rows - 1 - rr : rr, in && col < cols ? r[i] : make_uint4(0, 0, 0, 0));
       }
     }
   }
 };
 
+// What a chunk's decays enter as.
+template <int C>
+struct __attribute__((aligned(16))) DaDecays {
+  float gh[C], gl[C];  // G_t as a pair of floats
+  float in[C];         // exp(G_t), of the state in a step's output
+  float out[C];        // exp(G_last - G_s), of a step in the next chunk's state
+  float e[4];          // [0]: exp(G_last)
+};
+
+// Sums over lanes 0 .. lane, by DPP moves within rows of 16 lanes and then
+// from row to row (as wave_affine_scan).
+template <int CTRL, int ROWMASK>
+__device__ __forceinline__ double dpp_add(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWMASK, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWMASK, 0xF, false);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum_scan(double v) {
+  v = dpp_add<0x111, 0xF>(v);
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);
+  return dpp_add<0x143, 0xC>(v);
+}
+
 template <typename T, int DA, int NW, int NC, int NP, bool STATE_ONLY>
-struct DaLds {
-  static constexpr int C = Mx<T>::kChunk, TV = NW * NC * 16;
-  static constexpr int SA = DA + Mx<T>::kPad, SC = TV + Mx<T>::kPad, SP = C + Mx<T>::kPad;
+struct __attribute__((aligned(16))) DaLds {
+  typedef Mx<T> M;
+  static constexpr int C = M::kChunk, TV = NW * NC * 16, ES = sizeof(T);
+  static constexpr int SA = DA + M::kPadRow, SB = DA + M::kPadCol, SC = TV + M::kPadCol;
+  // Products of steps, only blocks of 32 x 32 up to the diagonal: two row tiles of
+  // 32 columns, then two of 64, without padding; instead the 16-byte units of a
+  // row are permuted by its number (swizzle), so that 16 rows meet all banks.
+  static constexpr int PLANE = 32 * 32 + (C > 32 ? 32 * 64 : 0);
+  static __device__ __forceinline__ int pwidth(int tt) { return tt < 2 ? 32 : 64; }
+  static __device__ __forceinline__ int prow(int tt, int r) { return (tt < 2 ? tt * 16 * 32 : 32 * 32 + (tt - 2) * 16 * 64) + r * pwidth(tt); }
+  static __device__ __forceinline__ int swizzle(int tt, int r) { return ES == 2 ? (tt < 2 ? (r >> 2) & 3 : (r >> 1) & 7) : r & 7; }
   T a[STATE_ONLY ? 8 : C * SA];
-  T b[C * SA];
+  T b[C * SB];
   T c[C * SC];
-  T p[STATE_ONLY ? 8 : NP * C * SP];
-  float gh[C], gl[C], in[C], out[C], diag[C];
-  float e;
-  int bad[2];
+  T p[STATE_ONLY ? 8 : NP * PLANE];
+  DaDecays<C> dec[2];  // of this chunk and the next
+  float diag[C];
+  float dots[NW][C];
+  int bad[2];      // whether c has a NaN or an infinity, in this chunk and the next,
+  int first[TV];   // and from which step on, by column (C: nowhere)
 };
 
 // T: storage type; DA: da rounded up; NW waves of NC tiles of 16 columns of dc
 // each; NP, NS: pieces of the products inside a chunk and of the state where
 // they are operands.  STATE_ONLY: the end state of a segment from zero (a
-// split sequence's first pass).
-template <typename T, int DA, int NW, int NC, int NP, int NS, bool STATE_ONLY>
-__global__ void __launch_bounds__(NW * 64) decay_attn_kernel(DaArgs args) {
+// split sequence's first pass).  DOTS: out . e wanted.
+template <typename T, int DA, int NW, int NC, int NP, int NS, bool DOTS, bool STATE_ONLY>
+__global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_attn_kernel(DaArgs args) {
   typedef Mx<T> M;
   typedef typename M::Frag Frag;
   typedef DaLds<T, DA, NW, NC, NP, STATE_ONLY> Lds;
   constexpr int C = M::kChunk, CT = C / 16, DT = DA / 16, NT = NW * 64, TV = Lds::TV;
-  constexpr int SA = Lds::SA, SC = Lds::SC, SP = Lds::SP;
-  constexpr int NB = sizeof(T) == 2 ? 3 : 1;  // pieces of c into the state: all of fp32
-  __shared__ __attribute__((aligned(16))) Lds lds;
+  constexpr int SA = Lds::SA, SB = Lds::SB, SC = Lds::SC, PLANE = Lds::PLANE;
+  constexpr int ES = sizeof(T);
+  constexpr int NB = ES == 2 ? 3 : 1;  // pieces of c into the state: all of fp32
+  __shared__ Lds lds;
 
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l15 = lane & 15, lg = lane >> 4;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l15 = lane & 15, lg = lane >> 4;
   // Workgroups go to the 8 XCDs in turn: give each XCD a contiguous run of
   // items, so that slices and roles that read the same rows share its L2.
   const int nitems = gridDim.x, xcd = blockIdx.x & 7, per = nitems >> 3, rem = nitems & 7;
@@ -286,16 +392,23 @@ __global__ void __launch_bounds__(NW * 64) decay_attn_kernel(DaArgs args) {
   const int64_t b = bh / args.H;
   const int col0 = slice * TV, wcol0 = col0 + w * NC * 16;
   const int64_t t0 = seg * args.seg_len;
-  const int64_t n = min(args.seg_len, args.L - t0);
-  const int64_t tfirst = rev ? t0 + n - 1 : t0;
-  const int64_t dir = rev ? -1 : 1;
+  const int n = (int)min(args.seg_len, args.L - t0);
   const int da = (int)args.da, dc = (int)args.dc;
-
-  const T *pa = (const T *)R.a.p + b * R.a.sb + (h / R.a.share) * R.a.sh + tfirst * R.a.st;
-  const T *pb = (const T *)R.b.p + b * R.b.sb + (h / R.b.share) * R.b.sh + tfirst * R.b.st;
-  const T *pc = (const T *)R.c.p + b * R.c.sb + (h / R.c.share) * R.c.sh + tfirst * R.c.st + col0;
-  const float *pg = args.g + b * args.g_b + h;
   const int ccols = min(TV, dc - col0);
+
+  // Rows t0 + u of the operands; strides in bytes.
+  const char *pa = (const char *)R.a.p + (b * R.a.sb + (h / R.a.share) * R.a.sh + t0 * R.a.st) * ES;
+  const char *pb = (const char *)R.b.p + (b * R.b.sb + (h / R.b.share) * R.b.sh + t0 * R.b.st) * ES;
+  const char *pc = (const char *)R.c.p + (b * R.c.sb + (h / R.c.share) * R.c.sh + t0 * R.c.st + col0) * ES;
+  const char *pe = DOTS ? (const char *)R.e.p + (b * R.e.sb + (h / R.e.share) * R.e.sh + t0 * R.e.st) * ES : nullptr;
+  const uint32_t sta = (uint32_t)R.a.st * ES, stb = (uint32_t)R.b.st * ES, stc = (uint32_t)R.c.st * ES, ste = (uint32_t)R.e.st * ES;
+  const bool out_f32 = R.out_f32 != 0;
+  const int oes = out_f32 ? 4 : ES;
+  const uint32_t sto = (uint32_t)args.H * (uint32_t)dc * oes;
+  char *po = (char *)R.out + (((b * args.L + t0) * args.H + h) * dc) * oes;
+  float *dots = DOTS ? R.dots + ((int64_t)slice * args.BH + bh) * args.L + t0 : nullptr;
+  const float *pg = args.g + b * args.g_b + h;
+  const float iscale = R.iscale, pscale = R.pscale, sscale = R.sscale;
 
   // The state: S[dt][ct][r] is row dt * 16 + lg * 4 + r, column wcol0 + ct * 16 + l15.
   f32x4 S[DT][NC];
@@ -305,113 +418,191 @@ __global__ void __launch_bounds__(NW * 64) decay_attn_kernel(DaArgs args) {
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
     for (int ct = 0; ct < NC; ++ct) S[dt][ct] = f32x4{0, 0, 0, 0};
+  auto edge_tile = [&](int i) { return R.edge + (((int64_t)bh * args.nedge + i) * args.nslice + slice) * kTile + wtile; };
+  auto store_edge = [&](int i) {
+    float *o = edge_tile(i);
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct) *(f32x4 *)(o + (dt * NC + ct) * 256) = S[dt][ct];
+  };
+  auto dot_edge = [&](int i) {
+    const float *o = edge_tile(i);
+    f32x4 d = {0, 0, 0, 0};
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct) {
+        const f32x4 x = *(const f32x4 *)(o + (dt * NC + ct) * 256);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[r] = fmaf(S[dt][ct][r], x[r], d[r]);
+      }
+    float v = (d[0] + d[1]) + (d[2] + d[3]);
+#pragma unroll
+    for (int k = 32; k >= 1; k >>= 1) v += __shfl_xor(v, k, 64);
+    if (lane == 0) R.edge_dot[((int64_t)(slice * NW + w) * args.BH + bh) * args.nedge + i] = v;
+  };
   if constexpr (!STATE_ONLY) {
-    if (R.state_in) {
-      const float *s = R.state_in + (int64_t)bh * da * dc;
+    if (args.combined) {
+      const float *loc = R.loc + (((int64_t)bh * args.nseg + seg) * args.nslice + slice) * kTile + wtile;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-        for (int ct = 0; ct < NC; ++ct)
+        for (int ct = 0; ct < NC; ++ct) S[dt][ct] = *(const f32x4 *)(loc + (dt * NC + ct) * 256);
+    } else {
+      if (R.state_in) {
+        const float *s = R.state_in + (int64_t)bh * da * dc;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = dt * 16 + lg * 4 + r, col = wcol0 + ct * 16 + l15;
-            if (row < da && col < dc) S[dt][ct][r] = s[R.state_in_t ? (int64_t)col * da + row : (int64_t)row * dc + col];
-          }
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int row = dt * 16 + lg * 4 + r, col = wcol0 + ct * 16 + l15;
+              if (row < da && col < dc) S[dt][ct][r] = s[R.state_in_t ? col * da + row : row * dc + col];
+            }
+      }
+      // the segments before this one, in the order of the recurrence
+      const int before = rev ? args.nseg - 1 - seg : seg;
+      for (int i = 0; i < before; ++i) {
+        const int64_t j = (int64_t)bh * args.nseg + (rev ? args.nseg - 1 - i : i);
+        const float e = R.tot[j];
+        const float *loc = R.loc + (j * args.nslice + slice) * kTile + wtile;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int ct = 0; ct < NC; ++ct) S[dt][ct] = S[dt][ct] * e + *(const f32x4 *)(loc + (dt * NC + ct) * 256);
+      }
     }
-    // the segments before this one, in the order of the recurrence
-    const int before = rev ? args.nseg - 1 - seg : seg;
-    for (int i = 0; i < before; ++i) {
-      const int64_t j = (int64_t)bh * args.nseg + (rev ? args.nseg - 1 - i : i);
-      const float e = R.tot[j];
-      const float *loc = R.loc + (j * args.nslice + slice) * kTile + wtile;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int ct = 0; ct < NC; ++ct) S[dt][ct] = S[dt][ct] * e + *(const f32x4 *)(loc + (dt * NC + ct) * 256);
-    }
-    // boundary j lies between segments j - 1 and j
-    if (R.edge && (rev || seg > 0)) {
-      float *o = R.edge + (((int64_t)bh * (args.nseg + 1) + (rev ? seg + 1 : seg)) * args.nslice + slice) * kTile + wtile;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int ct = 0; ct < NC; ++ct) *(f32x4 *)(o + (dt * NC + ct) * 256) = S[dt][ct];
-    }
+    if (DOTS && rev && args.last_edge && seg == args.nseg - 1) store_edge(args.nedge - 1);
     // products of steps later in a chunk are never written: they stay zero
-    for (int i = threadIdx.x; i < NP * C * SP * (int)sizeof(T) / 16; i += NT) ((uint4 *)lds.p)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < NP * PLANE * ES / 16; i += NT) ((uint4 *)lds.p)[i] = make_uint4(0, 0, 0, 0);
   }
   if (threadIdx.x < 2) lds.bad[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < TV; i += NT) lds.first[i] = C;
+  // (the first chunk's barrier comes after its own tile is put, so:)
+  __syncthreads();
 
+  // Chunk i of the recurrence holds rows low .. low + rows - 1 of the segment,
+  // in reverse order backward in time.
   TileRegs<T, C, DA, NT> ra, rb;
   TileRegs<T, C, TV, NT> rc;
+  const int nchunk = (n + C - 1) / C;
+  auto low_of = [&](int i) { return (rev ? nchunk - 1 - i : i) * C; };
+  auto fetch = [&](int i) {
+    const int low = low_of(i), rows = min(C, n - low);
+    if constexpr (!STATE_ONLY) ra.load(pa + (int64_t)low * sta, sta, rows, da);
+    rb.load(pb + (int64_t)low * stb, stb, rows, da);
+    rc.load(pc + (int64_t)low * stc, stc, rows, ccols);
+  };
+  // The last wave, which has the fewest products inside a chunk, prepares the
+  // next chunk's decays beside them and loads those of the one after.
   float rg = 0.0f;
-  auto fetch = [&](int64_t u0) {
-    const int rows = (int)min((int64_t)C, n - u0);
-    if constexpr (!STATE_ONLY) ra.load(pa + dir * u0 * R.a.st, dir * R.a.st, rows, da);
-    rb.load(pb + dir * u0 * R.b.st, dir * R.b.st, rows, da);
-    rc.load(pc + dir * u0 * R.c.st, dir * R.c.st, rows, ccols);
+  bool have_g = false;
+  auto fetch_decays = [&](int i) {
     // backward in time the decay into a step is the later step's
-    const int64_t t = tfirst + dir * (u0 + lane) + (rev ? 1 : 0);
-    rg = lane < rows && t < args.L ? decay_log2(pg[t * args.g_t]) : 0.0f;
+    const int low = low_of(i), rows = min(C, n - low);
+    const int64_t t = t0 + low + (rev ? rows - lane : lane);
+    have_g = i < nchunk && lane < rows && t < args.L;
+    rg = pg[have_g ? t * args.g_t : 0];
+  };
+  auto put_decays = [&](int i, DaDecays<C> &d) {
+    const double G = wave_sum_scan(have_g ? decay_log2(rg) : 0.0f);
+    const uint64_t gb = __builtin_bit_cast(uint64_t, G);
+    const double last = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(gb >> 32), 63) << 32 |
+                                                       (uint32_t)__builtin_amdgcn_readlane((int)gb, 63));
+    const float hi = (float)G;
+    // the last edge's state leaves out the last step (see no_dot)
+    const bool left_out = DOTS && args.last_edge && !rev && t0 + low_of(i) + lane == args.L - 1;
+    if (lane < C) {
+      d.gh[lane] = hi;
+      d.gl[lane] = (float)(G - (double)hi);
+      d.in[lane] = fast_exp2(hi) * iscale;
+      d.out[lane] = left_out ? 0.0f : fast_exp2((float)(last - G)) * sscale;
+    }
+    if (lane == 0) d.e[0] = fast_exp2((float)last);
+  };
+  // a chunk's dot products, of all waves
+  auto flush_dots = [&](int ci) {
+    const int i = threadIdx.x, low = low_of(ci), rows = min(C, n - low);
+    if (i < rows) {
+      float d = lds.dots[0][i];
+#pragma unroll
+      for (int k = 1; k < NW; ++k) d += lds.dots[k][i];
+      dots[low + (rev ? rows - 1 - i : i)] = d;
+    }
   };
   fetch(0);
+  if (w == NW - 1) {
+    fetch_decays(0);
+    put_decays(0, lds.dec[0]);
+    fetch_decays(1);
+  }
   float total = 1.0f;
+  int par = 0;
 
-  for (int64_t u0 = 0; u0 < n; u0 += C) {
-    const int rows = (int)min((int64_t)C, n - u0);
-    const int par = (int)(u0 / C) & 1;
+  for (int ci = 0; ci < nchunk; ++ci, par ^= 1) {
+    const int low = low_of(ci), rows = min(C, n - low);
+    // the edge before this chunk's rows, -1 if there is none
+    const int edge = DOTS && ((t0 + low) & ((1 << args.edge_shift) - 1)) == 0 ? (int)((t0 + low) >> args.edge_shift) - 1 : -1;
+    if (DOTS && !rev && edge >= 0) dot_edge(edge);
+    // byte offsets of this lane's row and columns in outputs, from those of row `low`
+    const uint32_t loff = (uint32_t)(rev ? rows - 1 - l15 : l15) * sto + (wcol0 + lg * 4) * oes;
     __syncthreads();  // the last chunk's readers are done
-    if constexpr (!STATE_ONLY)
-      ra.each(rows, da, [&](int r, int k, uint4 v) { M::put_perm(lds.a + r * SA, k, v); });
-    rb.each(rows, da, [&](int r, int k, uint4 v) { M::put_perm(lds.b + r * SA, k, v); });
-    rc.each(rows, ccols, [&](int r, int k, uint4 v) {
-      *(uint4 *)(lds.c + r * SC + k) = v;
-      if (!STATE_ONLY && M::nonfinite(v)) lds.bad[par] = 1;
-    });
-    if (w == 0) {
-      double G = rg;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(G, d, 64);
-        if (lane >= d) G += o;
-      }
-      const double last = __shfl(G, 63, 64);
-      const float hi = (float)G;
-      // the last boundary's state leaves out the last step (see no_dot)
-      const bool left_out = !STATE_ONLY && R.edge && !rev && t0 + u0 + lane == args.L - 1;
-      if (lane < C) {
-        lds.gh[lane] = hi;
-        lds.gl[lane] = (float)(G - (double)hi);
-        lds.in[lane] = fast_exp2(hi) * R.iscale;
-        lds.out[lane] = left_out ? 0.0f : fast_exp2((float)(last - G)) * R.sscale;
-      }
-      if (lane == 0) lds.e = fast_exp2((float)last);
-    }
-    if (u0 + C < n) fetch(u0 + C);
+    if constexpr (!STATE_ONLY) ra.template put<true, false>(lds.a, SA, rows, da, rev);
+    rb.template put<false, false>(lds.b, SB, rows, da, rev);
+    rc.template put<false, !STATE_ONLY>(lds.c, SC, rows, ccols, rev, lds.first, lds.bad + par);
+    if (DOTS && ci > 0) flush_dots(ci - 1);
     __syncthreads();
-    const float e = lds.e;
+    const DaDecays<C> &dec = lds.dec[par];
+    const float e = dec.e[0];
     total *= e;
+    if (w == NW - 1 && ci + 1 < nchunk) {
+      put_decays(ci + 1, lds.dec[par ^ 1]);
+      fetch_decays(ci + 2);
+    }
 
     f32x4 acc[CT][NC];
     if constexpr (!STATE_ONLY) {
       // products a_t . b_s of steps s <= t with their decays, 16 x 16 tiles over the waves
-      for (int idx = w; idx < CT * (CT + 1) / 2; idx += NW) {
-        const int tt = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, st = idx - tt * (tt + 1) / 2;
-        f32x4 x = {0, 0, 0, 0};
+      constexpr int NTILE = CT * (CT + 1) / 2;
 #pragma unroll
-        for (int kk = 0; kk < DA / 32; ++kk)
-          x = M::mma(M::rowfrag(lds.b, SA, st * 16, kk * 32), M::rowfrag(lds.a, SA, tt * 16, kk * 32), x);
+      for (int j = 0; j < (NTILE + NW - 1) / NW; ++j) {
+        // (opaque, so that addresses are formed here and hold no registers over the loop)
+        int idx = w + j * NW;
+        asm volatile("" : "+s"(idx));
+        if (idx >= NTILE) break;
+        const int tt = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, st = idx - tt * (tt + 1) / 2;
+        // all reads first, then two chains of products
+        constexpr int KB = DA / 32 < 2 ? DA / 32 : 2;
+        f32x4 x = {0, 0, 0, 0}, x2 = {0, 0, 0, 0};
+#pragma unroll
+        for (int k0 = 0; k0 < DA / 32; k0 += KB) {
+          Frag fa[KB], fb[KB];
+#pragma unroll
+          for (int k = 0; k < KB; ++k) {
+            fb[k] = M::rowfrag_inorder(lds.b, SB, st * 16, (k0 + k) * 32);
+            fa[k] = M::rowfrag(lds.a, SA, tt * 16, (k0 + k) * 32);
+          }
+#pragma unroll
+          for (int k = 0; k < KB; ++k) {
+            f32x4 &y = k & 1 ? x2 : x;
+            y = M::mma(fb[k], fa[k], y);
+          }
+        }
+        x += x2;
         const int t = tt * 16 + l15, s = st * 16 + lg * 4;
-        const float th = lds.gh[t], tl = lds.gl[t];
+        const float th = dec.gh[t], tl = dec.gl[t];
+        const f32x4 sh = *(const f32x4 *)(dec.gh + s), sl = *(const f32x4 *)(dec.gl + s);
         float p[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float d = fast_exp2((th - lds.gh[s + r]) + (tl - lds.gl[s + r]));
+          const float d = fast_exp2((th - sh[r]) + (tl - sl[r]));
           // for the dot products a step's own term is kept apart (below)
-          p[r] = s + r < t + (R.dots ? 0 : 1) ? x[r] * (d * R.pscale) : 0.0f;
-          if (s + r == t) lds.diag[t] = x[r] * R.pscale;
+          p[r] = s + r < t + (DOTS ? 0 : 1) ? x[r] * (d * pscale) : 0.0f;
+          if (DOTS && s + r == t) lds.diag[t] = x[r] * pscale;
         }
-        M::template put4<NP>(lds.p + t * SP + M::pos(s), C * SP, p);
+        M::template put4<NP>(lds.p + Lds::prow(tt, l15) + M::swizzled(s, Lds::swizzle(tt, l15)), PLANE, p);
       }
       // what the state gives
 #pragma unroll
@@ -428,96 +619,123 @@ __global__ void __launch_bounds__(NW * 64) decay_attn_kernel(DaArgs args) {
           for (int r = 0; r < 4; ++r) x[r] = S[2 * kk][ct][r], x[4 + r] = S[2 * kk + 1][ct][r];
           M::template split<NS>(x, sf[ct]);
         }
+        Frag af[CT];
 #pragma unroll
-        for (int tt = 0; tt < CT; ++tt) {
-          const Frag af = M::rowfrag(lds.a, SA, tt * 16, kk * 32);
+        for (int tt = 0; tt < CT; ++tt) af[tt] = M::rowfrag(lds.a, SA, tt * 16, kk * 32);
+        // (neighbouring products are independent)
 #pragma unroll
-          for (int ct = 0; ct < NC; ++ct)
+        for (int i = NS - 1; i >= 0; --i)
 #pragma unroll
-            for (int i = NS - 1; i >= 0; --i) acc[tt][ct] = M::mma(sf[ct][i], af, acc[tt][ct]);
-        }
+          for (int tt = 0; tt < CT; ++tt)
+#pragma unroll
+            for (int ct = 0; ct < NC; ++ct) acc[tt][ct] = M::mma(sf[ct][i], af[tt], acc[tt][ct]);
       }
 #pragma unroll
       for (int tt = 0; tt < CT; ++tt) {
-        const float f = lds.in[tt * 16 + l15];
+        const float f = dec.in[tt * 16 + l15];
 #pragma unroll
         for (int ct = 0; ct < NC; ++ct) acc[tt][ct] *= f;
       }
     }
+    // The next chunk's rows travel during the rest of this one (and hold no
+    // registers before).
+    typename Vec4<T>::raw ev[DOTS ? CT : 1][NC];
+    if constexpr (DOTS) {
+#pragma unroll
+      for (int tt = 0; tt < CT; ++tt)
+#pragma unroll
+        for (int ct = 0; ct < NC; ++ct) {
+          const int col = min(wcol0 + ct * 16 + lg * 4, dc - 4);
+          const int row = min(tt * 16 + l15, rows - 1);
+          ev[tt][ct] = Vec4<T>::load_b(pe + (int64_t)low * ste, (uint32_t)(rev ? rows - 1 - row : row) * ste + col * ES);
+        }
+    }
+    if (ci + 1 < nchunk) fetch(ci + 1);
+    if constexpr (!STATE_ONLY) __syncthreads();  // all products are there
     Frag cf[C / 32][NC];
 #pragma unroll
     for (int kk = 0; kk < C / 32; ++kk)
 #pragma unroll
-      for (int ct = 0; ct < NC; ++ct) cf[kk][ct] = M::colfrag(lds.c, SC, kk * 32, M::coloff((w * NC + ct) * 16));
+      for (int ct = 0; ct < NC; ++ct) cf[kk][ct] = M::colfrag(lds.c, SC, kk * 32, (w * NC + ct) * 16);
     if constexpr (!STATE_ONLY) {
-      __syncthreads();  // all products are there
       if (threadIdx.x == 0) lds.bad[par ^ 1] = 0;
-      if (!lds.bad[par]) {
+      // A NaN or an infinity in c must not meet the zeros of earlier steps in
+      // the products: it is left out of them and poisons what comes after.
+      const int bad = __builtin_amdgcn_readfirstlane(lds.bad[par]);
+      if (bad) {
 #pragma unroll
-        for (int tt = 0; tt < CT; ++tt)
+        for (int kk = 0; kk < C / 32; ++kk)
 #pragma unroll
-          for (int kk = 0; kk <= tt / 2; ++kk)
+          for (int ct = 0; ct < NC; ++ct) cf[kk][ct] = M::finite(cf[kk][ct]);
+      }
 #pragma unroll
-            for (int i = NP - 1; i >= 0; --i) {
-              const Frag pf = M::rowfrag(lds.p + i * C * SP, SP, tt * 16, kk * 32);
+      for (int kk = 0; kk < C / 32; ++kk)
 #pragma unroll
-              for (int ct = 0; ct < NC; ++ct) acc[tt][ct] = M::mma(cf[kk][ct], pf, acc[tt][ct]);
-            }
-      } else {
-        // A NaN or infinity in c must not meet the zeros of later steps: sum over s <= t alone.
+        for (int i = NP - 1; i >= 0; --i) {
+          Frag pf[CT];
 #pragma unroll
-        for (int tt = 0; tt < CT; ++tt)
+          for (int tt = 2 * kk; tt < CT; ++tt) pf[tt] = M::rowfrag_swizzled(lds.p + i * PLANE + Lds::prow(tt, l15), kk * 32, Lds::swizzle(tt, l15));
 #pragma unroll
-          for (int ct = 0; ct < NC; ++ct) {
-            const int t = tt * 16 + l15;
-            for (int s = 0; s <= t; ++s) {
-              float p = 0.0f;
+          for (int tt = 2 * kk; tt < CT; ++tt)
 #pragma unroll
-              for (int i = NP - 1; i >= 0; --i) p += load_io(lds.p + i * C * SP + t * SP, M::pos(s));
+            for (int ct = 0; ct < NC; ++ct) acc[tt][ct] = M::mma(cf[kk][ct], pf[tt], acc[tt][ct]);
+        }
+      if (bad) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                acc[tt][ct][r] = fmaf(p, load_io(lds.c + s * SC, (w * NC + ct) * 16 + lg * 4 + r), acc[tt][ct][r]);
-            }
+        for (int ct = 0; ct < NC; ++ct) {
+          int *first = lds.first + (w * NC + ct) * 16;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int f = first[lg * 4 + r];
+#pragma unroll
+            for (int tt = 0; tt < CT; ++tt)
+              if (tt * 16 + l15 >= f) acc[tt][ct][r] = NAN;
           }
+          if (first[l15] < C) {
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) S[dt][ct] = f32x4{NAN, NAN, NAN, NAN};
+          }
+          first[l15] = C;  // for the next chunk; these columns are this wave's alone
+        }
       }
       // out^T: column wcol0 + ct * 16 + lg * 4 + r of step tt * 16 + l15
 #pragma unroll
       for (int tt = 0; tt < CT; ++tt) {
         const int i = tt * 16 + l15;
-        const int64_t t = tfirst + dir * (u0 + i);
-        float dot = 0.0f;
-        if (i < rows) {
-          const int64_t o = ((b * args.L + t) * args.H + h) * dc;
-          const T *pe = (const T *)R.e.p + b * R.e.sb + (h / R.e.share) * R.e.sh + t * R.e.st;
+        if constexpr (DOTS) {
           // The dot products leave out a step's term with itself, and the last
           // step's with dstate_final: no decay lies between, so they cancel in
           // the decays' gradient, and where decays are strong they would leave
           // their rounding in place of much smaller sums.
+          const bool no_dot = rev && t0 + n == args.L && ci == 0 && i == 0;
           const float own = lds.diag[i];
-          const bool no_dot = rev && t == args.L - 1;
+          float dot = 0.0f;
 #pragma unroll
           for (int ct = 0; ct < NC; ++ct) {
             const int col = wcol0 + ct * 16 + lg * 4;
-            if (col < dc) {
-              float4 v = make_float4(acc[tt][ct][0], acc[tt][ct][1], acc[tt][ct][2], acc[tt][ct][3]);
-              if (R.dots) {
-                const float4 x = Vec4<T>::cvt(Vec4<T>::load(pe, col));
-                if (!no_dot) dot += v.x * x.x + v.y * x.y + v.z * x.z + v.w * x.w;
-                const T *c = lds.c + i * SC + (w * NC + ct) * 16 + lg * 4;
-                v.x = fmaf(own, load_io(c, 0), v.x), v.y = fmaf(own, load_io(c, 1), v.y);
-                v.z = fmaf(own, load_io(c, 2), v.z), v.w = fmaf(own, load_io(c, 3), v.w);
-              }
-              if (R.out_f32)
-                *(float4 *)((float *)R.out + o + col) = v;
-              else
-                Vec4<T>::store((T *)R.out, o + col, v);
+            const float4 c = Vec4<T>::cvt(Vec4<T>::load(lds.c + i * SC, (w * NC + ct) * 16 + lg * 4));
+            const float4 x = Vec4<T>::cvt(ev[tt][ct]);
+            const f32x4 cv = {c.x, c.y, c.z, c.w}, xv = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if (col < dc) dot = fmaf(acc[tt][ct][r], xv[r], dot);
+              acc[tt][ct][r] = fmaf(own, cv[r], acc[tt][ct][r]);
             }
           }
-        }
-        if (R.dots) {
           dot += __shfl_xor(dot, 16, 64);
           dot += __shfl_xor(dot, 32, 64);
-          if (lg == 0 && i < rows) R.dots[((int64_t)(slice * NW + w) * args.BH + bh) * args.L + t] = dot;
+          if (lg == 0) lds.dots[w][i] = no_dot ? 0.0f : dot;
+        }
+        if (i < rows && wcol0 + lg * 4 < dc) {
+          char *p = po + (int64_t)(low + (rev ? -tt * 16 : tt * 16)) * sto + loff;
+#pragma unroll
+          for (int ct = 0; ct < NC; ++ct) {
+            if (NC > 1 && wcol0 + ct * 16 + lg * 4 >= dc) break;
+            if (out_f32)
+              *(f32x4 *)(p + ct * 64) = acc[tt][ct];
+            else
+              M::store4(p + ct * 16 * ES, acc[tt][ct]);
+          }
         }
       }
     }
@@ -529,26 +747,34 @@ __global__ void __launch_bounds__(NW * 64) decay_attn_kernel(DaArgs args) {
 #pragma unroll
     for (int kk = 0; kk < C / 32; ++kk) {
       Frag xf[NC][NB];
+      const f32x4 y0 = *(const f32x4 *)(dec.out + kk * 32 + lg * 4), y1 = *(const f32x4 *)(dec.out + kk * 32 + 16 + lg * 4);
 #pragma unroll
       for (int ct = 0; ct < NC; ++ct) {
         float x[8];
         M::floats(cf[kk][ct], x);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[r] *= lds.out[kk * 32 + lg * 4 + r];
-          x[4 + r] *= lds.out[kk * 32 + 16 + lg * 4 + r];
-        }
+        for (int r = 0; r < 4; ++r) x[r] *= y0[r], x[4 + r] *= y1[r];
         M::template split<NB>(x, xf[ct]);
       }
+      constexpr int G = DT < 4 ? DT : 4;  // independent products side by side
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        const Frag bf = M::colfrag(lds.b, SA, kk * 32, M::coloff_perm(dt));
+      for (int d0 = 0; d0 < DT; d0 += G) {
+        Frag bf[G];
 #pragma unroll
-        for (int ct = 0; ct < NC; ++ct)
+        for (int d = 0; d < G; ++d) bf[d] = M::colfrag(lds.b, SB, kk * 32, (d0 + d) * 16);
 #pragma unroll
-          for (int i = NB - 1; i >= 0; --i) S[dt][ct] = M::mma(bf, xf[ct][i], S[dt][ct]);
+        for (int i = NB - 1; i >= 0; --i)
+#pragma unroll
+          for (int d = 0; d < G; ++d)
+#pragma unroll
+            for (int ct = 0; ct < NC; ++ct) S[d0 + d][ct] = M::mma(bf[d], xf[ct][i], S[d0 + d][ct]);
       }
     }
+    if (DOTS && rev && edge >= 0) store_edge(edge);
+  }
+  if constexpr (DOTS) {
+    __syncthreads();
+    flush_dots(nchunk - 1);
   }
 
   if constexpr (STATE_ONLY) {
@@ -560,13 +786,7 @@ __global__ void __launch_bounds__(NW * 64) decay_attn_kernel(DaArgs args) {
       for (int ct = 0; ct < NC; ++ct) *(f32x4 *)(loc + (dt * NC + ct) * 256) = S[dt][ct];
     if (threadIdx.x == 0 && slice == 0) R.tot[j] = total;
   } else if (seg == (rev ? 0 : args.nseg - 1)) {
-    if (R.edge && !rev) {
-      float *o = R.edge + (((int64_t)bh * (args.nseg + 1) + args.nseg) * args.nslice + slice) * kTile + wtile;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int ct = 0; ct < NC; ++ct) *(f32x4 *)(o + (dt * NC + ct) * 256) = S[dt][ct];
-    }
+    if (DOTS && !rev && args.last_edge) dot_edge(args.nedge - 1);
     if (R.state_out) {
       const float e = rev ? fast_exp2(decay_log2(pg[0])) : 1.0f;  // the first step's own decay
       float *s = R.state_out + (int64_t)bh * da * dc;
@@ -577,49 +797,52 @@ __global__ void __launch_bounds__(NW * 64) decay_attn_kernel(DaArgs args) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int row = dt * 16 + lg * 4 + r, col = wcol0 + ct * 16 + l15;
-            if (row < da && col < dc) s[(int64_t)row * dc + col] = S[dt][ct][r] * e;
+            if (row < da && col < dc) s[row * dc + col] = S[dt][ct][r] * e;
           }
     }
   }
 }
 
 // Launches the kernel for one set of roles (decay_attn_f32.hip, decay_attn_bf16.hip).
-// precise: outputs to fp32 (their dot products make the decays' gradient) and
-// not only to the storage type.
-hipError_t launch_decay_attn_f32(const DaArgs &a, int da_padded, bool precise, bool state_only, hipStream_t s);
-hipError_t launch_decay_attn_bf16(const DaArgs &a, int da_padded, bool precise, bool state_only, hipStream_t s);
+// dots: the outputs' dot products with e, and outputs to fp32 for them.
+hipError_t launch_decay_attn_f32(const DaArgs &a, int da_padded, bool dots, bool state_only, hipStream_t s);
+hipError_t launch_decay_attn_bf16(const DaArgs &a, int da_padded, bool dots, bool state_only, hipStream_t s);
 
-constexpr int kDaWaves = 4, kDaTiles = 1;
-constexpr int kDaCols = kDaWaves * kDaTiles * 16;  // columns of dc per workgroup
+// Waves per workgroup, of 16 columns of dc each.
+inline int da_waves(int64_t dc) { return dc > 64 ? 8 : 4; }
 
-template <typename T, int DA, int NP, int NS, bool STATE_ONLY>
+template <typename T, int DA, int NW, int NP, int NS, bool DOTS, bool STATE_ONLY>
 hipError_t launch_da(const DaArgs &a, hipStream_t s) {
   const int64_t items = (int64_t)a.nslice * a.nroles * (STATE_ONLY ? a.nseg - 1 : a.nseg) * a.BH;
   if (items > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((decay_attn_kernel<T, DA, kDaWaves, kDaTiles, NP, NS, STATE_ONLY>), dim3((unsigned)items),
-                     dim3(kDaWaves * 64), 0, s, a);
+  hipLaunchKernelGGL((decay_attn_kernel<T, DA, NW, 1, NP, NS, DOTS, STATE_ONLY>), dim3((unsigned)items), dim3(NW * 64), 0, s, a);
   return hipGetLastError();
 }
 
-template <typename T, int DA>
-hipError_t launch_da_mode(const DaArgs &a, bool precise, bool state_only, hipStream_t s) {
-  if (state_only) return launch_da<T, DA, 1, 1, true>(a, s);
+template <typename T, int DA, int NW>
+hipError_t launch_da_mode(const DaArgs &a, bool dots, bool state_only, hipStream_t s) {
+  if (state_only) return launch_da<T, DA, NW, 1, 1, false, true>(a, s);
   if constexpr (sizeof(T) == 2) {
     // One piece of the in-chunk products would leave the output an error of
     // 1.4 roundings instead of one; two pieces of both operands leave one.
-    return precise ? launch_da<T, DA, 3, 3, false>(a, s) : launch_da<T, DA, 2, 2, false>(a, s);
+    return dots ? launch_da<T, DA, NW, 3, 3, true, false>(a, s) : launch_da<T, DA, NW, 2, 2, false, false>(a, s);
   } else {
-    return launch_da<T, DA, 1, 1, false>(a, s);
+    return dots ? launch_da<T, DA, NW, 1, 1, true, false>(a, s) : launch_da<T, DA, NW, 1, 1, false, false>(a, s);
   }
 }
 
+template <typename T, int DA>
+hipError_t launch_da_waves(const DaArgs &a, bool dots, bool state_only, hipStream_t s) {
+  return da_waves(a.dc) == 8 ? launch_da_mode<T, DA, 8>(a, dots, state_only, s) : launch_da_mode<T, DA, 4>(a, dots, state_only, s);
+}
+
 template <typename T>
-hipError_t launch_da_type(const DaArgs &a, int da_padded, bool precise, bool state_only, hipStream_t s) {
+hipError_t launch_da_type(const DaArgs &a, int da_padded, bool dots, bool state_only, hipStream_t s) {
   switch (da_padded) {
-    case 32: return launch_da_mode<T, 32>(a, precise, state_only, s);
-    case 64: return launch_da_mode<T, 64>(a, precise, state_only, s);
-    case 128: return launch_da_mode<T, 128>(a, precise, state_only, s);
-    case 256: return launch_da_mode<T, 256>(a, precise, state_only, s);
+    case 32: return launch_da_waves<T, 32>(a, dots, state_only, s);
+    case 64: return launch_da_waves<T, 64>(a, dots, state_only, s);
+    case 128: return launch_da_waves<T, 128>(a, dots, state_only, s);
+    case 256: return launch_da_waves<T, 256>(a, dots, state_only, s);
   }
   return hipErrorInvalidValue;
 }

@@ -2,7 +2,7 @@
 #include "decay_attn.hpp"
 
 namespace ssm {
-hipError_t launch_decay_attn_f32(const DaArgs &a, int da_padded, bool precise, bool state_only, hipStream_t s) {
-  return launch_da_type<float>(a, da_padded, precise, state_only, s);
+hipError_t launch_decay_attn_f32(const DaArgs &a, int da_padded, bool dots, bool state_only, hipStream_t s) {
+  return launch_da_type<float>(a, da_padded, dots, state_only, s);
 }
 }  // namespace ssm
