@@ -21,22 +21,44 @@ def _view(name, t, shape, dtype, dev):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] != 1:
+    ptr = t.data_ptr()
+    if t.is_contiguous() and not (shape[-1] % 8 or ptr % 16):
+        st = shape[-1] * shape[-2]
+        return _lib.View4(ptr, st * shape[1] if len(shape) == 4 else st, st, shape[-1])
+    if len(shape) == 4:
+        sb, st, sh, se = t.stride()
+    else:
+        sb, sh, se = t.stride()
+        st = 0
+    if se != 1 and shape[-1] != 1:
         raise ValueError(f"{name} must have adjacent elements in its last dimension "
-                         f"(strides {st})")
-    st = [s if n > 1 else 0 for s, n in zip(st, shape)]
-    unit = 4 if dtype is _F32 else 8
-    if any(s % unit for s in st[:-1]) or t.data_ptr() % 16:
+                         f"(strides {t.stride()})")
+    # strides of dimensions of size 1 are not used
+    sb, sh = sb if shape[0] > 1 else 0, sh if shape[-2] > 1 else 0
+    if len(shape) == 4 and shape[1] == 1:
+        st = 0
+    if (sb | st | sh) % (4 if dtype is _F32 else 8) or ptr % 16:
         raise ValueError(f"{name} must keep 16-byte alignment from head to head (strides "
-                         f"{t.stride()}, address {t.data_ptr():#x}); make it contiguous")
-    if len(st) == 3:
-        return _lib.View4(t.data_ptr(), st[0], 0, st[1])
-    return _lib.View4(t.data_ptr(), st[0], st[1], st[2])
+                         f"{t.stride()}, address {ptr:#x}); make it contiguous")
+    return _lib.View4(ptr, sb, st, sh)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(fn, dev, *args):
+    """fn(*args, current stream) with dev as the current device."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream(dev) if _raw_stream is None else _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
+    if st:
+        _lib.check(st)
 
 
 def _gpu(name, t):
@@ -92,14 +114,11 @@ def decay_attn_fwd(q, k, v, log_decay, scale=None, state0=None, return_final_sta
     lib = _lib.load()
     nbytes = lib.ssm_decay_attn_fwd_workspace_bytes(B, L, H, G, dk, dv, io)
     ws = _workspace(nbytes, dev)
-    o = torch.empty((B, L, H, dv), dtype=dt, device=dev)
+    o = torch.empty_like(v, memory_format=torch.contiguous_format)
     final = torch.empty((B, H, dk, dv), dtype=_F32, device=dev) if return_final_state else None
-    with torch.cuda.device(dev):
-        st = lib.ssm_decay_attn_fwd(B, L, H, G, dk, dv, io, qv, kv, vv, log_decay.data_ptr(),
-                                    per_token, dk ** -0.5 if scale is None else scale,
-                                    _ptr(state0), _ptr(final), o.data_ptr(), _ptr(ws), nbytes,
-                                    _stream(dev))
-    _lib.check(st)
+    _call(lib.ssm_decay_attn_fwd, dev, B, L, H, G, dk, dv, io, qv, kv, vv, log_decay.data_ptr(),
+          per_token, dk ** -0.5 if scale is None else scale,
+          _ptr(state0), _ptr(final), o.data_ptr(), _ptr(ws), nbytes)
     return o, final
 
 
@@ -123,13 +142,11 @@ def decay_attn_bwd(q, k, v, log_decay, do, scale=None, state0=None, dstate_final
              dv=torch.empty((B, L, H, dv), dtype=dt, device=dev),
              dlog_decay=torch.empty_like(log_decay) if want_dlog_decay else None,
              dstate0=torch.empty((B, H, dk, dv), dtype=_F32, device=dev) if want_dstate0 else None)
-    with torch.cuda.device(dev):
-        st = lib.ssm_decay_attn_bwd(B, L, H, G, dk, dv, io, qv, kv, vv, log_decay.data_ptr(),
-                                    per_token, dk ** -0.5 if scale is None else scale,
-                                    _ptr(state0), ov, _ptr(dstate_final), _ptr(g["dq"]),
-                                    _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dlog_decay"]),
-                                    _ptr(g["dstate0"]), _ptr(ws), nbytes, _stream(dev))
-    _lib.check(st)
+    _call(lib.ssm_decay_attn_bwd, dev, B, L, H, G, dk, dv, io, qv, kv, vv, log_decay.data_ptr(),
+          per_token, dk ** -0.5 if scale is None else scale,
+          _ptr(state0), ov, _ptr(dstate_final), _ptr(g["dq"]),
+          _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dlog_decay"]),
+          _ptr(g["dstate0"]), _ptr(ws), nbytes)
     return g
 
 
@@ -144,13 +161,11 @@ def decay_attn_update(state, q, k, v, log_decay, scale=None):
     qv, kv = _view("q", q, (B, G, dk), dt, dev), _view("k", k, (B, G, dk), dt, dev)
     vv = _view("v", v, (B, H, dv), dt, dev)
     per_token = _per_token(log_decay, (B,), H, dev)
-    o = torch.empty((B, H, dv), dtype=dt, device=dev)
-    with torch.cuda.device(dev):
-        st = _lib.load().ssm_decay_attn_update(B, H, G, dk, dv, io, state.data_ptr(), qv, kv, vv,
-                                               log_decay.data_ptr(), per_token,
-                                               dk ** -0.5 if scale is None else scale,
-                                               o.data_ptr(), _stream(dev))
-    _lib.check(st)
+    o = torch.empty_like(v, memory_format=torch.contiguous_format)
+    _call(_lib.load().ssm_decay_attn_update, dev, B, H, G, dk, dv, io, state.data_ptr(), qv, kv, vv,
+          log_decay.data_ptr(), per_token,
+          dk ** -0.5 if scale is None else scale,
+          o.data_ptr())
     return o
 
 
@@ -212,14 +227,12 @@ def residual_norm_fwd(x, residual, weight, scale=None, eps=1e-5):
     _need("residual", residual, x.shape, residual.dtype, dev)
     _need("weight", weight, (D,), _F32, dev)
     _need("scale", scale, (D,), _F32, dev, optional=True)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
     h = torch.empty_like(residual)
     rstd = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
-    with torch.cuda.device(dev):
-        st = _lib.load().ssm_residual_norm_fwd(rows, D, io, ro, xp, xs, residual.data_ptr(),
-                                               weight.data_ptr(), _ptr(scale), eps, y.data_ptr(),
-                                               h.data_ptr(), rstd.data_ptr(), _stream(dev))
-    _lib.check(st)
+    _call(_lib.load().ssm_residual_norm_fwd, dev, rows, D, io, ro, xp, xs, residual.data_ptr(),
+          weight.data_ptr(), _ptr(scale), eps, y.data_ptr(),
+          h.data_ptr(), rstd.data_ptr())
     return y, h, rstd
 
 
@@ -244,13 +257,10 @@ def residual_norm_bwd(dy, dh, h, rstd, weight, x=None, scale=None):
     lib = _lib.load()
     nbytes = lib.ssm_residual_norm_bwd_workspace_bytes(rows, D)
     ws = _workspace(nbytes, dev)
-    with torch.cuda.device(dev):
-        st = lib.ssm_residual_norm_bwd(rows, D, io, ro, dy.data_ptr(), _ptr(dh), h.data_ptr(),
-                                       rstd.data_ptr(), weight.data_ptr(), xp, xs, _ptr(scale),
-                                       None if same else dx.data_ptr(), dres.data_ptr(),
-                                       dw.data_ptr(), _ptr(dscale), ws.data_ptr(), nbytes,
-                                       _stream(dev))
-    _lib.check(st)
+    _call(lib.ssm_residual_norm_bwd, dev, rows, D, io, ro, dy.data_ptr(), _ptr(dh), h.data_ptr(),
+          rstd.data_ptr(), weight.data_ptr(), xp, xs, _ptr(scale),
+          None if same else dx.data_ptr(), dres.data_ptr(),
+          dw.data_ptr(), _ptr(dscale), ws.data_ptr(), nbytes)
     return dict(dx=dx, dresidual=dres, dweight=dw, dscale=dscale)
 
 
@@ -268,13 +278,11 @@ def gated_norm_fwd(x, z, weight, group=None, eps=1e-5, gate_first=False):
     _need("weight", weight, (D,), _F32, dev)
     if group < 1 or D % group:
         raise ValueError(f"{D} channels are not a multiple of group={group}")
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
     rstd = torch.empty((*x.shape[:-1], D // group), dtype=_F32, device=dev)
-    with torch.cuda.device(dev):
-        st = _lib.load().ssm_gated_norm_fwd(rows, D, group, io, xp, xs, zp, zs, weight.data_ptr(),
-                                            eps, int(bool(gate_first)), y.data_ptr(),
-                                            rstd.data_ptr(), _stream(dev))
-    _lib.check(st)
+    _call(_lib.load().ssm_gated_norm_fwd, dev, rows, D, group, io, xp, xs, zp, zs, weight.data_ptr(),
+          eps, int(bool(gate_first)), y.data_ptr(),
+          rstd.data_ptr())
     return y, rstd
 
 
@@ -295,12 +303,9 @@ def gated_norm_bwd(dy, x, z, weight, rstd, group=None, gate_first=False):
     lib = _lib.load()
     nbytes = lib.ssm_gated_norm_bwd_workspace_bytes(rows, D, group)
     ws = _workspace(nbytes, dev)
-    with torch.cuda.device(dev):
-        st = lib.ssm_gated_norm_bwd(rows, D, group, io, dy.data_ptr(), xp, xs, zp, zs,
-                                    weight.data_ptr(), rstd.data_ptr(), int(bool(gate_first)),
-                                    dx.data_ptr(), _ptr(dz), dw.data_ptr(), ws.data_ptr(), nbytes,
-                                    _stream(dev))
-    _lib.check(st)
+    _call(lib.ssm_gated_norm_bwd, dev, rows, D, group, io, dy.data_ptr(), xp, xs, zp, zs,
+          weight.data_ptr(), rstd.data_ptr(), int(bool(gate_first)),
+          dx.data_ptr(), _ptr(dz), dw.data_ptr(), ws.data_ptr(), nbytes)
     return dict(dx=dx, dz=dz, dweight=dw)
 
 
