@@ -82,178 +82,191 @@ struct DaArgs {
 //   bf16 row in order, 2 x ds_read_b64            4.8     8.1   (ds_read2_b64: 16, 32)
 //   bf16 column in order, 2 x ds_read_b64_tr      8.1     4.8
 //   bf16 column, side by side, the same          16.1     8.1
-//   fp32 row, 2 x ds_read_b128                   16.1     8.2
-//   fp32 column, 8 x ds_read_b32                 18.4    32.4
-template <typename T>
-struct Mx;
+//
+// Matrices in LDS are bf16.  Values of fp32 (inputs of that type, the state,
+// products of steps, decayed rows) are sums of bf16 pieces: three hold all 24
+// bits, each taking the next 8, and of the products of two such operands the
+// six largest are formed (the others are below 2^-24), at 6 / 16 of the time of
+// the fp32 matrix instructions.
+template <int N>
+struct Pieces {
+  uint4 p[N];
+};
 
-template <>
-struct Mx<bf16> {
-  typedef uint4 Frag;
-  static constexpr int kChunk = 64;
-  static constexpr int kPadRow = 16, kPadCol = 16;  // elements, for matrices read by rows alone or by columns too
-  static __device__ __forceinline__ constexpr int pos(int k) { return (k & ~31) | ((k & 12) << 1) | ((k & 16) >> 2) | (k & 3); }
-  static __device__ __forceinline__ Frag rowfrag(const bf16 *m, int stride, int row0, int k0) {
-    const int l = threadIdx.x & 63;
-    return *(const uint4 *)(m + (row0 + (l & 15)) * stride + k0 + (l >> 4) * 8);
-  }
-  // a row whose 16-byte units are permuted by x
-  static __device__ __forceinline__ int swizzled(int k, int x) { return pos(k) ^ (x * 8); }
-  static __device__ __forceinline__ Frag rowfrag_swizzled(const bf16 *row, int k0, int x) {
-    const int l = threadIdx.x & 63;
-    return *(const uint4 *)(row + ((k0 + (l >> 4) * 8) ^ (x * 8)));
-  }
-  // from a matrix in order: two reads, volatile so that they do not become one ds_read2_b64
-  static __device__ __forceinline__ Frag rowfrag_inorder(const bf16 *m, int stride, int row0, int k0) {
-    typedef __attribute__((address_space(3))) const volatile uint64_t lds_u64;
-    const int l = threadIdx.x & 63;
-    lds_u64 *p = (lds_u64 *)(m + (row0 + (l & 15)) * stride + k0 + (l >> 4) * 4);
+// acc[x] += a(x) b(x) for x = 0 .. X - 1, smallest products first, neighbours independent
+template <int NA, int NB, int X, typename A, typename B, typename Acc>
+__device__ __forceinline__ void mma_pieces(A a, B b, Acc acc) {
+  constexpr int M = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+  for (int s = M; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+          acc(x) = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a(x).p[i]), __builtin_bit_cast(bf16x8, b(x).p[s - i]), acc(x), 0, 0, 0);
+}
+
+constexpr int kPad = 16;  // elements between rows
+
+__device__ __forceinline__ constexpr int pos(int k) { return (k & ~31) | ((k & 12) << 1) | ((k & 16) >> 2) | (k & 3); }
+
+// Fragments of a matrix of N planes, `plane` elements apart; l: the lane.
+template <int N>
+__device__ __forceinline__ Pieces<N> rowfrag(const bf16 *m, int plane, int stride, int row0, int k0, int l) {
+  Pieces<N> f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) f.p[i] = *(const uint4 *)(m + i * plane + (row0 + (l & 15)) * stride + k0 + (l >> 4) * 8);
+  return f;
+}
+// from a row whose 16-byte units are permuted by x
+__device__ __forceinline__ int swizzled(int k, int x) { return pos(k) ^ (x * 8); }
+template <int N>
+__device__ __forceinline__ Pieces<N> rowfrag_swizzled(const bf16 *row, int plane, int k0, int x, int l) {
+  Pieces<N> f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) f.p[i] = *(const uint4 *)(row + i * plane + ((k0 + (l >> 4) * 8) ^ (x * 8)));
+  return f;
+}
+// from a matrix in order: two reads, volatile so that they do not become one ds_read2_b64
+template <int N>
+__device__ __forceinline__ Pieces<N> rowfrag_inorder(const bf16 *m, int plane, int stride, int row0, int k0, int l) {
+  typedef __attribute__((address_space(3))) const volatile uint64_t lds_u64;
+  Pieces<N> f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    lds_u64 *p = (lds_u64 *)(m + i * plane + (row0 + (l & 15)) * stride + k0 + (l >> 4) * 4);
     const uint2 x = __builtin_bit_cast(uint2, (uint64_t)p[0]), y = __builtin_bit_cast(uint2, (uint64_t)p[4]);
-    return make_uint4(x.x, x.y, y.x, y.y);
+    f.p[i] = make_uint4(x.x, x.y, y.x, y.y);
   }
-  // 16 bytes of a row (elements k .. k + 7), side by side
-  static __device__ __forceinline__ void put_row(bf16 *row, int k, uint4 v) {
-    *(uint2 *)(row + pos(k)) = make_uint2(v.x, v.y);
-    *(uint2 *)(row + pos(k) + 8) = make_uint2(v.z, v.w);
-  }
-  // transposed: contracted along rows, column col0 + l % 16.  The transposing
-  // read gives lane i of 16 column i of a block of 4 rows x 16 columns, of
-  // which it addresses row i / 4, columns 4 (i % 4) ...
-  static __device__ __forceinline__ uint2 tr4(const bf16 *p) {
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p)));
-  }
-  static __device__ __forceinline__ Frag colfrag(const bf16 *m, int stride, int row0, int col0) {
-    const int l = threadIdx.x & 63;
-    const bf16 *p = m + (row0 + (l >> 4) * 4 + ((l >> 2) & 3)) * stride + col0 + (l & 3) * 4;
+  return f;
+}
+// transposed: contracted along rows, column col0 + l % 16.  The transposing
+// read gives lane i of 16 column i of a block of 4 rows x 16 columns, of
+// which it addresses row i / 4, columns 4 (i % 4) ...
+__device__ __forceinline__ uint2 tr4(const bf16 *p) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p)));
+}
+template <int N>
+__device__ __forceinline__ Pieces<N> colfrag(const bf16 *m, int plane, int stride, int row0, int col0, int l) {
+  Pieces<N> f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bf16 *p = m + i * plane + (row0 + (l >> 4) * 4 + ((l >> 2) & 3)) * stride + col0 + (l & 3) * 4;
     const uint2 x = tr4(p), y = tr4(p + 16 * stride);
-    return make_uint4(x.x, x.y, y.x, y.y);
+    f.p[i] = make_uint4(x.x, x.y, y.x, y.y);
   }
-  static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ void floats(Frag f, float (&x)[8]) {
-    const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+  return f;
+}
+template <int N>
+__device__ __forceinline__ void floats(const Pieces<N> &f, float (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-  static __device__ __forceinline__ uint32_t pack_rne(float a, float b) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
-  }
-  // fp32 values as a sum of N bf16 pieces: one piece is rounded to nearest;
-  // of more, each takes the next 8 significant bits (three pieces hold all 24
-  // bits of an fp32 value, two leave a relative error below 2^-15).
-  template <int N>
-  static __device__ __forceinline__ void split2(float a, float b, uint32_t (&o)[N]) {
-    if constexpr (N == 1) {
-      o[0] = pack_rne(a, b);
-    } else {
+  for (int n = N - 1; n >= 0; --n) {
+    const uint32_t w[4] = {f.p[n].x, f.p[n].y, f.p[n].z, f.p[n].w};
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        o[i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-        a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
-        b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xffff0000u);
+      x[2 * i] = n == N - 1 ? a : x[2 * i] + a, x[2 * i + 1] = n == N - 1 ? b : x[2 * i + 1] + b;
     }
   }
-  template <int N>
-  static __device__ __forceinline__ void split(const float (&x)[8], Frag (&o)[N]) {
-    uint32_t w[4][N];
+}
+__device__ __forceinline__ uint32_t pack_rne(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+// Two fp32 values as N pieces, cut off after each 8 bits (three hold all of
+// them, two leave a relative error below 2^-15).
+template <int N>
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&o)[N]) {
+  static_assert(N >= 2, "one piece would be rounded");
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split2<N>(x[2 * i], x[2 * i + 1], w[i]);
-#pragma unroll
-    for (int n = 0; n < N; ++n) o[n] = make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
+  for (int i = 0; i < N; ++i) {
+    o[i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+    a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+    b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
   }
-  // four adjacent values, in N pieces `plane` elements apart
-  template <int N>
-  static __device__ __forceinline__ void put4(bf16 *p, int plane, const float (&x)[4]) {
-    uint32_t a[N], b[N];
-    split2<N>(x[0], x[1], a);
-    split2<N>(x[2], x[3], b);
+}
+template <int N>
+__device__ __forceinline__ Pieces<N> split(const float (&x)[8]) {
+  uint32_t w[4][N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) *(uint2 *)(p + n * plane) = make_uint2(a[n], b[n]);
+  for (int i = 0; i < 4; ++i) split2<N>(x[2 * i], x[2 * i + 1], w[i]);
+  Pieces<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) f.p[n] = make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
+  return f;
+}
+// four adjacent values
+template <int N>
+__device__ __forceinline__ void put4(bf16 *p, int plane, const float (&x)[4]) {
+  uint32_t a[N], b[N];
+  split2<N>(x[0], x[1], a);
+  split2<N>(x[2], x[3], b);
+#pragma unroll
+  for (int n = 0; n < N; ++n) *(uint2 *)(p + n * plane) = make_uint2(a[n], b[n]);
+}
+template <int N>
+__device__ __forceinline__ f32x4 get4(const bf16 *p, int plane) {
+  f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n) {
+    const uint2 w = *(const uint2 *)(p + n * plane);
+    v += f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
   }
-  static __device__ __forceinline__ void store4(void *p, f32x4 v) { *(uint2 *)p = make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3])); }
-  // zeros in place of NaN and infinities
-  static __device__ __forceinline__ Frag finite(Frag f) {
-    uint32_t w[4] = {f.x, f.y, f.z, f.w};
+  return v;
+}
+// zeros in place of NaN and infinities
+template <int N>
+__device__ __forceinline__ void make_finite(Pieces<N> &f) {
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n) {
+    uint32_t w[4] = {f.p[n].x, f.p[n].y, f.p[n].z, f.p[n].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
       if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    f.p[n] = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+// Storage types: pieces of an element, steps per chunk (what LDS holds), and 16
+// bytes of a row of elements k .. on.
+template <typename T>
+struct Store;
+template <>
+struct Store<bf16> {
+  static constexpr int NX = 1, kChunk = 64;
+  static __device__ __forceinline__ void put_inorder(bf16 *row, int, int k, uint4 v) { *(uint4 *)(row + k) = v; }
+  static __device__ __forceinline__ void put_row(bf16 *row, int, int k, uint4 v) {
+    *(uint2 *)(row + pos(k)) = make_uint2(v.x, v.y);
+    *(uint2 *)(row + pos(k) + 8) = make_uint2(v.z, v.w);
+  }
+  static __device__ __forceinline__ void store4(void *p, f32x4 v) { *(uint2 *)p = make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3])); }
   // sign bits of the result are set where an exponent is all ones
   static __device__ __forceinline__ uint32_t nonfinite(uint4 v) {
     constexpr uint32_t m = 0x7f807f80u, one = 0x00800080u;
     return (((v.x & m) + one) | ((v.y & m) + one) | ((v.z & m) + one) | ((v.w & m) + one)) & 0x80008000u;
   }
+  static __device__ __forceinline__ float element(uint4 v, int j) {
+    const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
+    return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+  }
 };
-
 template <>
-struct Mx<float> {
-  struct Frag {
-    f32x4 a, b;
-  };
-  static constexpr int kChunk = 32;
-  static constexpr int kPadRow = 8, kPadCol = 4;
-  static __device__ __forceinline__ constexpr int pos(int k) { return k; }
-  static __device__ __forceinline__ void put_row(float *row, int k, uint4 v) { *(uint4 *)(row + k) = v; }
-  static __device__ __forceinline__ Frag rowfrag_inorder(const float *m, int stride, int row0, int k0) { return rowfrag(m, stride, row0, k0); }
-  static __device__ __forceinline__ int swizzled(int k, int x) { return k ^ (x * 4); }
-  static __device__ __forceinline__ Frag rowfrag_swizzled(const float *row, int k0, int x) {
-    const int l = threadIdx.x & 63, k = k0 + (l >> 4) * 4;
-    return Frag{*(const f32x4 *)(row + (k ^ (x * 4))), *(const f32x4 *)(row + ((k + 16) ^ (x * 4)))};
+struct Store<float> {
+  static constexpr int NX = 3, kChunk = 32;
+  static __device__ __forceinline__ void put_inorder(bf16 *row, int plane, int k, uint4 v) {
+    const float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+    put4<3>(row + k, plane, x);
   }
-  static __device__ __forceinline__ Frag rowfrag(const float *m, int stride, int row0, int k0) {
-    const int l = threadIdx.x & 63;
-    const float *p = m + (row0 + (l & 15)) * stride + k0 + (l >> 4) * 4;
-    return Frag{*(const f32x4 *)p, *(const f32x4 *)(p + 16)};
-  }
-  static __device__ __forceinline__ Frag colfrag(const float *m, int stride, int row0, int col0) {
-    const int l = threadIdx.x & 63;
-    const float *p = m + (row0 + (l >> 4) * 4) * stride + col0 + (l & 15);
-    Frag f;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) f.a[r] = p[r * stride], f.b[r] = p[(16 + r) * stride];
-    return f;
-  }
-  static __device__ __forceinline__ f32x4 mma(const Frag &a, const Frag &b, f32x4 c) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[r], b.a[r], c, 0, 0, 0);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[r], b.b[r], c, 0, 0, 0);
-    return c;
-  }
-  static __device__ __forceinline__ void floats(const Frag &f, float (&x)[8]) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = f.a[r], x[4 + r] = f.b[r];
-  }
-  template <int N>
-  static __device__ __forceinline__ void split(const float (&x)[8], Frag (&o)[N]) {
-    static_assert(N == 1, "fp32 operands are whole");
-#pragma unroll
-    for (int r = 0; r < 4; ++r) o[0].a[r] = x[r], o[0].b[r] = x[4 + r];
-  }
-  template <int N>
-  static __device__ __forceinline__ void put4(float *p, int, const float (&x)[4]) {
-    static_assert(N == 1, "fp32 operands are whole");
-    *(float4 *)p = make_float4(x[0], x[1], x[2], x[3]);
-  }
+  static __device__ __forceinline__ void put_row(bf16 *row, int plane, int k, uint4 v) { put_inorder(row + pos(k) - k, plane, k, v); }
   static __device__ __forceinline__ void store4(void *p, f32x4 v) { *(f32x4 *)p = v; }
-  static __device__ __forceinline__ Frag finite(Frag f) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if ((__float_as_uint(f.a[r]) & 0x7f800000u) == 0x7f800000u) f.a[r] = 0.0f;
-      if ((__float_as_uint(f.b[r]) & 0x7f800000u) == 0x7f800000u) f.b[r] = 0.0f;
-    }
-    return f;
-  }
   static __device__ __forceinline__ uint32_t nonfinite(uint4 v) {
     constexpr uint32_t m = 0x7f800000u, one = 0x00800000u;
     return (((v.x & m) + one) | ((v.y & m) + one) | ((v.z & m) + one) | ((v.w & m) + one)) & 0x80000000u;
   }
+  static __device__ __forceinline__ float element(uint4 v, int j) { return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w); }
 };
 
 // The value, opaque to the compiler: what is computed from it stays where it is
@@ -283,17 +296,17 @@ struct TileRegs {
   // first row of a column with a NaN or an infinity, and *any nonzero.
   // ROWS_ONLY: side by side for row fragments.
   template <bool ROWS_ONLY, bool CHECK>
-  __device__ __forceinline__ void put(T *lds, int stride, int rows, int cols, bool rev, int *first = nullptr, int *any = nullptr) const {
+  __device__ __forceinline__ void put(bf16 *lds, int plane, int stride, int rows, int cols, bool rev, int *first = nullptr, int *any = nullptr) const {
     const int tid = here(threadIdx.x), row = tid / PPR, col = (tid % PPR) * EPP;
     auto one = [&](int lr, uint4 v) {
       if (ROWS_ONLY)
-        Mx<T>::put_row(lds + lr * stride, col, v);
+        Store<T>::put_row(lds + lr * stride, plane, col, v);
       else
-        *(uint4 *)(lds + lr * stride + col) = v;
-      if (CHECK && Mx<T>::nonfinite(v)) {
+        Store<T>::put_inorder(lds + lr * stride, plane, col, v);
+      if (CHECK && Store<T>::nonfinite(v)) {
         *any = 1;
         for (int j = 0; j < EPP; ++j)
-          if (!(fabsf(load_io(lds + lr * stride + col, j)) < INFINITY)) atomicMin(first + col + j, lr);
+          if (!(fabsf(Store<T>::element(v, j)) < INFINITY)) atomicMin(first + col + j, lr);
       }
     };
     if (rows == ROWS && cols == COLS && N * NT == ROWS * PPR) {  // the same for all lanes
@@ -339,20 +352,19 @@ __device__ __forceinline__ double wave_sum_scan(double v) {
 
 template <typename T, int DA, int NW, int NC, int NP, bool STATE_ONLY>
 struct __attribute__((aligned(16))) DaLds {
-  typedef Mx<T> M;
-  static constexpr int C = M::kChunk, TV = NW * NC * 16, ES = sizeof(T);
-  static constexpr int SA = DA + M::kPadRow, SB = DA + M::kPadCol, SC = TV + M::kPadCol;
+  static constexpr int C = Store<T>::kChunk, NX = Store<T>::NX, TV = NW * NC * 16;
+  static constexpr int SA = DA + kPad, SC = TV + kPad;  // rows of a and b, of c
   // Products of steps, only blocks of 32 x 32 up to the diagonal: two row tiles of
   // 32 columns, then two of 64, without padding; instead the 16-byte units of a
   // row are permuted by its number (swizzle), so that 16 rows meet all banks.
   static constexpr int PLANE = 32 * 32 + (C > 32 ? 32 * 64 : 0);
   static __device__ __forceinline__ int pwidth(int tt) { return tt < 2 ? 32 : 64; }
   static __device__ __forceinline__ int prow(int tt, int r) { return (tt < 2 ? tt * 16 * 32 : 32 * 32 + (tt - 2) * 16 * 64) + r * pwidth(tt); }
-  static __device__ __forceinline__ int swizzle(int tt, int r) { return ES == 2 ? (tt < 2 ? (r >> 2) & 3 : (r >> 1) & 7) : r & 7; }
-  T a[STATE_ONLY ? 8 : C * SA];
-  T b[C * SB];
-  T c[C * SC];
-  T p[STATE_ONLY ? 8 : NP * PLANE];
+  static __device__ __forceinline__ int swizzle(int tt, int r) { return tt < 2 ? (r >> 2) & 3 : (r >> 1) & 7; }
+  bf16 a[STATE_ONLY ? 8 : NX * C * SA];
+  bf16 b[NX * C * SA];
+  bf16 c[NX * C * SC];
+  bf16 p[STATE_ONLY ? 8 : NP * PLANE];
   DaDecays<C> dec[2];  // of this chunk and the next
   float diag[C];
   float dots[NW][C];
@@ -366,13 +378,12 @@ struct __attribute__((aligned(16))) DaLds {
 // split sequence's first pass).  DOTS: out . e wanted.
 template <typename T, int DA, int NW, int NC, int NP, int NS, bool DOTS, bool STATE_ONLY>
 __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_attn_kernel(DaArgs args) {
-  typedef Mx<T> M;
-  typedef typename M::Frag Frag;
+  typedef Store<T> M;
   typedef DaLds<T, DA, NW, NC, NP, STATE_ONLY> Lds;
-  constexpr int C = M::kChunk, CT = C / 16, DT = DA / 16, NT = NW * 64, TV = Lds::TV;
-  constexpr int SA = Lds::SA, SB = Lds::SB, SC = Lds::SC, PLANE = Lds::PLANE;
+  constexpr int C = M::kChunk, NX = M::NX, CT = C / 16, DT = DA / 16, NT = NW * 64, TV = Lds::TV;
+  constexpr int SA = Lds::SA, SC = Lds::SC, PLANE = Lds::PLANE, PA = C * SA, PC = C * SC;  // rows, planes
   constexpr int ES = sizeof(T);
-  constexpr int NB = ES == 2 ? 3 : 1;  // pieces of c into the state: all of fp32
+  constexpr int NB = 3;  // pieces of decayed rows into the state: all of fp32
   __shared__ Lds lds;
 
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l15 = lane & 15, lg = lane >> 4;
@@ -476,7 +487,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     }
     if (DOTS && rev && args.last_edge && seg == args.nseg - 1) store_edge(args.nedge - 1);
     // products of steps later in a chunk are never written: they stay zero
-    for (int i = threadIdx.x; i < NP * PLANE * ES / 16; i += NT) ((uint4 *)lds.p)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < NP * PLANE / 8; i += NT) ((uint4 *)lds.p)[i] = make_uint4(0, 0, 0, 0);
   }
   if (threadIdx.x < 2) lds.bad[threadIdx.x] = 0;
   for (int i = threadIdx.x; i < TV; i += NT) lds.first[i] = C;
@@ -546,12 +557,10 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     // the edge before this chunk's rows, -1 if there is none
     const int edge = DOTS && ((t0 + low) & ((1 << args.edge_shift) - 1)) == 0 ? (int)((t0 + low) >> args.edge_shift) - 1 : -1;
     if (DOTS && !rev && edge >= 0) dot_edge(edge);
-    // byte offsets of this lane's row and columns in outputs, from those of row `low`
-    const uint32_t loff = (uint32_t)(rev ? rows - 1 - l15 : l15) * sto + (wcol0 + lg * 4) * oes;
     __syncthreads();  // the last chunk's readers are done
-    if constexpr (!STATE_ONLY) ra.template put<true, false>(lds.a, SA, rows, da, rev);
-    rb.template put<false, false>(lds.b, SB, rows, da, rev);
-    rc.template put<false, !STATE_ONLY>(lds.c, SC, rows, ccols, rev, lds.first, lds.bad + par);
+    if constexpr (!STATE_ONLY) ra.template put<true, false>(lds.a, PA, SA, rows, da, rev);
+    rb.template put<false, false>(lds.b, PA, SA, rows, da, rev);
+    rc.template put<false, !STATE_ONLY>(lds.c, PC, SC, rows, ccols, rev, lds.first, lds.bad + par);
     if (DOTS && ci > 0) flush_dots(ci - 1);
     __syncthreads();
     const DaDecays<C> &dec = lds.dec[par];
@@ -572,25 +581,25 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
         int idx = w + j * NW;
         asm volatile("" : "+s"(idx));
         if (idx >= NTILE) break;
+        const int l = here(lane), l15 = l & 15, lg = l >> 4;
         const int tt = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, st = idx - tt * (tt + 1) / 2;
-        // all reads first, then two chains of products
-        constexpr int KB = DA / 32 < 2 ? DA / 32 : 2;
-        f32x4 x = {0, 0, 0, 0}, x2 = {0, 0, 0, 0};
+        // two chains of products, their reads first
+        constexpr int KB = DA / 32 < 2 ? 1 : 2;
+        f32x4 y[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) y[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int k0 = 0; k0 < DA / 32; k0 += KB) {
-          Frag fa[KB], fb[KB];
+          Pieces<NX> fa[KB], fb[KB];
 #pragma unroll
           for (int k = 0; k < KB; ++k) {
-            fb[k] = M::rowfrag_inorder(lds.b, SB, st * 16, (k0 + k) * 32);
-            fa[k] = M::rowfrag(lds.a, SA, tt * 16, (k0 + k) * 32);
+            fb[k] = rowfrag_inorder<NX>(lds.b, PA, SA, st * 16, (k0 + k) * 32, l);
+            fa[k] = rowfrag<NX>(lds.a, PA, SA, tt * 16, (k0 + k) * 32, l);
           }
-#pragma unroll
-          for (int k = 0; k < KB; ++k) {
-            f32x4 &y = k & 1 ? x2 : x;
-            y = M::mma(fb[k], fa[k], y);
-          }
+          mma_pieces<NX, NX, KB>([&](int k) { return fb[k]; }, [&](int k) { return fa[k]; }, [&](int k) -> f32x4 & { return y[k]; });
         }
-        x += x2;
+        f32x4 x = y[0];
+        if (KB == 2) x += y[KB - 1];
         const int t = tt * 16 + l15, s = st * 16 + lg * 4;
         const float th = dec.gh[t], tl = dec.gl[t];
         const f32x4 sh = *(const f32x4 *)(dec.gh + s), sl = *(const f32x4 *)(dec.gl + s);
@@ -602,7 +611,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
           p[r] = s + r < t + (DOTS ? 0 : 1) ? x[r] * (d * pscale) : 0.0f;
           if (DOTS && s + r == t) lds.diag[t] = x[r] * pscale;
         }
-        M::template put4<NP>(lds.p + Lds::prow(tt, l15) + M::swizzled(s, Lds::swizzle(tt, l15)), PLANE, p);
+        put4<NP>(lds.p + Lds::prow(tt, l15) + swizzled(s, Lds::swizzle(tt, l15)), PLANE, p);
       }
       // what the state gives
 #pragma unroll
@@ -611,24 +620,17 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
         for (int ct = 0; ct < NC; ++ct) acc[tt][ct] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int kk = 0; kk < DA / 32; ++kk) {
-        Frag sf[NC][NS];
+        Pieces<NX> af[CT];
+#pragma unroll
+        for (int tt = 0; tt < CT; ++tt) af[tt] = rowfrag<NX>(lds.a, PA, SA, tt * 16, kk * 32, lane);
 #pragma unroll
         for (int ct = 0; ct < NC; ++ct) {
           float x[8];
 #pragma unroll
           for (int r = 0; r < 4; ++r) x[r] = S[2 * kk][ct][r], x[4 + r] = S[2 * kk + 1][ct][r];
-          M::template split<NS>(x, sf[ct]);
+          const Pieces<NS> sf = split<NS>(x);
+          mma_pieces<NS, NX, CT>([&](int) { return sf; }, [&](int tt) { return af[tt]; }, [&](int tt) -> f32x4 & { return acc[tt][ct]; });
         }
-        Frag af[CT];
-#pragma unroll
-        for (int tt = 0; tt < CT; ++tt) af[tt] = M::rowfrag(lds.a, SA, tt * 16, kk * 32);
-        // (neighbouring products are independent)
-#pragma unroll
-        for (int i = NS - 1; i >= 0; --i)
-#pragma unroll
-          for (int tt = 0; tt < CT; ++tt)
-#pragma unroll
-            for (int ct = 0; ct < NC; ++ct) acc[tt][ct] = M::mma(sf[ct][i], af[tt], acc[tt][ct]);
       }
 #pragma unroll
       for (int tt = 0; tt < CT; ++tt) {
@@ -650,13 +652,13 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
           ev[tt][ct] = Vec4<T>::load_b(pe + (int64_t)low * ste, (uint32_t)(rev ? rows - 1 - row : row) * ste + col * ES);
         }
     }
-    if (ci + 1 < nchunk) fetch(ci + 1);
+    if ((STATE_ONLY || !DOTS) && ci + 1 < nchunk) fetch(ci + 1);
     if constexpr (!STATE_ONLY) __syncthreads();  // all products are there
-    Frag cf[C / 32][NC];
+    Pieces<NX> cf[C / 32][NC];
 #pragma unroll
     for (int kk = 0; kk < C / 32; ++kk)
 #pragma unroll
-      for (int ct = 0; ct < NC; ++ct) cf[kk][ct] = M::colfrag(lds.c, SC, kk * 32, (w * NC + ct) * 16);
+      for (int ct = 0; ct < NC; ++ct) cf[kk][ct] = colfrag<NX>(lds.c, PC, SC, kk * 32, (w * NC + ct) * 16, here(lane));
     if constexpr (!STATE_ONLY) {
       if (threadIdx.x == 0) lds.bad[par ^ 1] = 0;
       // A NaN or an infinity in c must not meet the zeros of earlier steps in
@@ -666,19 +668,24 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
 #pragma unroll
         for (int kk = 0; kk < C / 32; ++kk)
 #pragma unroll
-          for (int ct = 0; ct < NC; ++ct) cf[kk][ct] = M::finite(cf[kk][ct]);
+          for (int ct = 0; ct < NC; ++ct) make_finite(cf[kk][ct]);
       }
+      const int lp = here(lane);
+      // (steps kk * 32 on meet row tiles 2 kk on; one piece of the products at a time)
 #pragma unroll
       for (int kk = 0; kk < C / 32; ++kk)
 #pragma unroll
         for (int i = NP - 1; i >= 0; --i) {
-          Frag pf[CT];
+          Pieces<1> pf[CT];
 #pragma unroll
-          for (int tt = 2 * kk; tt < CT; ++tt) pf[tt] = M::rowfrag_swizzled(lds.p + i * PLANE + Lds::prow(tt, l15), kk * 32, Lds::swizzle(tt, l15));
+          for (int tt = 2 * kk; tt < CT; ++tt) pf[tt] = rowfrag_swizzled<1>(lds.p + i * PLANE + Lds::prow(tt, lp & 15), 0, kk * 32, Lds::swizzle(tt, lp & 15), lp);
 #pragma unroll
-          for (int tt = 2 * kk; tt < CT; ++tt)
+          for (int j = NX == 1 ? 0 : NP - 1 - i; j >= 0; --j)
 #pragma unroll
-            for (int ct = 0; ct < NC; ++ct) acc[tt][ct] = M::mma(cf[kk][ct], pf[tt], acc[tt][ct]);
+            for (int tt = 2 * kk; tt < CT; ++tt)
+#pragma unroll
+              for (int ct = 0; ct < NC; ++ct)
+                acc[tt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cf[kk][ct].p[j]), __builtin_bit_cast(bf16x8, pf[tt].p[0]), acc[tt][ct], 0, 0, 0);
         }
       if (bad) {
 #pragma unroll
@@ -686,19 +693,22 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
           int *first = lds.first + (w * NC + ct) * 16;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int f = first[lg * 4 + r];
+            const int f = first[(lp >> 4) * 4 + r];
 #pragma unroll
             for (int tt = 0; tt < CT; ++tt)
-              if (tt * 16 + l15 >= f) acc[tt][ct][r] = NAN;
+              if (tt * 16 + (lp & 15) >= f) acc[tt][ct][r] = NAN;
           }
-          if (first[l15] < C) {
+          if (first[lp & 15] < C) {
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) S[dt][ct] = f32x4{NAN, NAN, NAN, NAN};
           }
-          first[l15] = C;  // for the next chunk; these columns are this wave's alone
+          first[lp & 15] = C;  // for the next chunk; these columns are this wave's alone
         }
       }
-      // out^T: column wcol0 + ct * 16 + lg * 4 + r of step tt * 16 + l15
+      // out^T: column wcol0 + ct * 16 + lg * 4 + r of step tt * 16 + l15; loff: byte
+      // offset of this lane's row and columns from those of row `low`
+      const int lo = here(lane), l15 = lo & 15, lg = lo >> 4;
+      const uint32_t loff = (uint32_t)(rev ? rows - 1 - l15 : l15) * sto + (wcol0 + lg * 4) * oes;
 #pragma unroll
       for (int tt = 0; tt < CT; ++tt) {
         const int i = tt * 16 + l15;
@@ -713,9 +723,9 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
 #pragma unroll
           for (int ct = 0; ct < NC; ++ct) {
             const int col = wcol0 + ct * 16 + lg * 4;
-            const float4 c = Vec4<T>::cvt(Vec4<T>::load(lds.c + i * SC, (w * NC + ct) * 16 + lg * 4));
+            const f32x4 cv = get4<NX>(lds.c + i * SC + (w * NC + ct) * 16 + lg * 4, PC);
             const float4 x = Vec4<T>::cvt(ev[tt][ct]);
-            const f32x4 cv = {c.x, c.y, c.z, c.w}, xv = {x.x, x.y, x.z, x.w};
+            const f32x4 xv = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               if (col < dc) dot = fmaf(acc[tt][ct][r], xv[r], dot);
@@ -739,6 +749,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
         }
       }
     }
+    if (!STATE_ONLY && DOTS && ci + 1 < nchunk) fetch(ci + 1);
     // the chunk's steps enter the state
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
@@ -746,28 +757,26 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
       for (int ct = 0; ct < NC; ++ct) S[dt][ct] *= e;
 #pragma unroll
     for (int kk = 0; kk < C / 32; ++kk) {
-      Frag xf[NC][NB];
+      Pieces<NB> xf[NC];
       const f32x4 y0 = *(const f32x4 *)(dec.out + kk * 32 + lg * 4), y1 = *(const f32x4 *)(dec.out + kk * 32 + 16 + lg * 4);
 #pragma unroll
       for (int ct = 0; ct < NC; ++ct) {
         float x[8];
-        M::floats(cf[kk][ct], x);
+        floats(cf[kk][ct], x);
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[r] *= y0[r], x[4 + r] *= y1[r];
-        M::template split<NB>(x, xf[ct]);
+        xf[ct] = split<NB>(x);
       }
-      constexpr int G = DT < 4 ? DT : 4;  // independent products side by side
+      const int ls = here(lane);
+      constexpr int G = (DT < 4 ? DT : 4) / (NX == 1 ? 1 : 2);  // independent products side by side
 #pragma unroll
       for (int d0 = 0; d0 < DT; d0 += G) {
-        Frag bf[G];
+        Pieces<NX> bf[G];
 #pragma unroll
-        for (int d = 0; d < G; ++d) bf[d] = M::colfrag(lds.b, SB, kk * 32, (d0 + d) * 16);
+        for (int d = 0; d < G; ++d) bf[d] = colfrag<NX>(lds.b, PA, SA, kk * 32, (d0 + d) * 16, ls);
 #pragma unroll
-        for (int i = NB - 1; i >= 0; --i)
-#pragma unroll
-          for (int d = 0; d < G; ++d)
-#pragma unroll
-            for (int ct = 0; ct < NC; ++ct) S[d0 + d][ct] = M::mma(bf[d], xf[ct][i], S[d0 + d][ct]);
+        for (int ct = 0; ct < NC; ++ct)
+          mma_pieces<NX, NB, G>([&](int d) { return bf[d]; }, [&](int) { return xf[ct]; }, [&](int d) -> f32x4 & { return S[d0 + d][ct]; });
       }
     }
     if (DOTS && rev && edge >= 0) store_edge(edge);
@@ -821,14 +830,12 @@ hipError_t launch_da(const DaArgs &a, hipStream_t s) {
 
 template <typename T, int DA, int NW>
 hipError_t launch_da_mode(const DaArgs &a, bool dots, bool state_only, hipStream_t s) {
-  if (state_only) return launch_da<T, DA, NW, 1, 1, false, true>(a, s);
-  if constexpr (sizeof(T) == 2) {
-    // One piece of the in-chunk products would leave the output an error of
-    // 1.4 roundings instead of one; two pieces of both operands leave one.
-    return dots ? launch_da<T, DA, NW, 3, 3, true, false>(a, s) : launch_da<T, DA, NW, 2, 2, false, false>(a, s);
-  } else {
-    return dots ? launch_da<T, DA, NW, 1, 1, true, false>(a, s) : launch_da<T, DA, NW, 1, 1, false, false>(a, s);
-  }
+  if (state_only) return launch_da<T, DA, NW, 2, 2, false, true>(a, s);
+  if (dots) return launch_da<T, DA, NW, 3, 3, true, false>(a, s);
+  // To a bf16 output, one piece of the in-chunk products would leave an error
+  // of 1.4 roundings instead of one; two pieces of both operands leave one.
+  constexpr int N = sizeof(T) == 2 ? 2 : 3;
+  return launch_da<T, DA, NW, N, N, false, false>(a, s);
 }
 
 template <typename T, int DA>
