@@ -56,7 +56,7 @@ __device__ __forceinline__ float row_sum(float v, float (*lds)[16], int slot) {
     __syncthreads();
     v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) v += lds[slot][i];
+    for (int i = 0; i < TPR / 64; ++i) v += lds[slot][threadIdx.x / TPR * (TPR / 64) + i];
   }
   return v;
 }
@@ -86,20 +86,34 @@ __device__ __forceinline__ void put_partial(const F8 (&acc)[V], int n8, float *o
   }
 }
 
-// out[c] = sum over rows of part[row][c], in a fixed order.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int rows, int64_t dim, float *out) {
-  __shared__ float s[32][33];
-  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + c;
+// out[c] = sum over rows of part[row][c], in a fixed order; blockIdx.y: the
+// first or the second of two such sums, whose partial sums lie one after the other.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int rows, int64_t dim, float *out, float *out2) {
+  __shared__ float s[64][17];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int64_t col = (int64_t)blockIdx.x * 16 + c;
+  part += blockIdx.y * rows * dim;
+  if (blockIdx.y) out = out2;
   float v = 0.0f;
-  if (col < dim)
-    for (int i = r; i < rows; i += 32) v += part[(int64_t)i * dim + col];
+  if (col < dim) {
+    constexpr int U = 4;  // loads under way
+    int i = r;
+    for (; i + 64 * (U - 1) < rows; i += 64 * U) {
+      float x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = part[(int64_t)(i + 64 * u) * dim + col];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v += x[u];
+    }
+    for (; i < rows; i += 64) v += part[(int64_t)i * dim + col];
+  }
   s[r][c] = v;
   __syncthreads();
-  if (r == 0 && col < dim) {
-    for (int i = 1; i < 32; ++i) v += s[i][c];
-    out[col] = v;
+  for (int n = 32; n >= 1; n >>= 1) {
+    if (r < n) s[r][c] += s[r + n][c];
+    __syncthreads();
   }
+  if (r == 0 && col < dim) out[col] = s[0][c];
 }
 
 template <typename T, typename R, int TPR, int V, int NT>
@@ -173,14 +187,25 @@ __global__ void __launch_bounds__(NT) residual_norm_bwd_kernel(ResidualNormArgs 
     const int64_t row = r0 + threadIdx.x / TPR;
     const bool on = row < a.rows;
     const float rstd = on ? a.rstd[row] : 0.0f;
-    F8 hat[V], u[V];
+    F8 hat[V], u[V], d[V], x[V];
     float s = 0.0f;
+    // Everything of the row is on its way before the sum needs the first of it
+    // (16384 x 2048, bf16 and fp32: 127 us against 156 us), where registers hold it.
+    constexpr bool kEarly = V <= 3;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int p = i * TPR + l;
       if (on && p < n8) {
         hat[i] = load8((const R *)a.h + row * a.dim + p * 8);
         u[i] = load8((const T *)a.dy + row * a.dim + p * 8);
+        if (kEarly && a.dh) d[i] = load8((const R *)a.dh + row * a.dim + p * 8);
+        if (kEarly && a.dscale) x[i] = load8((const T *)a.x + row * a.x_stride + p * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int p = i * TPR + l;
+      if (on && p < n8) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           hat[i].v[j] *= rstd;
@@ -196,26 +221,19 @@ __global__ void __launch_bounds__(NT) residual_norm_bwd_kernel(ResidualNormArgs 
       const int p = i * TPR + l;
       if (on && p < n8) {
         const int64_t o = row * a.dim + p * 8;
-        F8 d;
-        if (a.dh) {
-          d = load8((const R *)a.dh + o);
+        if (!kEarly && a.dh) d[i] = load8((const R *)a.dh + o);
+        if (!kEarly && a.dscale) x[i] = load8((const T *)a.x + row * a.x_stride + p * 8);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d.v[j] = fmaf(rstd, u[i].v[j] - hat[i].v[j] * s, d.v[j]);
-        } else {
+        for (int j = 0; j < 8; ++j) d[i].v[j] = fmaf(rstd, u[i].v[j] - hat[i].v[j] * s, a.dh ? d[i].v[j] : 0.0f);
+        store8((R *)a.dresidual + o, d[i]);
+        if (a.dscale)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d.v[j] = rstd * (u[i].v[j] - hat[i].v[j] * s);
-        }
-        store8((R *)a.dresidual + o, d);
-        if (a.dscale) {
-          const F8 x = load8((const T *)a.x + row * a.x_stride + p * 8);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) as[i].v[j] = fmaf(d.v[j], x.v[j], as[i].v[j]);
-        }
+          for (int j = 0; j < 8; ++j) as[i].v[j] = fmaf(d[i].v[j], x[i].v[j], as[i].v[j]);
         if (a.dx) {
           if (a.scale)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d.v[j] *= sc[i].v[j];
-          store8((T *)a.dx + o, d);
+            for (int j = 0; j < 8; ++j) d[i].v[j] *= sc[i].v[j];
+          store8((T *)a.dx + o, d[i]);
         }
       }
     }
@@ -314,6 +332,12 @@ __global__ void __launch_bounds__(NT) gated_norm_bwd_kernel(GatedNormArgs a, int
         xs[i] = load8(x + p * 8);
         ds[i] = load8((const T *)a.dy + o0 + p * 8);
         if (a.z) zs[i] = load8(z + p * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int p = i * TPR + l;
+      if (on && p < n8) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float gate = a.z ? silu_f(zs[i].v[j]) : 1.0f;
@@ -349,35 +373,43 @@ __global__ void __launch_bounds__(NT) gated_norm_bwd_kernel(GatedNormArgs a, int
   put_partial<TPR, V, NT>(aw, n8, part_w + (int64_t)rb * a.dim + c0, lds);
 }
 
-// Lanes per row: a row of up to 2048 elements by (part of) a wave, more by a
-// workgroup.  Calls f with (TPR, V, NT) as integral constants.
+// Lanes per row and pieces per lane: few pieces, so that many waves share a CU,
+// and few lanes without one.  Calls f with (TPR, V, NT) as integral constants.
 template <int X>
 struct Int {
   static constexpr int v = X;
 };
 template <typename F>
 hipError_t by_row_length(int64_t n, F f) {
+  if (n <= 64) return f(Int<8>{}, Int<1>{}, Int<256>{});
   if (n <= 128) return f(Int<16>{}, Int<1>{}, Int<256>{});
+  if (n <= 256) return f(Int<32>{}, Int<1>{}, Int<256>{});
   if (n <= 512) return f(Int<64>{}, Int<1>{}, Int<256>{});
-  if (n <= 1024) return f(Int<64>{}, Int<2>{}, Int<256>{});
-  if (n <= 2048) return f(Int<64>{}, Int<4>{}, Int<256>{});
+  if (n <= 1024) return f(Int<128>{}, Int<1>{}, Int<256>{});
+  if (n <= 2048) return f(Int<256>{}, Int<1>{}, Int<256>{});
   if (n <= 4096) return f(Int<256>{}, Int<2>{}, Int<256>{});
-  if (n <= 8192) return f(Int<256>{}, Int<4>{}, Int<256>{});
+  if (n <= 6144) return f(Int<256>{}, Int<3>{}, Int<256>{});
+  if (n <= 8192) return f(Int<512>{}, Int<2>{}, Int<512>{});
+  if (n <= 12288) return f(Int<512>{}, Int<3>{}, Int<512>{});
   return f(Int<512>{}, Int<4>{}, Int<512>{});
 }
-int rows_per_workgroup(int64_t n) { return n <= 128 ? 16 : n <= 2048 ? 4 : 1; }
+int rows_per_workgroup(int64_t n) { return n <= 64 ? 32 : n <= 128 ? 16 : n <= 256 ? 8 : n <= 512 ? 4 : n <= 1024 ? 2 : 1; }
 
-// Workgroups that share the rows of one group of channels.
+// Workgroups that share the rows of one group of channels, `most` over all groups.
 int64_t row_workgroups(int64_t rows, int64_t row_len, int64_t ngroups, int64_t most) {
   const int64_t need = (rows + rows_per_workgroup(row_len) - 1) / rows_per_workgroup(row_len);
   int64_t n = most / ngroups;
   if (n < 1) n = 1;
   return need < n ? need : n;
 }
-constexpr int64_t kFwdWorkgroups = 2048, kBwdWorkgroups = 1024;
+constexpr int64_t kFwdWorkgroups = 2048;
+// With gradients of weights: as many as are resident at once (registers grow
+// with the pieces per lane), since each writes a row of partial sums
+// (2000 x 16384: 262 us with 1024, 212 us with 256; 4096 x 8192: 151 and 127 us).
+int64_t bwd_workgroups(int64_t n) { return n <= 2048 ? 1024 : n <= 4096 ? 768 : n <= 6144 ? 512 : 256; }
 
-hipError_t column_sum(const float *part, int64_t rows, int64_t dim, float *out, hipStream_t s) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((dim + 31) / 32)), dim3(1024), 0, s, part, (int)rows, dim, out);
+hipError_t column_sum(const float *part, int64_t rows, int64_t dim, float *out, float *out2, hipStream_t s) {
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((dim + 15) / 16), out2 ? 2 : 1), dim3(1024), 0, s, part, (int)rows, dim, out, out2);
   return hipGetLastError();
 }
 
@@ -392,15 +424,13 @@ hipError_t residual_fwd(const ResidualNormArgs &a, hipStream_t s) {
 
 template <typename T, typename R>
 hipError_t residual_bwd(const ResidualNormArgs &a, hipStream_t s) {
-  const int64_t grid = row_workgroups(a.rows, a.dim, 1, kBwdWorkgroups);
+  const int64_t grid = row_workgroups(a.rows, a.dim, 1, bwd_workgroups(a.dim));
   float *pw = (float *)a.workspace, *ps = pw + grid * a.dim;
   hipError_t e = by_row_length(a.dim, [&](auto tpr, auto v, auto nt) {
     hipLaunchKernelGGL((residual_norm_bwd_kernel<T, R, decltype(tpr)::v, decltype(v)::v, decltype(nt)::v>), dim3((unsigned)grid), dim3(decltype(nt)::v), 0, s, a, pw, ps);
     return hipGetLastError();
   });
-  if (e == hipSuccess) e = column_sum(pw, grid, a.dim, a.dweight, s);
-  if (e == hipSuccess && a.dscale) e = column_sum(ps, grid, a.dim, a.dscale, s);
-  return e;
+  return e == hipSuccess ? column_sum(pw, grid, a.dim, a.dweight, a.dscale, s) : e;
 }
 
 template <typename T>
@@ -414,22 +444,22 @@ hipError_t gated_fwd(const GatedNormArgs &a, hipStream_t s) {
 
 template <typename T>
 hipError_t gated_bwd(const GatedNormArgs &a, hipStream_t s) {
-  const int64_t ng = a.dim / a.group, nrow = row_workgroups(a.rows, a.group, ng, kBwdWorkgroups);
+  const int64_t ng = a.dim / a.group, nrow = row_workgroups(a.rows, a.group, ng, bwd_workgroups(a.group));
   float *pw = (float *)a.workspace;
   const hipError_t e = by_row_length(a.group, [&](auto tpr, auto v, auto nt) {
     hipLaunchKernelGGL((gated_norm_bwd_kernel<T, decltype(tpr)::v, decltype(v)::v, decltype(nt)::v>), dim3((unsigned)(ng * nrow)), dim3(decltype(nt)::v), 0, s, a, (int)ng, (int)nrow, pw);
     return hipGetLastError();
   });
-  return e == hipSuccess ? column_sum(pw, nrow, a.dim, a.dweight, s) : e;
+  return e == hipSuccess ? column_sum(pw, nrow, a.dim, a.dweight, nullptr, s) : e;
 }
 
 }  // namespace
 
 int64_t residual_norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
-  return 2 * row_workgroups(rows, dim, 1, kBwdWorkgroups) * dim * 4;
+  return 2 * row_workgroups(rows, dim, 1, bwd_workgroups(dim)) * dim * 4;
 }
 int64_t gated_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t group) {
-  return row_workgroups(rows, group, dim / group, kBwdWorkgroups) * dim * 4;
+  return row_workgroups(rows, group, dim / group, bwd_workgroups(group)) * dim * 4;
 }
 
 hipError_t launch_residual_norm_fwd(const ResidualNormArgs &a, int io_dtype, int res_dtype, hipStream_t s) {
