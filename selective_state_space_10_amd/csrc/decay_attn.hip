@@ -200,22 +200,19 @@ hipError_t launch_kernel(const DaArgs &a, int io_dtype, bool dots, bool state_on
                        : launch_decay_attn_bf16(a, padded(a.da), dots, state_only, s);
 }
 
-// Both passes of a set of roles.
-hipError_t launch_passes(const DaArgs &a, int io_dtype, bool dots, hipStream_t s) {
-  hipError_t e;
-  if (a.nseg > 1) {
-    if ((e = launch_kernel(a, io_dtype, false, true, s)) != hipSuccess) return e;
-    if (a.combined) {
-      const int64_t n = (int64_t)padded(a.da) * cols_of(a.dc) / 4 * a.nslice * a.BH;
-      hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((n + 255) / 256), a.nroles), dim3(256), 0, s, a, padded(a.da), cols_of(a.dc));
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+// The states before all segments (or what they are folded from) of a set of roles.
+hipError_t launch_first_pass(const DaArgs &a, int io_dtype, hipStream_t s) {
+  if (a.nseg == 1) return hipSuccess;
+  hipError_t e = launch_kernel(a, io_dtype, false, true, s);
+  if (e == hipSuccess && a.combined) {
+    const int64_t n = (int64_t)padded(a.da) * cols_of(a.dc) / 4 * a.nslice * a.BH;
+    hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((n + 255) / 256), a.nroles), dim3(256), 0, s, a, padded(a.da), cols_of(a.dc));
+    e = hipGetLastError();
   }
-  return launch_kernel(a, io_dtype, dots, false, s);
+  return e;
 }
 
-DaArgs base_args(const DecayAttnArgs &a, int64_t da, int64_t dc) {
-  const Split sp = split_of(a.L, a.B * a.H, da, dc);
+DaArgs base_args(const DecayAttnArgs &a, int64_t da, int64_t dc, Split sp) {
   DaArgs r{};
   r.combined = sp.nseg >= kCombineFrom;
   r.L = a.L, r.da = da, r.dc = dc, r.g = a.g, r.g_b = a.g_b, r.g_t = a.g_t;
@@ -234,7 +231,7 @@ void take_segments(Carve &c, DaRole &r, const DaArgs &a) {
 }
 
 DaArgs fwd_args(const DecayAttnArgs &a, Carve &c) {
-  DaArgs r = base_args(a, a.dk, a.dv);
+  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L, a.B * a.H, a.dk, a.dv));
   DaRole &o = r.role[0];
   o.a = a.q, o.b = a.k, o.c = a.v;
   o.out = a.o;
@@ -264,7 +261,8 @@ BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
   BwdSet r{};
   const int edge_len = edge_len_of(a, io_dtype == 0 ? 4 : 2);
   r.want_g = want_g;
-  r.q = r.k = base_args(a, a.dv, a.dk), r.v = base_args(a, a.dk, a.dv);
+  const Split sp = split_of(a.L, a.B * a.H, a.dv, a.dk);
+  r.q = r.k = base_args(a, a.dv, a.dk, sp), r.v = base_args(a, a.dk, a.dv, sp);
   DaRole &q = r.q.role[0], &k = r.k.role[0], &v = r.v.role[0];
   q.a = a.dout, q.b = a.v, q.c = a.k, q.e = a.q;
   k.a = a.v, k.b = a.dout, k.c = a.q, k.e = a.k;
@@ -274,7 +272,8 @@ BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
   q.state_in = a.state0, q.state_in_t = 1, k.state_in_t = 1;
   v.state_out = a.dstate0;
   q.out = a.dq, k.out = a.dk_out, v.out = a.dv_out;
-  take_segments(c, q, r.q), take_segments(c, k, r.k), take_segments(c, v, r.v);
+  take_segments(c, q, r.q), take_segments(c, k, r.k);
+  if (r.k.nseg > 1) v.loc = k.loc, v.tot = k.tot, v.loc_t = 1, v.cols_t = cols_of(a.dk), v.nslice_t = (int)slices_of(a.dk), r.v.dc_t = padded(a.dv);
   if (a.G < a.H) {
     const int64_t n = a.B * a.L * a.H * a.dk;
     q.out = r.dq_part = c.take<float>(n), k.out = r.dk_part = c.take<float>(n);
@@ -310,16 +309,22 @@ int64_t decay_attn_bwd_workspace_bytes(const DecayAttnArgs &a, int io_dtype) {
 
 hipError_t launch_decay_attn_fwd(const DecayAttnArgs &a, int io_dtype, hipStream_t s) {
   Carve c{(char *)a.workspace};
-  return launch_passes(fwd_args(a, c), io_dtype, false, s);
+  const DaArgs r = fwd_args(a, c);
+  const hipError_t e = launch_first_pass(r, io_dtype, s);
+  return e == hipSuccess ? launch_kernel(r, io_dtype, false, false, s) : e;
 }
 
 hipError_t launch_decay_attn_bwd(const DecayAttnArgs &a, int io_dtype, hipStream_t s) {
   Carve c{(char *)a.workspace};
   const BwdSet r = bwd_args(a, io_dtype, a.dlog_decay != nullptr, c);
   hipError_t e;
-  // backward in time first: it writes the states that the forward pass dots at edges
+  // dk and dq have states of one shape: one first pass for both; dv's is dk's, transposed
+  DaArgs first = r.k;
+  first.nroles = 2, first.role[1] = r.q.role[0];
+  if ((e = launch_first_pass(first, io_dtype, s)) != hipSuccess) return e;
+  // backward in time before forward: it writes the states that the latter dots at edges
   for (const DaArgs *p : {&r.k, &r.v, &r.q})
-    if ((e = launch_passes(*p, io_dtype, r.want_g && p != &r.v, s)) != hipSuccess) return e;
+    if ((e = launch_kernel(*p, io_dtype, r.want_g && p != &r.v, false, s)) != hipSuccess) return e;
   if (r.want_g) {
     DaDecayGrad d{};
     d.dots_q = r.q.role[0].dots, d.dots_k = r.k.role[0].dots, d.edge_dot = r.q.role[0].edge_dot;

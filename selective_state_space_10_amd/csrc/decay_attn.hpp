@@ -47,6 +47,7 @@ struct DaRole {
   float *state_out;      // (B, H, da, dc), NULL = not wanted
   float *dots;           // (slices, B * H, L) partial sums of out . e, or NULL
   float *loc, *tot;      // segments: end states from zero (or, combined, the states before them), total decays
+  int loc_t, cols_t, nslice_t;  // loc is of a role with the transposed state, with slices of cols_t
   float *edge;           // states at edges (below), (B * H, edges, slices, tile), or NULL
   float *edge_dot;       // forward in time: <S, R> at edges, (slices * waves, B * H, edges)
 };
@@ -56,6 +57,7 @@ struct DaArgs {
   const float *g;
   int64_t g_b, g_t;
   int H, BH, nseg, nslice, nroles;
+  int dc_t;              // rows of the transposed role's tiles
   int combined;          // loc holds the states before the segments
   int64_t seg_len;       // a multiple of the chunk
   // An edge lies before every step E, 2 E, ..., E = 2^edge_shift; edge i - 1 before
@@ -453,26 +455,54 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     for (int k = 32; k >= 1; k >>= 1) v += __shfl_xor(v, k, 64);
     if (lane == 0) R.edge_dot[((int64_t)(slice * NW + w) * args.BH + bh) * args.nedge + i] = v;
   };
+  auto load_state_in = [&] {
+    if (R.state_in) {
+      const float *s = R.state_in + (int64_t)bh * da * dc;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = dt * 16 + lg * 4 + r, col = wcol0 + ct * 16 + l15;
+            if (row < da && col < dc) S[dt][ct][r] = s[R.state_in_t ? col * da + row : row * dc + col];
+          }
+    }
+  };
   if constexpr (!STATE_ONLY) {
-    if (args.combined) {
+    if (R.loc_t) {
+      // From the states of a role whose state is this one's transpose: its tile
+      // of row x (a step of this role's columns) and column y holds, for lane
+      // (x % 16) / 4 * 16 + y % 16, element x % 4.
+      const int cols_t = R.cols_t, tiles_t = (args.dc_t >> 4);
+      auto add = [&](int64_t j, float e) {
+        const int x = wcol0 + l15;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          const int y = dt * 16 + lg * 4, w_t = y % cols_t / 16;
+          const float *p = R.loc + ((j * R.nslice_t + y / cols_t) * cols_t * args.dc_t) + (int64_t)(w_t * tiles_t + x / 16) * 256 + ((x % 16) / 4 * 16 + y % 16) * 4 + x % 4;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[dt][0][r] = S[dt][0][r] * e + (x < dc && y + r < da ? p[r * 4] : 0.0f);
+        }
+      };
+      const int before = rev ? args.nseg - 1 - seg : seg;
+      if (args.combined) {
+        add((int64_t)bh * args.nseg + seg, 0.0f);
+      } else {
+        load_state_in();
+        for (int i = 0; i < before; ++i) {
+          const int64_t j = (int64_t)bh * args.nseg + (rev ? args.nseg - 1 - i : i);
+          add(j, R.tot[j]);
+        }
+      }
+    } else if (args.combined) {
       const float *loc = R.loc + (((int64_t)bh * args.nseg + seg) * args.nslice + slice) * kTile + wtile;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
         for (int ct = 0; ct < NC; ++ct) S[dt][ct] = *(const f32x4 *)(loc + (dt * NC + ct) * 256);
     } else {
-      if (R.state_in) {
-        const float *s = R.state_in + (int64_t)bh * da * dc;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int ct = 0; ct < NC; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int row = dt * 16 + lg * 4 + r, col = wcol0 + ct * 16 + l15;
-              if (row < da && col < dc) S[dt][ct][r] = s[R.state_in_t ? col * da + row : row * dc + col];
-            }
-      }
+      load_state_in();
       // the segments before this one, in the order of the recurrence
       const int before = rev ? args.nseg - 1 - seg : seg;
       for (int i = 0; i < before; ++i) {
@@ -572,6 +602,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     }
 
     f32x4 acc[CT][NC];
+    typename Vec4<T>::raw ev[DOTS ? CT : 1][NC];
     if constexpr (!STATE_ONLY) {
       // products a_t . b_s of steps s <= t with their decays, 16 x 16 tiles over the waves
       constexpr int NTILE = CT * (CT + 1) / 2;
@@ -613,6 +644,15 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
         }
         put4<NP>(lds.p + Lds::prow(tt, l15) + swizzled(s, Lds::swizzle(tt, l15)), PLANE, p);
       }
+      if constexpr (DOTS) {
+#pragma unroll
+        for (int tt = 0; tt < CT; ++tt)
+#pragma unroll
+          for (int ct = 0; ct < NC; ++ct) {
+            const int l = here(lane), col = min(wcol0 + ct * 16 + (l >> 4) * 4, dc - 4), row = min(tt * 16 + (l & 15), rows - 1);
+            ev[tt][ct] = Vec4<T>::load_b(pe + (int64_t)low * ste, (uint32_t)(rev ? rows - 1 - row : row) * ste + col * ES);
+          }
+      }
       // what the state gives
 #pragma unroll
       for (int tt = 0; tt < CT; ++tt)
@@ -620,16 +660,20 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
         for (int ct = 0; ct < NC; ++ct) acc[tt][ct] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int kk = 0; kk < DA / 32; ++kk) {
-        Pieces<NX> af[CT];
-#pragma unroll
-        for (int tt = 0; tt < CT; ++tt) af[tt] = rowfrag<NX>(lds.a, PA, SA, tt * 16, kk * 32, lane);
 #pragma unroll
         for (int ct = 0; ct < NC; ++ct) {
           float x[8];
 #pragma unroll
           for (int r = 0; r < 4; ++r) x[r] = S[2 * kk][ct][r], x[4 + r] = S[2 * kk + 1][ct][r];
           const Pieces<NS> sf = split<NS>(x);
-          mma_pieces<NS, NX, CT>([&](int) { return sf; }, [&](int tt) { return af[tt]; }, [&](int tt) -> f32x4 & { return acc[tt][ct]; });
+          constexpr int G = DOTS ? CT / 2 : CT;  // row tiles at a time
+#pragma unroll
+          for (int t0 = 0; t0 < CT; t0 += G) {
+            Pieces<NX> af[G];
+#pragma unroll
+            for (int i = 0; i < G; ++i) af[i] = rowfrag<NX>(lds.a, PA, SA, (t0 + i) * 16, kk * 32, lane);
+            mma_pieces<NS, NX, G>([&](int) { return sf; }, [&](int i) { return af[i]; }, [&](int i) -> f32x4 & { return acc[t0 + i][ct]; });
+          }
         }
       }
 #pragma unroll
@@ -640,18 +684,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
       }
     }
     // The next chunk's rows travel during the rest of this one (and hold no
-    // registers before).
-    typename Vec4<T>::raw ev[DOTS ? CT : 1][NC];
-    if constexpr (DOTS) {
-#pragma unroll
-      for (int tt = 0; tt < CT; ++tt)
-#pragma unroll
-        for (int ct = 0; ct < NC; ++ct) {
-          const int col = min(wcol0 + ct * 16 + lg * 4, dc - 4);
-          const int row = min(tt * 16 + l15, rows - 1);
-          ev[tt][ct] = Vec4<T>::load_b(pe + (int64_t)low * ste, (uint32_t)(rev ? rows - 1 - row : row) * ste + col * ES);
-        }
-    }
+    // registers before; with dot products, which need more, from the state on).
     if ((STATE_ONLY || !DOTS) && ci + 1 < nchunk) fetch(ci + 1);
     if constexpr (!STATE_ONLY) __syncthreads();  // all products are there
     Pieces<NX> cf[C / 32][NC];
