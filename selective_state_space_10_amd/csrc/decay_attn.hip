@@ -39,27 +39,45 @@ int64_t compute_units() {
   return n;
 }
 
-// A sequence is split where batch rows, heads and slices do not fill the card:
-// into so many segments that every CU has the workgroups that its LDS holds, of
-// at least kMinSegment steps.  Measured, bf16, forward: 8 x 2048, 16 heads of
+// Into how many segments a sequence is split: the estimate below is least.
+// Workgroups run `slots` to a CU (as LDS and registers hold them); a CU takes
+// about chunk_us for a chunk of all of them, and 0.3 more of it for a round
+// that is not full.  A first pass costs 0.4 of a main pass of its segments and a
+// launch, combining another.  Measured, bf16, forward: 8 x 2048, 16 heads of
 // 128: 188 us in one piece, 118 us in 2, 111 us in 4, 149 us in 8 segments;
 // 1 x 32768, 40 heads of 128: 2.7 ms in one piece, 552 us in 32, 738 us in 128;
 // 3 x 1111, 8 heads of 72 x 96, fp32: 204 us in one piece, 81 us in 5, 54 us in 9.
 constexpr int64_t kMinSegment = 64;
-Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc) {
-  const int64_t wgs = bh * slices_of(dc), want = compute_units() * (padded(da) > 128 ? 1 : da_waves(dc) == 8 ? 2 : 3);
-  int64_t n = (want + wgs - 1) / wgs;
-  if (n > L / kMinSegment) n = L / kMinSegment;
-  if (n <= 1) return {1, L};
-  const int64_t len = ((L + n - 1) / n + 63) / 64 * 64;
-  return {(int)((L + len - 1) / len), len};
-}
-
 // From how many segments on the states before them are computed once, by a
 // kernel of its own, and not by every workgroup from the end states before it
 // (32 segments of 40 heads of 128: 552 us against 597 us; 4 segments of the
 // 8 x 2048 shape: no difference beyond the launch).
 constexpr int kCombineFrom = 5;
+Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es) {
+  const bool wide = da_waves(dc) == 8;
+  const int64_t cus = compute_units(), wgs = bh * slices_of(dc), chunk = es == 2 ? 64 : 32;
+  const int64_t slots = padded(da) > 128 ? 1 : es == 4 && padded(da) == 128 ? (wide ? 1 : 2) : wide ? 2 : 3;
+  const double chunk_us = wide ? 10.0 : 6.0, launch_us = 5.0;
+  // a segment's states go out and in about four times, at 5 TB/s
+  const double state_us = 4.0 * padded(da) * cols_of(dc) * 4 / 5e6;
+  auto rounds = [&](int64_t n) {
+    const int64_t q = (n + cus - 1) / cus;
+    return (double)q / slots + (q % slots ? 0.3 : 0.0);
+  };
+  Split best{1, L};
+  double least = 0.0;
+  for (int64_t n = 1; n <= 128 && n <= (L + kMinSegment - 1) / kMinSegment; ++n) {
+    const int64_t len = n == 1 ? L : ((L + n - 1) / n + 63) / 64 * 64, segs = (L + len - 1) / len;
+    if (segs != n) continue;
+    const double chunks = (double)((len + chunk - 1) / chunk);
+    double us = rounds(wgs * n) * chunks * chunk_us;
+    if (n > 1) us += 0.4 * rounds(wgs * (n - 1)) * chunks * chunk_us + launch_us;
+    if (n >= kCombineFrom) us += launch_us;
+    if (n > 1) us += n * wgs * state_us;
+    if (n == 1 || us < least) best = {(int)n, len}, least = us;
+  }
+  return best;
+}
 
 }  // namespace
 
@@ -230,8 +248,8 @@ void take_segments(Carve &c, DaRole &r, const DaArgs &a) {
   r.tot = c.take<float>((int64_t)a.BH * a.nseg);
 }
 
-DaArgs fwd_args(const DecayAttnArgs &a, Carve &c) {
-  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L, a.B * a.H, a.dk, a.dv));
+DaArgs fwd_args(const DecayAttnArgs &a, int io_dtype, Carve &c) {
+  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L, a.B * a.H, a.dk, a.dv, io_dtype == 0 ? 4 : 2));
   DaRole &o = r.role[0];
   o.a = a.q, o.b = a.k, o.c = a.v;
   o.out = a.o;
@@ -261,7 +279,7 @@ BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
   BwdSet r{};
   const int edge_len = edge_len_of(a, io_dtype == 0 ? 4 : 2);
   r.want_g = want_g;
-  const Split sp = split_of(a.L, a.B * a.H, a.dv, a.dk);
+  const Split sp = split_of(a.L, a.B * a.H, a.dv, a.dk, io_dtype == 0 ? 4 : 2);
   r.q = r.k = base_args(a, a.dv, a.dk, sp), r.v = base_args(a, a.dk, a.dv, sp);
   DaRole &q = r.q.role[0], &k = r.k.role[0], &v = r.v.role[0];
   q.a = a.dout, q.b = a.v, q.c = a.k, q.e = a.q;
@@ -295,9 +313,9 @@ BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
 
 }  // namespace
 
-int64_t decay_attn_fwd_workspace_bytes(const DecayAttnArgs &a, int) {
+int64_t decay_attn_fwd_workspace_bytes(const DecayAttnArgs &a, int io_dtype) {
   Carve c{nullptr};
-  fwd_args(a, c);
+  fwd_args(a, io_dtype, c);
   return c.used;
 }
 
@@ -309,7 +327,7 @@ int64_t decay_attn_bwd_workspace_bytes(const DecayAttnArgs &a, int io_dtype) {
 
 hipError_t launch_decay_attn_fwd(const DecayAttnArgs &a, int io_dtype, hipStream_t s) {
   Carve c{(char *)a.workspace};
-  const DaArgs r = fwd_args(a, c);
+  const DaArgs r = fwd_args(a, io_dtype, c);
   const hipError_t e = launch_first_pass(r, io_dtype, s);
   return e == hipSuccess ? launch_kernel(r, io_dtype, false, false, s) : e;
 }
