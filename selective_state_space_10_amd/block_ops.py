@@ -12,11 +12,19 @@ from . import _lib
 from .ops import _IO, _io_code, _need, _ptr, _stream
 
 _F32 = torch.float32
+_View4 = _lib.View4
 
 
 def _view(name, t, shape, dtype, dev):
     """A (batch, [step,] head, element) tensor as an ssm_view4: any strides that
     keep 16-byte alignment, with the elements of a head adjacent."""
+    # (the usual tensor first: these calls are most of a small call's time)
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.device == dev and not shape[-1] % 8):
+        ptr = t.data_ptr()
+        if not ptr % 16:
+            st = shape[-1] * shape[-2]
+            return _View4(ptr, st * shape[1] if len(shape) == 4 else st, st, shape[-1])
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.device != dev:
@@ -26,9 +34,6 @@ def _view(name, t, shape, dtype, dev):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     ptr = t.data_ptr()
-    if t.is_contiguous() and not (shape[-1] % 8 or ptr % 16):
-        st = shape[-1] * shape[-2]
-        return _lib.View4(ptr, st * shape[1] if len(shape) == 4 else st, st, shape[-1])
     if len(shape) == 4:
         sb, st, sh, se = t.stride()
     else:
@@ -44,21 +49,39 @@ def _view(name, t, shape, dtype, dev):
     if (sb | st | sh) % (4 if dtype is _F32 else 8) or ptr % 16:
         raise ValueError(f"{name} must keep 16-byte alignment from head to head (strides "
                          f"{t.stride()}, address {ptr:#x}); make it contiguous")
-    return _lib.View4(ptr, sb, st, sh)
+    return _View4(ptr, sb, st, sh)
 
 
+# what torch.cuda.current_stream and current_device ask, without their wrappers
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(fn, dev, *args):
     """fn(*args, current stream) with dev as the current device."""
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream(dev) if _raw_stream is None else _raw_stream(dev.index))
+    index = dev.index
+    if _raw_stream is not None and index == _current_device():
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
             st = fn(*args, _stream(dev))
     if st:
         _lib.check(st)
+
+
+def _is(t, shape, dtype, dev):
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.device == dev)
+
+
+def _want(name, t, shape, dtype, dev):
+    if not _is(t, shape, dtype, dev):
+        _need(name, t, shape, dtype, dev)  # says what is wrong
+
+
+def _want_or_none(name, t, shape, dtype, dev):
+    if t is not None and not _is(t, shape, dtype, dev):
+        _need(name, t, shape, dtype, dev)
 
 
 def _gpu(name, t):
@@ -89,9 +112,12 @@ def _attn_sizes(q, v, rank):
     return dev, G, H, q.shape[-1], v.shape[-1]
 
 
-def _per_token(log_decay, shape, H, dev):
+def _per_token(log_decay, shape, dev):
+    """shape: of one decay per token and head."""
+    if _is(log_decay, shape, _F32, dev):
+        return 1
     per_token = isinstance(log_decay, torch.Tensor) and log_decay.dim() != 1
-    _need("log_decay", log_decay, (*shape, H) if per_token else (H,), _F32, dev)
+    _need("log_decay", log_decay, shape if per_token else shape[-1:], _F32, dev)
     return int(per_token)
 
 
@@ -109,8 +135,8 @@ def decay_attn_fwd(q, k, v, log_decay, scale=None, state0=None, return_final_sta
     io, dt = _io_code(q), q.dtype
     qv, kv = _view("q", q, (B, L, G, dk), dt, dev), _view("k", k, (B, L, G, dk), dt, dev)
     vv = _view("v", v, (B, L, H, dv), dt, dev)
-    per_token = _per_token(log_decay, (B, L), H, dev)
-    _need("state0", state0, (B, H, dk, dv), _F32, dev, optional=True)
+    per_token = _per_token(log_decay, (B, L, H), dev)
+    _want_or_none("state0", state0, (B, H, dk, dv), _F32, dev)
     lib = _lib.load()
     nbytes = lib.ssm_decay_attn_fwd_workspace_bytes(B, L, H, G, dk, dv, io)
     ws = _workspace(nbytes, dev)
@@ -131,9 +157,9 @@ def decay_attn_bwd(q, k, v, log_decay, do, scale=None, state0=None, dstate_final
     io, dt = _io_code(q), q.dtype
     qv, kv = _view("q", q, (B, L, G, dk), dt, dev), _view("k", k, (B, L, G, dk), dt, dev)
     vv, ov = _view("v", v, (B, L, H, dv), dt, dev), _view("do", do, (B, L, H, dv), dt, dev)
-    per_token = _per_token(log_decay, (B, L), H, dev)
-    _need("state0", state0, (B, H, dk, dv), _F32, dev, optional=True)
-    _need("dstate_final", dstate_final, (B, H, dk, dv), _F32, dev, optional=True)
+    per_token = _per_token(log_decay, (B, L, H), dev)
+    _want_or_none("state0", state0, (B, H, dk, dv), _F32, dev)
+    _want_or_none("dstate_final", dstate_final, (B, H, dk, dv), _F32, dev)
     lib = _lib.load()
     nbytes = lib.ssm_decay_attn_bwd_workspace_bytes(B, L, H, G, dk, dv, io)
     ws = _workspace(nbytes, dev)
@@ -157,10 +183,10 @@ def decay_attn_update(state, q, k, v, log_decay, scale=None):
     dev, G, H, dk, dv = _attn_sizes(q, v, 3)
     B = q.shape[0]
     io, dt = _io_code(q), q.dtype
-    _need("state", state, (B, H, dk, dv), _F32, dev)
+    _want("state", state, (B, H, dk, dv), _F32, dev)
     qv, kv = _view("q", q, (B, G, dk), dt, dev), _view("k", k, (B, G, dk), dt, dev)
     vv = _view("v", v, (B, H, dv), dt, dev)
-    per_token = _per_token(log_decay, (B,), H, dev)
+    per_token = _per_token(log_decay, (B, H), dev)
     o = torch.empty_like(v, memory_format=torch.contiguous_format)
     _call(_lib.load().ssm_decay_attn_update, dev, B, H, G, dk, dv, io, state.data_ptr(), qv, kv, vv,
           log_decay.data_ptr(), per_token,
@@ -172,6 +198,8 @@ def decay_attn_update(state, q, k, v, log_decay, scale=None):
 def _rows(name, t, shape, dtype, dev):
     """(pointer, elements from row to row) of a tensor whose rows are evenly
     spaced: contiguous, or a slice of one along its last dimension."""
+    if _is(t, shape, dtype, dev):
+        return t.data_ptr(), shape[-1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.device != dev:
@@ -180,8 +208,6 @@ def _rows(name, t, shape, dtype, dev):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[-1]
     step, span = None, None
     for n, s in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
@@ -224,9 +250,9 @@ def residual_norm_fwd(x, residual, weight, scale=None, eps=1e-5):
     dev, io, D, rows = _norm_input(x)
     xp, xs = _rows("x", x, x.shape, x.dtype, dev)
     ro = _residual_code(residual, x)
-    _need("residual", residual, x.shape, residual.dtype, dev)
-    _need("weight", weight, (D,), _F32, dev)
-    _need("scale", scale, (D,), _F32, dev, optional=True)
+    _want("residual", residual, x.shape, residual.dtype, dev)
+    _want("weight", weight, (D,), _F32, dev)
+    _want_or_none("scale", scale, (D,), _F32, dev)
     y = torch.empty_like(x, memory_format=torch.contiguous_format)
     h = torch.empty_like(residual)
     rstd = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
@@ -242,12 +268,12 @@ def residual_norm_bwd(dy, dh, h, rstd, weight, x=None, scale=None):
     same tensor as dx where they are equal), dweight, dscale (needs x)."""
     dev, io, D, rows = _norm_input(dy)
     ro = _residual_code(h, dy)
-    _need("dy", dy, dy.shape, dy.dtype, dev)
-    _need("h", h, dy.shape, h.dtype, dev)
-    _need("dh", dh, dy.shape, h.dtype, dev, optional=True)
-    _need("rstd", rstd, dy.shape[:-1], _F32, dev)
-    _need("weight", weight, (D,), _F32, dev)
-    _need("scale", scale, (D,), _F32, dev, optional=True)
+    _want("dy", dy, dy.shape, dy.dtype, dev)
+    _want("h", h, dy.shape, h.dtype, dev)
+    _want_or_none("dh", dh, dy.shape, h.dtype, dev)
+    _want("rstd", rstd, dy.shape[:-1], _F32, dev)
+    _want("weight", weight, (D,), _F32, dev)
+    _want_or_none("scale", scale, (D,), _F32, dev)
     xp, xs = (None, D) if x is None or scale is None else _rows("x", x, dy.shape, dy.dtype, dev)
     dres = torch.empty_like(h)
     same = scale is None and h.dtype == dy.dtype
@@ -275,7 +301,7 @@ def gated_norm_fwd(x, z, weight, group=None, eps=1e-5, gate_first=False):
     group = D if group is None else int(group)
     xp, xs = _rows("x", x, x.shape, x.dtype, dev)
     zp, zs = (None, D) if z is None else _rows("z", z, x.shape, x.dtype, dev)
-    _need("weight", weight, (D,), _F32, dev)
+    _want("weight", weight, (D,), _F32, dev)
     if group < 1 or D % group:
         raise ValueError(f"{D} channels are not a multiple of group={group}")
     y = torch.empty_like(x, memory_format=torch.contiguous_format)
@@ -292,11 +318,11 @@ def gated_norm_bwd(dy, x, z, weight, rstd, group=None, gate_first=False):
     group = D if group is None else int(group)
     xp, xs = _rows("x", x, x.shape, x.dtype, dev)
     zp, zs = (None, D) if z is None else _rows("z", z, x.shape, x.dtype, dev)
-    _need("dy", dy, x.shape, x.dtype, dev)
-    _need("weight", weight, (D,), _F32, dev)
+    _want("dy", dy, x.shape, x.dtype, dev)
+    _want("weight", weight, (D,), _F32, dev)
     if group < 1 or D % group:
         raise ValueError(f"{D} channels are not a multiple of group={group}")
-    _need("rstd", rstd, (*x.shape[:-1], D // group), _F32, dev)
+    _want("rstd", rstd, (*x.shape[:-1], D // group), _F32, dev)
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     dz = torch.empty(x.shape, dtype=x.dtype, device=dev) if z is not None else None
     dw = torch.empty_like(weight)

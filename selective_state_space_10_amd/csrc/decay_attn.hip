@@ -196,9 +196,11 @@ __global__ void __launch_bounds__(64) decay_grad_heads_kernel(const float *sums,
   out[h] = (float)v;
 }
 
-// Gradients of shared heads: (rows, G, share, d) fp32 -> (rows, G, d), summed in order.
+// Gradients of shared heads, dq (blockIdx.y 0) and dk: (rows, G, share, d) fp32
+// -> (rows, G, d), summed in order.
 template <typename T>
-__global__ void __launch_bounds__(256) shared_heads_kernel(const float *part, int64_t n4, int d4, int share, T *out) {
+__global__ void __launch_bounds__(256) shared_heads_kernel(const float *part, const float *part2, int64_t n4, int d4, int share, T *out, T *out2) {
+  if (blockIdx.y) part = part2, out = out2;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n4) return;
   const int64_t rg = i / d4, x = i % d4;
@@ -361,16 +363,12 @@ hipError_t launch_decay_attn_bwd(const DecayAttnArgs &a, int io_dtype, hipStream
   }
   if (r.dq_part) {
     const int64_t n4 = a.B * a.L * a.G * a.dk / 4;
-    const dim3 grid((unsigned)((n4 + 255) / 256));
-    for (int i = 0; i < 2; ++i) {
-      const float *p = i ? r.dk_part : r.dq_part;
-      void *o = i ? a.dk_out : a.dq;
-      if (io_dtype == 0)
-        hipLaunchKernelGGL(shared_heads_kernel<float>, grid, dim3(256), 0, s, p, n4, (int)(a.dk / 4), (int)(a.H / a.G), (float *)o);
-      else
-        hipLaunchKernelGGL(shared_heads_kernel<bf16>, grid, dim3(256), 0, s, p, n4, (int)(a.dk / 4), (int)(a.H / a.G), (bf16 *)o);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+    const dim3 grid((unsigned)((n4 + 255) / 256), 2);
+    if (io_dtype == 0)
+      hipLaunchKernelGGL(shared_heads_kernel<float>, grid, dim3(256), 0, s, r.dq_part, r.dk_part, n4, (int)(a.dk / 4), (int)(a.H / a.G), (float *)a.dq, (float *)a.dk_out);
+    else
+      hipLaunchKernelGGL(shared_heads_kernel<bf16>, grid, dim3(256), 0, s, r.dq_part, r.dk_part, n4, (int)(a.dk / 4), (int)(a.H / a.G), (bf16 *)a.dq, (bf16 *)a.dk_out);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
 }
