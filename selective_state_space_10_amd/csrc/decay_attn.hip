@@ -43,16 +43,25 @@ int64_t compute_units() {
 // Workgroups run `slots` to a CU (as LDS and registers hold them); a CU takes
 // about chunk_us for a chunk of all of them, and 0.3 more of it for a round
 // that is not full.  A first pass costs 0.4 of a main pass of its segments and a
-// launch, combining another.  Measured, bf16, forward: 8 x 2048, 16 heads of
-// 128: 188 us in one piece, 118 us in 2, 111 us in 4, 149 us in 8 segments;
-// 1 x 32768, 40 heads of 128: 2.7 ms in one piece, 552 us in 32, 738 us in 128;
-// 3 x 1111, 8 heads of 72 x 96, fp32: 204 us in one piece, 81 us in 5, 54 us in 9.
+// launch, combining another.  Measured, forward and backward, in us (* the split taken):
+//   segments                              1           2 to 6             more
+//   8 x 2048, 16 heads of 128, bf16       152, 587    2: 137, 422        8: 162, 514
+//                                                     4*: 125, 416
+//   1 x 32768, 40 heads of 128, bf16      2117, 9235  6: 675, 2240       12*: 624, 2062  32: 651, 2155  64: 705, 2315
+//   3 x 1111, 8 heads of 72 x 96, fp32    155, 542    6: 58, 154         9*: 48, 130     18: 55, 160
+//   2 x 1537, 32 heads of 64, fp32        143, 535    4: 74, 214         12*: 59, 174    25: 67, 210
+// A second workgroup on a CU adds little where the first has one to itself (one
+// segment of the first shape takes 4.7 us per chunk on half of the CUs, two on
+// each of all CUs 5.3 us each): the vector ALU's issue and the clock, which falls
+// to 1.85 GHz under this load, bound both.
 constexpr int64_t kMinSegment = 64;
 // From how many segments on the states before them are computed once, by a
-// kernel of its own, and not by every workgroup from the end states before it
-// (32 segments of 40 heads of 128: 552 us against 597 us; 4 segments of the
-// 8 x 2048 shape: no difference beyond the launch).
-constexpr int kCombineFrom = 5;
+// kernel of its own, and not by every workgroup from the end states before it.
+// Forward, folded and combined: 9 segments (3 x 1111, 8 heads of 72 x 96, fp32)
+// 43.5 and 47.4 us, 12 (2 x 1537, 32 heads of 64, fp32) 55 and 56, 32 (1 x 32768,
+// 40 heads of 128, bf16) 678 and 653.  Backward, where dv folds transposed states
+// and there are more passes to one combining: 131 and 127, 162 and 165, 2335 and 2155 us.
+constexpr int kCombineFwd = 16, kCombineBwd = 5;
 Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es) {
   const bool wide = da_waves(dc) == 8;
   const int64_t cus = compute_units(), wgs = bh * slices_of(dc), chunk = es == 2 ? 64 : 32;
@@ -72,7 +81,7 @@ Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es) {
     const double chunks = (double)((len + chunk - 1) / chunk);
     double us = rounds(wgs * n) * chunks * chunk_us;
     if (n > 1) us += 0.4 * rounds(wgs * (n - 1)) * chunks * chunk_us + launch_us;
-    if (n >= kCombineFrom) us += launch_us;
+    if (n >= kCombineBwd) us += launch_us;
     if (n > 1) us += n * wgs * state_us;
     if (n == 1 || us < least) best = {(int)n, len}, least = us;
   }
@@ -232,9 +241,9 @@ hipError_t launch_first_pass(const DaArgs &a, int io_dtype, hipStream_t s) {
   return e;
 }
 
-DaArgs base_args(const DecayAttnArgs &a, int64_t da, int64_t dc, Split sp) {
+DaArgs base_args(const DecayAttnArgs &a, int64_t da, int64_t dc, Split sp, int combine_from) {
   DaArgs r{};
-  r.combined = sp.nseg >= kCombineFrom;
+  r.combined = sp.nseg >= combine_from;
   r.L = a.L, r.da = da, r.dc = dc, r.g = a.g, r.g_b = a.g_b, r.g_t = a.g_t;
   r.nroles = 1;
   r.H = (int)a.H, r.BH = (int)(a.B * a.H), r.nseg = sp.nseg, r.seg_len = sp.seg_len;
@@ -251,7 +260,7 @@ void take_segments(Carve &c, DaRole &r, const DaArgs &a) {
 }
 
 DaArgs fwd_args(const DecayAttnArgs &a, int io_dtype, Carve &c) {
-  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L, a.B * a.H, a.dk, a.dv, io_dtype == 0 ? 4 : 2));
+  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L, a.B * a.H, a.dk, a.dv, io_dtype == 0 ? 4 : 2), kCombineFwd);
   DaRole &o = r.role[0];
   o.a = a.q, o.b = a.k, o.c = a.v;
   o.out = a.o;
@@ -282,7 +291,7 @@ BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
   const int edge_len = edge_len_of(a, io_dtype == 0 ? 4 : 2);
   r.want_g = want_g;
   const Split sp = split_of(a.L, a.B * a.H, a.dv, a.dk, io_dtype == 0 ? 4 : 2);
-  r.q = r.k = base_args(a, a.dv, a.dk, sp), r.v = base_args(a, a.dk, a.dv, sp);
+  r.q = r.k = base_args(a, a.dv, a.dk, sp, kCombineBwd), r.v = base_args(a, a.dk, a.dv, sp, kCombineBwd);
   DaRole &q = r.q.role[0], &k = r.k.role[0], &v = r.v.role[0];
   q.a = a.dout, q.b = a.v, q.c = a.k, q.e = a.q;
   k.a = a.v, k.b = a.dout, k.c = a.q, k.e = a.k;
