@@ -10,6 +10,11 @@
 // group of channels, so that the gradients of weights and scales are sums in
 // registers over its rows; workgroups' sums are added in order by a second
 // small kernel.
+//
+// Measured: residual norm backward, 16384 x 2048, bf16 with fp32 stream (604 MB):
+// 115 us and 7 for the second kernel; gated norm forward, 32768 x 5120 in groups of
+// 128, bf16 (1.0 GB): 213 us; gated norm backward, 4099 x 5120 fp32 (420 MB): 82 us
+// and 6; 5.3, 4.7 and 5.1 TB/s, a large copy 5.0.  One row of 5120: 4 us, latency.
 #include "block_kernels.hpp"
 #include "device_common.hpp"
 

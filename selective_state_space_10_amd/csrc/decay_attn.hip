@@ -95,7 +95,9 @@ Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es) {
 // where S and R are the states that both directions carry over it: what crosses
 // t is the products of pairs around t.  (The dot products leave out pairs with
 // no decay between, decay_attn.hpp.)  Edges bound the length over which rounding
-// adds up.  One workgroup per edge; the running sum is fp64.
+// adds up.  One workgroup per edge; the running sum is fp64.  A few MB and chains
+// of dependent sums: latency (8 us for 8 x 2048 steps of 16 heads, 1024 workgroups;
+// 2% of the backward).
 struct DaDecayGrad {
   const float *dots_q, *dots_k;   // (slices, BH, L)
   const float *edge_dot;          // (parts, BH, nblock)
@@ -154,7 +156,9 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DaDecayGrad a) {
 }
 
 // The states before every segment from the end states of the ones before it
-// (in place): one thread per 4 elements, in the order of the recurrence.
+// (in place): one thread per 4 elements, in the order of the recurrence, 8
+// segments' loads under way (7 us for 12 segments of 64 heads of 64 x 64 in two
+// roles, of which the bytes are 8 MB in, 18 out: latency of the chain).
 __global__ void __launch_bounds__(256) combine_kernel(DaArgs a, int da_padded, int cols) {
   const DaRole &R = a.role[blockIdx.y];
   const int64_t tile4 = (int64_t)da_padded * cols / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -206,7 +210,8 @@ __global__ void __launch_bounds__(64) decay_grad_heads_kernel(const float *sums,
 }
 
 // Gradients of shared heads, dq (blockIdx.y 0) and dk: (rows, G, share, d) fp32
-// -> (rows, G, d), summed in order.
+// -> (rows, G, d), summed in order.  Bound by HBM and caches (57 MB in 9 us at 3074
+// rows, 4 x 8 heads of 64).
 template <typename T>
 __global__ void __launch_bounds__(256) shared_heads_kernel(const float *part, const float *part2, int64_t n4, int d4, int share, T *out, T *out2) {
   if (blockIdx.y) part = part2, out = out2;

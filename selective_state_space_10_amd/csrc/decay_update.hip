@@ -1,7 +1,9 @@
 // decay_update.hip -- one token of the decay attention: S <- exp(g) S + k v^T,
 // o = scale S^T q, with S (B, H, dk, dv) fp32 updated in place.  The state is
 // streamed once in and once out with 16-byte accesses and everything else is
-// small, so the kernel is bound by HBM.
+// small, so the kernel is bound by HBM: 256 requests of 40 heads of 128 x 128
+// (1.35 GB) take 264 us, 5.1 TB/s, where a large copy reaches 5.0; one request
+// of 16 heads takes 7 us, which is latency.
 //
 // Mapping: a workgroup owns a slab of columns of one (batch row, head); LPR
 // lanes cover a row of the slab, 4 columns each, and the other lanes and the
