@@ -94,8 +94,13 @@ Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es) {
 //   dg_t = sum_{r >= t up to the next edge} (q_r . dq_r - k_r . dk_r) + <exp(g) S, R> at that edge,
 // where S and R are the states that both directions carry over it: what crosses
 // t is the products of pairs around t.  (The dot products leave out pairs with
-// no decay between, decay_attn.hpp.)  Edges bound the length over which rounding
-// adds up.  One workgroup per edge; the running sum is fp64.  A few MB and chains
+// no decay between, decay_attn.hpp.)  The edge before t gives it as well,
+//   dg_t = <exp(g) S, R> there - sum_{r < t from there on} (q_r . dq_r - k_r . dk_r),
+// and the two are averaged with weights linear in t: the rounding of the dot
+// products, which adds up with the distance from an edge, is then zero at both
+// ends of a block, and in a sum over its steps a dot product counts at most half
+// the block (from one edge: all of it).
+// One workgroup per block between edges; the running sum is fp64.  A few MB and chains
 // of dependent sums: latency (8 us for 8 x 2048 steps of 16 heads, 1024 workgroups;
 // 2% of the backward).
 struct DaDecayGrad {
@@ -103,7 +108,7 @@ struct DaDecayGrad {
   const float *edge_dot;          // (parts, BH, nblock)
   const float *g;
   int64_t g_b, g_t, L;
-  int H, BH, nblock, edge_len, last_edge, slices, parts;
+  int H, BH, nblock, edge_len, last_edge, state0, slices, parts;
   float *out;       // (B, L, H), or NULL
   float *sums;      // (BH, nblock) sums over the steps before an edge, or NULL
 };
@@ -116,27 +121,47 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DaDecayGrad a) {
   const int64_t b = bh / a.H;
   const int64_t t0 = (int64_t)blk * a.edge_len, t1 = min(a.L, t0 + a.edge_len);
   const float *pg = a.g + b * a.g_b + h;
-  double carry = 0.0;
-  if (blk + 1 < a.nblock || a.last_edge) {
-    for (int p = 0; p < a.parts; ++p) carry += a.edge_dot[((int64_t)p * a.BH + bh) * a.nblock + blk];
-    if (t1 < a.L) carry *= fast_exp2(decay_log2(pg[t1 * a.g_t]));
+  // at the edge before step t (i its number; L: after the last step)
+  auto at_edge = [&](int i, int64_t t) {
+    double v = 0.0;
+    for (int p = 0; p < a.parts; ++p) v += a.edge_dot[((int64_t)p * a.BH + bh) * a.nblock + i];
+    return t < a.L ? v * fast_exp2(decay_log2(pg[t * a.g_t])) : v;
+  };
+  auto dots = [&](int64_t t) {
+    double v = 0.0;
+    for (int p = 0; p < a.slices; ++p) {
+      const int64_t o = ((int64_t)p * a.BH + bh) * a.L + t;
+      v += (double)a.dots_q[o] - (double)a.dots_k[o];
+    }
+    return v;
+  };
+  double carry = blk + 1 < a.nblock || a.last_edge ? at_edge(blk, t1) : 0.0;
+  // what the edge before the block gives more than the one after it: 0 but for
+  // rounding, and not known at a given first state
+  double more = 0.0;
+  if (blk > 0 || !a.state0) {
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += 256) more -= dots(t);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) more += __shfl_xor(more, d, 64);
+    if (lane == 0) wsum[w] = more;
+    __syncthreads();
+    more = wsum[0] + wsum[1] + wsum[2] + wsum[3] - carry;
+    if (blk > 0) more += at_edge(blk - 1, t0);
+    if (!(fabs(more) < INFINITY)) more = 0.0;  // a NaN or an infinity before a step is no reason for one at it
+    __syncthreads();
   }
+  const double slope = more / (double)(t1 - t0);
   double total = 0.0;
   // from the last step to the first, 256 at a time
   for (int64_t hi = t1; hi > t0; hi -= 256) {
     const int64_t t = hi - 1 - threadIdx.x;
-    double v = 0.0;
-    if (t >= t0)
-      for (int p = 0; p < a.slices; ++p) {
-        const int64_t o = ((int64_t)p * a.BH + bh) * a.L + t;
-        v += (double)a.dots_q[o] - (double)a.dots_k[o];
-      }
+    double v = t >= t0 ? dots(t) : 0.0;
     v = wave_sum_scan(v);
     __syncthreads();
     if (lane == 63) wsum[w] = v;
     __syncthreads();
     for (int i = 0; i < w; ++i) v += wsum[i];
-    v += carry;
+    v += carry + (t1 - t) * slope;
     carry += wsum[0] + wsum[1] + wsum[2] + wsum[3];
     if (t >= t0) {
       // a cleared state passes nothing on (what the sums leave there is rounding)
@@ -277,11 +302,13 @@ DaArgs fwd_args(const DecayAttnArgs &a, int io_dtype, Carve &c) {
 
 // Steps between two edges: the shortest power of two for which writing and
 // reading the states there (8 bytes per element) stays within an eighth of the
-// bytes that the three passes read and write per step (8 rows of each kind).
-int edge_len_of(const DecayAttnArgs &a, int es) {
+// bytes that the three passes read and write per step (8 rows of each kind), or a
+// quarter for decays by head: in their gradient's sum over the steps a rounding
+// counts as often as there are steps to its edge.
+int edge_len_of(const DecayAttnArgs &a, int es, bool heads) {
   const int64_t state = 8 * padded(a.dv) * cols_of(a.dk) * slices_of(a.dk), step = es * (a.dk + a.dv);
   int e = 64;
-  while (e < 1024 && state > (int64_t)e * step) e *= 2;
+  while (e < 1024 && state > (int64_t)e * step * (heads ? 2 : 1)) e *= 2;
   return e;
 }
 
@@ -293,7 +320,7 @@ struct BwdSet {
 
 BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
   BwdSet r{};
-  const int edge_len = edge_len_of(a, io_dtype == 0 ? 4 : 2);
+  const int edge_len = edge_len_of(a, io_dtype == 0 ? 4 : 2, a.g_t == 0);
   r.want_g = want_g;
   const Split sp = split_of(a.L, a.B * a.H, a.dv, a.dk, io_dtype == 0 ? 4 : 2);
   r.q = r.k = base_args(a, a.dv, a.dk, sp, kCombineBwd), r.v = base_args(a, a.dk, a.dv, sp, kCombineBwd);
@@ -316,13 +343,14 @@ BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
   if (want_g) {
     const int64_t n = a.B * a.H * a.L * r.q.nslice;
     q.dots = c.take<float>(n), k.dots = c.take<float>(n);
-    // an edge after the last step is there whether dstate_final is given or not: the size goes by the shape
     const int inner = (int)((a.L - 1) / edge_len);
+    // the size goes by the shape: an edge after the last step whether dstate_final is given or not, as many as decays by head have
+    const int64_t room = (a.L - 1) / edge_len_of(a, io_dtype == 0 ? 4 : 2, true) + 1;
     r.q.edge_shift = r.k.edge_shift = __builtin_ctz(edge_len);
     r.q.nedge = r.k.nedge = inner + 1, r.q.last_edge = r.k.last_edge = a.dstate_final != nullptr;
-    q.edge = k.edge = c.take<float>(a.B * a.H * (inner + 1) * edge_size(a.dv, a.dk));
-    q.edge_dot = c.take<float>(a.B * a.H * (inner + 1) * r.q.nslice * da_waves(a.dk));
-    r.sums = c.take<float>(a.B * a.H * (inner + 1));
+    q.edge = k.edge = c.take<float>(a.B * a.H * room * edge_size(a.dv, a.dk));
+    q.edge_dot = c.take<float>(a.B * a.H * room * r.q.nslice * da_waves(a.dk));
+    r.sums = c.take<float>(a.B * a.H * room);
   }
   return r;
 }
@@ -364,7 +392,7 @@ hipError_t launch_decay_attn_bwd(const DecayAttnArgs &a, int io_dtype, hipStream
     d.dots_q = r.q.role[0].dots, d.dots_k = r.k.role[0].dots, d.edge_dot = r.q.role[0].edge_dot;
     d.g = a.g, d.g_b = a.g_b, d.g_t = a.g_t, d.L = a.L;
     d.H = (int)a.H, d.BH = (int)(a.B * a.H), d.edge_len = 1 << r.q.edge_shift;
-    d.nblock = r.q.nedge, d.last_edge = r.q.last_edge;
+    d.nblock = r.q.nedge, d.last_edge = r.q.last_edge, d.state0 = a.state0 != nullptr;
     d.slices = r.q.nslice, d.parts = r.q.nslice * da_waves(a.dk);
     const bool heads = a.g_t == 0;
     d.out = heads ? nullptr : a.dlog_decay, d.sums = heads ? r.sums : nullptr;
