@@ -101,7 +101,7 @@ Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es) {
 // ends of a block, and in a sum over its steps a dot product counts at most half
 // the block (from one edge: all of it).
 // One workgroup per block between edges; the running sum is fp64.  A few MB and chains
-// of dependent sums: latency (8 us for 8 x 2048 steps of 16 heads, 1024 workgroups;
+// of dependent sums: latency (9 us for 8 x 2048 steps of 16 heads, 1024 workgroups;
 // 2% of the backward).
 struct DaDecayGrad {
   const float *dots_q, *dots_k;   // (slices, BH, L)
