@@ -352,8 +352,13 @@ __device__ __forceinline__ double wave_sum_scan(double v) {
   return dpp_add<0x143, 0xC>(v);
 }
 
-template <typename T, int DA, int NW, int NC, int NP, bool STATE_ONLY>
+template <typename T, int DA, int NW, int NC, bool STATE_ONLY>
 struct __attribute__((aligned(16))) DaLds {
+  // Pieces of the products inside a chunk: all of fp32, for bf16 inputs too.  (Two
+  // of them and of the state round one bf16 result in 500 the other way, and sums
+  // that cancel lose 16 bits' worth; 8 x 2048 steps of 16 heads of 128: 117 us
+  // against 124.)
+  static constexpr int NP = 3;
   static constexpr int C = Store<T>::kChunk, NX = Store<T>::NX, TV = NW * NC * 16;
   static constexpr int SA = DA + kPad, SC = TV + kPad;  // rows of a and b, of c
   // Products of steps, only blocks of 32 x 32 up to the diagonal: two row tiles of
@@ -375,9 +380,8 @@ struct __attribute__((aligned(16))) DaLds {
 };
 
 // T: storage type; DA: da rounded up; NW waves of NC tiles of 16 columns of dc
-// each; NP, NS: pieces of the products inside a chunk and of the state where
-// they are operands.  STATE_ONLY: the end state of a segment from zero (a
-// split sequence's first pass).  DOTS: out . e wanted.
+// each.  STATE_ONLY: the end state of a segment from zero (a split sequence's
+// first pass).  DOTS: out . e wanted.
 //
 // What bounds it is the vector ALU's issue (decays onto products, the state and
 // c, and their pieces), not HBM or the matrix instructions: at 8 x 2048 steps of
@@ -390,14 +394,14 @@ struct __attribute__((aligned(16))) DaLds {
 // read a and b, 167 us against 126.  Chunks are as long as LDS holds for two
 // workgroups per CU (fp32, 128 wide: one): longer ones have more products inside,
 // shorter ones more updates of the state.
-template <typename T, int DA, int NW, int NC, int NP, int NS, bool DOTS, bool STATE_ONLY>
+template <typename T, int DA, int NW, int NC, bool DOTS, bool STATE_ONLY>
 __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_attn_kernel(DaArgs args) {
   typedef Store<T> M;
-  typedef DaLds<T, DA, NW, NC, NP, STATE_ONLY> Lds;
+  typedef DaLds<T, DA, NW, NC, STATE_ONLY> Lds;
   constexpr int C = M::kChunk, NX = M::NX, CT = C / 16, DT = DA / 16, NT = NW * 64, TV = Lds::TV;
   constexpr int SA = Lds::SA, SC = Lds::SC, PLANE = Lds::PLANE, PA = C * SA, PC = C * SC;  // rows, planes
   constexpr int ES = sizeof(T);
-  constexpr int NB = 3;  // pieces of decayed rows into the state: all of fp32
+  constexpr int NP = Lds::NP, NS = 3, NB = 3;  // pieces of products inside a chunk, of the state, of decayed rows into it: all of fp32
   __shared__ Lds lds;
 
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l15 = lane & 15, lg = lane >> 4;
@@ -865,22 +869,18 @@ hipError_t launch_decay_attn_bf16(const DaArgs &a, int da_padded, bool dots, boo
 // Waves per workgroup, of 16 columns of dc each.
 inline int da_waves(int64_t dc) { return dc > 64 ? 8 : 4; }
 
-template <typename T, int DA, int NW, int NP, int NS, bool DOTS, bool STATE_ONLY>
+template <typename T, int DA, int NW, bool DOTS, bool STATE_ONLY>
 hipError_t launch_da(const DaArgs &a, hipStream_t s) {
   const int64_t items = (int64_t)a.nslice * a.nroles * (STATE_ONLY ? a.nseg - 1 : a.nseg) * a.BH;
   if (items > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((decay_attn_kernel<T, DA, NW, 1, NP, NS, DOTS, STATE_ONLY>), dim3((unsigned)items), dim3(NW * 64), 0, s, a);
+  hipLaunchKernelGGL((decay_attn_kernel<T, DA, NW, 1, DOTS, STATE_ONLY>), dim3((unsigned)items), dim3(NW * 64), 0, s, a);
   return hipGetLastError();
 }
 
 template <typename T, int DA, int NW>
 hipError_t launch_da_mode(const DaArgs &a, bool dots, bool state_only, hipStream_t s) {
-  if (state_only) return launch_da<T, DA, NW, 2, 2, false, true>(a, s);
-  if (dots) return launch_da<T, DA, NW, 3, 3, true, false>(a, s);
-  // To a bf16 output, one piece of the in-chunk products would leave an error
-  // of 1.4 roundings instead of one; two pieces of both operands leave one.
-  constexpr int N = sizeof(T) == 2 ? 2 : 3;
-  return launch_da<T, DA, NW, N, N, false, false>(a, s);
+  if (state_only) return launch_da<T, DA, NW, false, true>(a, s);
+  return dots ? launch_da<T, DA, NW, true, false>(a, s) : launch_da<T, DA, NW, false, false>(a, s);
 }
 
 template <typename T, int DA>
