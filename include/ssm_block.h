@@ -63,7 +63,8 @@ typedef struct ssm_view4 {
  *
  * Sizes: batch, seqlen >= 1; 1 <= heads <= 65536; batch * heads <= 2^26; dk, dv
  * multiples of 8 from 8 to 256; heads * dk, heads * dv and step strides <= 2^23.
- * A NaN or an infinity at one step reaches no earlier step.
+ * A NaN or an infinity at one step reaches no earlier step.  fp32 values and
+ * states of 3.396e38 and more, half a step of bf16 below 2^128, count as infinite.
  */
 int64_t ssm_decay_attn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
                                            int64_t key_heads, int64_t dk, int64_t dv, int io_dtype);

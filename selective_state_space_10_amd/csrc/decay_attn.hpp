@@ -86,10 +86,13 @@ struct DaArgs {
 //   bf16 column, side by side, the same          16.1     8.1
 //
 // Matrices in LDS are bf16.  Values of fp32 (inputs of that type, the state,
-// products of steps, decayed rows) are sums of bf16 pieces: three hold all 24
-// bits, each taking the next 8, and of the products of two such operands the
-// six largest are formed (the others are below 2^-24), at 6 / 16 of the time of
-// the fp32 matrix instructions.
+// products of steps, decayed rows) are sums of three bf16 pieces that hold all 24
+// bits: each is what is left, rounded to nearest, so that the second is at most
+// 2^-8 of the value's power of two and the third 2^-17.  Of the products of two
+// such operands the six largest are formed, at 6 / 16 of the time of the fp32
+// matrix instructions.  The other three add up to at most 2^-24 of the operands'
+// powers of two, of either sign: a rounding of fp32.  (Pieces that are cut off
+// leave up to 2^-21, always towards zero, which adds up over like-signed sums.)
 template <int N>
 struct Pieces {
   uint4 p[N];
@@ -176,18 +179,18 @@ __device__ __forceinline__ void floats(const Pieces<N> &f, float (&x)[8]) {
 __device__ __forceinline__ uint32_t pack_rne(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
-// Two fp32 values as N pieces, cut off after each 8 bits (three hold all of
-// them, two leave a relative error below 2^-15).
+// Two fp32 values as N pieces, each rounded to nearest.
 template <int N>
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&o)[N]) {
-  static_assert(N >= 2, "one piece would be rounded");
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    o[i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-    a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
-    b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+    o[i] = pack_rne(a, b);
+    a -= __uint_as_float(o[i] << 16);
+    b -= __uint_as_float(o[i] & 0xffff0000u);
   }
 }
+// From here on a value's first piece is infinite.
+constexpr float kRoundsToInf = 0x1.ffp127f;
 template <int N>
 __device__ __forceinline__ Pieces<N> split(const float (&x)[8]) {
   uint32_t w[4][N];
@@ -265,7 +268,8 @@ struct Store<float> {
   static __device__ __forceinline__ void put_row(bf16 *row, int plane, int k, uint4 v) { put_inorder(row + pos(k) - k, plane, k, v); }
   static __device__ __forceinline__ void store4(void *p, f32x4 v) { *(f32x4 *)p = v; }
   static __device__ __forceinline__ uint32_t nonfinite(uint4 v) {
-    constexpr uint32_t m = 0x7f800000u, one = 0x00800000u;
+    // (values that round to it count as infinite)
+    constexpr uint32_t m = 0x7fffffffu, one = 0x80000000u - 0x7f7f8000u;
     return (((v.x & m) + one) | ((v.y & m) + one) | ((v.z & m) + one) | ((v.w & m) + one)) & 0x80000000u;
   }
   static __device__ __forceinline__ float element(uint4 v, int j) { return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w); }
@@ -308,7 +312,7 @@ struct TileRegs {
       if (CHECK && Store<T>::nonfinite(v)) {
         *any = 1;
         for (int j = 0; j < EPP; ++j)
-          if (!(fabsf(Store<T>::element(v, j)) < INFINITY)) atomicMin(first + col + j, lr);
+          if (!(fabsf(Store<T>::element(v, j)) < kRoundsToInf)) atomicMin(first + col + j, lr);
       }
     };
     if (rows == ROWS && cols == COLS && N * NT == ROWS * PPR) {  // the same for all lanes

@@ -2,7 +2,12 @@
 
 Exact sums: every operand is a bf16 value or a sum of powers of two 2^0 .. 2^-20,
 and so is every partial sum (at most 22 bits), so fp32 arithmetic gives 2^-20
-where operands that were cut to two bf16 pieces (16 bits) give 0 or 2^-12."""
+where operands that were cut to two bf16 pieces (16 bits) give 0 or 2^-12.
+
+Like-signed sums: errors that all point one way add up.  Units of 2^-24 of the
+result: a product of operands in three bf16 pieces rounded to nearest leaves out
+at most 1, its sum is rounded last to 1 (2 if cut off), the multiplication by a
+decay rounds to 1."""
 from __future__ import annotations
 
 import pytest
@@ -87,6 +92,41 @@ def test_gradients_keep_their_bits(ssm, dtype, want_dlog_decay, dk, dv):
     assert (r["dv"][0, 1] == TINY).all()
 
 
+def _one_signed(heads):
+    """A value per head: mantissas whose lower bits are all set behind an 8-bit piece, and random ones."""
+    x = 1 + torch.rand(heads, generator=torch.Generator().manual_seed(1))
+    x[0], x[1], x[2] = 1 + 2.0 ** -7 - 2.0 ** -23, 2 - 2.0 ** -23, 1 + 2.0 ** -8 - 2.0 ** -23
+    x[3], x[4], x[5] = 1 + 2.0 ** -8 + 2.0 ** -17, 1 + 2.0 ** -8 + 2.0 ** -16 - 2.0 ** -23, 1 + 2.0 ** -7 + 2.0 ** -15 - 2.0 ** -23
+    return x
+
+
+def _units(got, want):
+    return float(((got.double().cpu() - want).abs() / want.abs()).max() * 2 ** 24)
+
+
+def test_like_signed_products_fp32(ssm):
+    """One step, one value per head: o = 32 x^3 (two products of full operands, the
+    weight rounded between: 1 + 2 + 1 + 1 + 2 units, and 1 to spare), the last state
+    x^2 (1 + 2, and 1 to spare)."""
+    H = 256
+    x = _one_signed(H)
+    full = lambda d: x[None, None, :, None].expand(1, 1, H, d).contiguous().cuda()  # noqa: E731
+    o, state = ssm.decay_attn_fwd(full(32), full(32), full(16), torch.zeros(1, 1, H, device="cuda"), 1.0, return_final_state=True)
+    x = x.double()
+    assert _units(o, 32 * x[None, None, :, None] ** 3) <= 8
+    assert _units(state, x[None, :, None, None] ** 2) <= 4
+
+
+def test_like_signed_state_products_fp32(ssm):
+    """o = 32 x^2 from the state alone (1 + 2 units, the decay's 1 and 1 to spare)."""
+    H = 256
+    x = _one_signed(H)
+    q = x[None, None, :, None].expand(1, 1, H, 32).contiguous().cuda()
+    state = x[None, :, None, None].expand(1, H, 32, 16).contiguous().cuda()
+    o, _ = ssm.decay_attn_fwd(q, torch.zeros_like(q), q[..., :16].contiguous(), torch.zeros(1, 1, H, device="cuda"), 1.0, state)
+    assert _units(o, 32 * x.double()[None, None, :, None] ** 2) <= 5
+
+
 @pytest.mark.parametrize("H,G", [(4, 4), (6, 2)])
 def test_results_in_bf16_are_the_rounded_fp32_results(ssm, H, G):
     """A result whose fp32 error is e is rounded the other way where it lies within
@@ -105,3 +145,14 @@ def test_results_in_bf16_are_the_rounded_fp32_results(ssm, H, G):
         share = float((t.cpu() != w)[usual].double().mean())
         print(n, share, flush=True)
         assert share <= 2.0 ** -11, (n, share)
+
+
+@pytest.mark.parametrize("value", [3.3961e38, 3.4e38])
+def test_the_largest_values_reach_no_earlier_step(ssm, value):
+    """fp32 values next to 2^128, whose first piece is the largest bf16 value or infinite."""
+    p = ref.attn_inputs(1, 100, 2, 2, 32, 32, seed=6)
+    want, _ = ref.attn_fwd(p, 32 ** -0.5)
+    p["v"][:, 70] = value
+    d = {n: t.cuda() for n, t in p.items()}
+    o, _ = ssm.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], None, d["state0"])
+    assert ref.error(o[:, :70], want[:, :70]) <= 1e-5
