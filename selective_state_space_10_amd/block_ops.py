@@ -7,6 +7,7 @@ workspaces, and the call on the current stream; nothing here computes.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .ops import _IO, _io_code, _need, _ptr, _stream
@@ -347,6 +348,7 @@ class DecayAttentionFn(torch.autograd.Function):
         return o, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dfinal):
         q, k, v, log_decay, state0 = ctx.saved_tensors
         do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None else do.contiguous()
@@ -374,6 +376,7 @@ class ResidualNormFn(torch.autograd.Function):
         return y, h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         x, h, rstd, weight, scale = ctx.saved_tensors
         shape, dtype, dev = ctx.x_like
@@ -398,6 +401,7 @@ class GatedNormFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, z, weight, rstd = ctx.saved_tensors
         g = gated_norm_bwd(dy.contiguous(), x, z, weight, rstd, ctx.group, ctx.gate_first)
