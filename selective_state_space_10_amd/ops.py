@@ -7,6 +7,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -325,6 +326,7 @@ class SelectiveScanFn(torch.autograd.Function):
         return y, hf
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dhf):
         u, delta, A, B, C, D, z, delta_bias, h0, cs = ctx.saved_tensors
         g = scan_bwd(u, delta, A, B, C, D, z, delta_bias, ctx.delta_softplus, h0, cs,
@@ -366,6 +368,7 @@ class ConvScanFn(torch.autograd.Function):
         return y, hf
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dhf):
         x, conv_w, conv_b, delta, A, B, C, D, z, delta_bias, h0, cs = ctx.saved_tensors
         g = scan_bwd_conv(x, conv_w, conv_b, delta, A, B, C, D, z, delta_bias, ctx.delta_softplus,
