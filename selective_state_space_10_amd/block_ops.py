@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from .ops import _IO, _io_code, _need, _ptr, _stream
@@ -193,6 +194,7 @@ def decay_attn_update(state, q, k, v, log_decay, scale=None):
           log_decay.data_ptr(), per_token,
           dk ** -0.5 if scale is None else scale,
           o.data_ptr())
+    increment_version(state)  # a backward that saved it must not read it
     return o
 
 
