@@ -8,6 +8,7 @@ from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import _lib
 
@@ -138,6 +139,8 @@ def scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=
                                  int(bool(delta_softplus)), _ptr(h0), _ptr(hf), _ptr(y), _ptr(cs),
                                  _ptr(ws), wsb, _stream(dev), flags)
     _lib.check(st)
+    if out is not None:
+        increment_version(out)
     return y, hf, cs
 
 
@@ -215,6 +218,8 @@ def scan_fwd_conv(x, conv_w, conv_b, delta, A, B, C, D=None, z=None, delta_bias=
                                    _ptr(delta_bias), int(bool(delta_softplus)), _ptr(h0), _ptr(hf),
                                    _ptr(y), _ptr(cs), _ptr(ws), wsb, _stream(dev), flags)
     _lib.check(st)
+    if out is not None:
+        increment_version(out)
     return y, hf, cs
 
 
@@ -285,6 +290,7 @@ def state_update(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, delt
                                      int(bool(delta_softplus)), _ptr(y), _stream(dev),
                                      _lib.FLAG_ZOH if zoh else 0)
     _lib.check(st)
+    increment_version(state)  # a backward that saved it must not read it
     return y
 
 
