@@ -56,7 +56,9 @@ typedef struct ssm_view4 {
  *   log_decay: g, fp32, contiguous: (batch, seqlen, heads) if decay_per_token,
  *              else (heads).  g = -inf (any g below -177, where exp(g) is zero
  *              in fp32 many times over) clears the state: packed documents.
- *              g > 0 grows the state and is not refused.
+ *              g > 0 grows the state and is not refused; the decays of several
+ *              steps together may exceed fp32's range where states, outputs and
+ *              gradients do not.
  *   state0:    (batch, heads, dk, dv) fp32 or NULL
  *   state_final: the same shape, NULL = not wanted
  *   o:         (batch, seqlen, heads, dv) contiguous, io_dtype

@@ -121,11 +121,10 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DaDecayGrad a) {
   const int64_t b = bh / a.H;
   const int64_t t0 = (int64_t)blk * a.edge_len, t1 = min(a.L, t0 + a.edge_len);
   const float *pg = a.g + b * a.g_b + h;
-  // at the edge before step t (i its number; L: after the last step)
-  auto at_edge = [&](int i, int64_t t) {
+  auto at_edge = [&](int i) {
     double v = 0.0;
     for (int p = 0; p < a.parts; ++p) v += a.edge_dot[((int64_t)p * a.BH + bh) * a.nblock + i];
-    return t < a.L ? v * fast_exp2(decay_log2(pg[t * a.g_t])) : v;
+    return v;
   };
   auto dots = [&](int64_t t) {
     double v = 0.0;
@@ -135,7 +134,7 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DaDecayGrad a) {
     }
     return v;
   };
-  double carry = blk + 1 < a.nblock || a.last_edge ? at_edge(blk, t1) : 0.0;
+  double carry = blk + 1 < a.nblock || a.last_edge ? at_edge(blk) : 0.0;
   // what the edge before the block gives more than the one after it: 0 but for
   // rounding, and not known at a given first state
   double more = 0.0;
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DaDecayGrad a) {
     if (lane == 0) wsum[w] = more;
     __syncthreads();
     more = wsum[0] + wsum[1] + wsum[2] + wsum[3] - carry;
-    if (blk > 0) more += at_edge(blk - 1, t0);
+    if (blk > 0) more += at_edge(blk - 1);
     if (!(fabs(more) < INFINITY)) more = 0.0;  // a NaN or an infinity before a step is no reason for one at it
     __syncthreads();
   }
@@ -200,27 +199,27 @@ __global__ void __launch_bounds__(256) combine_kernel(DaArgs a, int da_padded, i
   }
   const int64_t step = tile4 * a.nslice;
   f32x4 *p = (f32x4 *)R.loc + bh * a.nseg * step + x;
-  const float *tot = R.tot + bh * a.nseg;
+  const float2 *tot = R.tot + bh * a.nseg;
   const int first = R.reverse ? a.nseg - 1 : 0, dir = R.reverse ? -1 : 1;
   int j = 0;
   constexpr int U = 8;  // loads under way
   for (; j + U < a.nseg; j += U) {
     f32x4 l[U];
-    float e[U];
+    float2 e[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) l[u] = p[(first + dir * (j + u)) * step], e[u] = tot[first + dir * (j + u)];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       p[(first + dir * (j + u)) * step] = cur;
-      cur = cur * e[u] + l[u];
+      cur = cur * e[u].x * e[u].y + l[u];
     }
   }
   for (; j < a.nseg; ++j) {
     f32x4 l = cur;
-    float e = 0.0f;
+    float2 e = make_float2(0.0f, 0.0f);
     if (j + 1 < a.nseg) l = p[(first + dir * j) * step], e = tot[first + dir * j];
     p[(first + dir * j) * step] = cur;
-    cur = cur * e + l;
+    cur = cur * e.x * e.y + l;
   }
 }
 
@@ -286,7 +285,7 @@ int64_t edge_size(int64_t da, int64_t dc) { return padded(da) * cols_of(dc) * sl
 void take_segments(Carve &c, DaRole &r, const DaArgs &a) {
   if (a.nseg == 1) return;
   r.loc = c.take<float>((int64_t)a.BH * a.nseg * edge_size(a.da, a.dc));
-  r.tot = c.take<float>((int64_t)a.BH * a.nseg);
+  r.tot = c.take<float2>((int64_t)a.BH * a.nseg);
 }
 
 DaArgs fwd_args(const DecayAttnArgs &a, int io_dtype, Carve &c) {

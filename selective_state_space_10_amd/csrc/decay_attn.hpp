@@ -12,8 +12,11 @@
 //   out_t = exp(G_t) S^T a_t + sum_{s<=t} exp(G_t - G_s) (a_t . b_s) c_s,
 //   S    <- exp(G_last) S + sum_s b_s (exp(G_last - G_s) c_s)^T,
 // which are four matrix products.  Every exponent is a sum of decays over a
-// range of steps, so nothing overflows where the recurrence does not; G is
-// summed in 64 bits and kept as a pair of floats, so that differences of
+// range of steps, so that nothing overflows where decays are at most one.  Where
+// they grow, a factor of many steps may leave fp32's range although the states
+// do not, being zero or small: there outputs and state are formed 2^-shift times
+// as large, with factors of about half the exponent, and scaled at the end.  G
+// is summed in 64 bits and kept as a pair of floats, so that differences of
 // nearby steps stay exact to fp32 after steps of very strong decay.
 #pragma once
 
@@ -35,6 +38,14 @@ __device__ __forceinline__ float decay_log2(float g) {
   return g < kMinLog2Decay * kLn2 ? kMinLog2Decay : g * kLog2e;  // NaN passes
 }
 
+// 2^x in two factors, each in fp32's range for |x| up to 240 (beyond, what
+// they multiply is zero or out of range itself).
+__device__ __forceinline__ float2 exp2_in_two(double x) {
+  const double n = rint(x);
+  const int k = (int)fmin(fmax(n, -300.0), 240.0), k1 = k >> 1;
+  return make_float2(ldexpf(fast_exp2((float)(x - n)), k1), ldexpf(1.0f, k - k1));
+}
+
 // One direction and set of operands of the recurrence.
 struct DaRole {
   View4 a, b, c, e;      // e: what the outputs are dotted with (the decays' gradient)
@@ -46,10 +57,11 @@ struct DaRole {
   int state_in_t;
   float *state_out;      // (B, H, da, dc), NULL = not wanted
   float *dots;           // (slices, B * H, L) partial sums of out . e, or NULL
-  float *loc, *tot;      // segments: end states from zero (or, combined, the states before them), total decays
+  float *loc;            // segments: end states from zero (or, combined, the states before them),
+  float2 *tot;           // total decays, in two factors
   int loc_t, cols_t, nslice_t;  // loc is of a role with the transposed state, with slices of cols_t
   float *edge;           // states at edges (below), (B * H, edges, slices, tile), or NULL
-  float *edge_dot;       // forward in time: <S, R> at edges, (slices * waves, B * H, edges)
+  float *edge_dot;       // forward in time: <exp(g) S, R> at edges, (slices * waves, B * H, edges)
 };
 
 struct DaArgs {
@@ -335,8 +347,18 @@ struct __attribute__((aligned(16))) DaDecays {
   float gh[C], gl[C];  // G_t as a pair of floats
   float in[C];         // exp(G_t), of the state in a step's output
   float out[C];        // exp(G_last - G_s), of a step in the next chunk's state
-  float e[4];          // [0]: exp(G_last)
+  float shift[C];      // in a chunk that grows: powers of two that a step's output is formed too small by
+  float e[4];          // [0]: exp(G_last); [1]: not zero if the chunk grows, then [2]: 2^shift of the state
 };
+// A chunk can grow by 2^100 only if a step of it grows by more than this.
+template <int C>
+constexpr float kGrows = 100.0f / C;
+// A shift is half of the growth, at most kMostShift (what does not grow must stay
+// far from fp32's smallest numbers); factors are kept finite, so that zeros stay zero.
+constexpr float kMostShift = 100.0f, kMostPowers = 120.0f;
+// (NaN and infinities pass)
+__device__ __forceinline__ float in_range(float x) { return x > kMostPowers && x < 1e30f ? kMostPowers : x; }
+__device__ __forceinline__ float shift_of(float growth) { return growth < 1e30f ? fminf(rintf(0.5f * growth), kMostShift) : 0.0f; }
 
 // Sums over lanes 0 .. lane, by DPP moves within rows of 16 lanes and then
 // from row to row (as wave_affine_scan).
@@ -459,8 +481,10 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
 #pragma unroll
       for (int ct = 0; ct < NC; ++ct) *(f32x4 *)(o + (dt * NC + ct) * 256) = S[dt][ct];
   };
-  auto dot_edge = [&](int i) {
+  // exp(g) of the step after the edge comes to S first: <S, R> may be out of range where this is not
+  auto dot_edge = [&](int i, int64_t t) {
     const float *o = edge_tile(i);
+    const float2 e = exp2_in_two(t < args.L ? decay_log2(pg[t * args.g_t]) : 0.0f);
     f32x4 d = {0, 0, 0, 0};
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
@@ -468,7 +492,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
       for (int ct = 0; ct < NC; ++ct) {
         const f32x4 x = *(const f32x4 *)(o + (dt * NC + ct) * 256);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) d[r] = fmaf(S[dt][ct][r], x[r], d[r]);
+        for (int r = 0; r < 4; ++r) d[r] = fmaf(S[dt][ct][r] * e.x * e.y, x[r], d[r]);
       }
     float v = (d[0] + d[1]) + (d[2] + d[3]);
 #pragma unroll
@@ -495,19 +519,19 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
       // of row x (a step of this role's columns) and column y holds, for lane
       // (x % 16) / 4 * 16 + y % 16, element x % 4.
       const int cols_t = R.cols_t, tiles_t = (args.dc_t >> 4);
-      auto add = [&](int64_t j, float e) {
+      auto add = [&](int64_t j, float2 e) {
         const int x = wcol0 + l15;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) {
           const int y = dt * 16 + lg * 4, w_t = y % cols_t / 16;
           const float *p = R.loc + ((j * R.nslice_t + y / cols_t) * cols_t * args.dc_t) + (int64_t)(w_t * tiles_t + x / 16) * 256 + ((x % 16) / 4 * 16 + y % 16) * 4 + x % 4;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[dt][0][r] = S[dt][0][r] * e + (x < dc && y + r < da ? p[r * 4] : 0.0f);
+          for (int r = 0; r < 4; ++r) S[dt][0][r] = S[dt][0][r] * e.x * e.y + (x < dc && y + r < da ? p[r * 4] : 0.0f);
         }
       };
       const int before = rev ? args.nseg - 1 - seg : seg;
       if (args.combined) {
-        add((int64_t)bh * args.nseg + seg, 0.0f);
+        add((int64_t)bh * args.nseg + seg, make_float2(0.0f, 0.0f));
       } else {
         load_state_in();
         for (int i = 0; i < before; ++i) {
@@ -527,12 +551,12 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
       const int before = rev ? args.nseg - 1 - seg : seg;
       for (int i = 0; i < before; ++i) {
         const int64_t j = (int64_t)bh * args.nseg + (rev ? args.nseg - 1 - i : i);
-        const float e = R.tot[j];
+        const float2 e = R.tot[j];
         const float *loc = R.loc + (j * args.nslice + slice) * kTile + wtile;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-          for (int ct = 0; ct < NC; ++ct) S[dt][ct] = S[dt][ct] * e + *(const f32x4 *)(loc + (dt * NC + ct) * 256);
+          for (int ct = 0; ct < NC; ++ct) S[dt][ct] = S[dt][ct] * e.x * e.y + *(const f32x4 *)(loc + (dt * NC + ct) * 256);
       }
     }
     if (DOTS && rev && args.last_edge && seg == args.nseg - 1) store_edge(args.nedge - 1);
@@ -567,21 +591,38 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     have_g = i < nchunk && lane < rows && t < args.L;
     rg = pg[have_g ? t * args.g_t : 0];
   };
+  double total = 0.0;  // of all chunks, in the last wave
   auto put_decays = [&](int i, DaDecays<C> &d) {
-    const double G = wave_sum_scan(have_g ? decay_log2(rg) : 0.0f);
+    const float g2 = have_g ? decay_log2(rg) : 0.0f;
+    const bool grow = __ballot(g2 > kGrows<C>) != 0;
+    const double G = wave_sum_scan(g2);
     const uint64_t gb = __builtin_bit_cast(uint64_t, G);
     const double last = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(gb >> 32), 63) << 32 |
                                                        (uint32_t)__builtin_amdgcn_readlane((int)gb, 63));
     const float hi = (float)G;
     // the last edge's state leaves out the last step (see no_dot)
     const bool left_out = DOTS && args.last_edge && !rev && t0 + low_of(i) + lane == args.L - 1;
+    float in = hi, out = (float)(last - G), e = (float)last;
+    if (grow) {
+      float least = fminf(hi, 0.0f);  // of G up to this step
+#pragma unroll
+      for (int k = 1; k < 64; k *= 2) {
+        const float o = __shfl_up(least, k, 64);
+        if (lane >= k) least = fminf(least, o);
+      }
+      const float shift = shift_of(hi - least), state_shift = shift_of(e - __shfl(least, 63, 64));
+      in = in_range(in - shift), out = in_range(out - state_shift), e = in_range(e - state_shift);
+      if (lane < C) d.shift[lane] = shift;
+      if (lane == 0) d.e[2] = ldexpf(1.0f, (int)state_shift);
+    }
     if (lane < C) {
       d.gh[lane] = hi;
       d.gl[lane] = (float)(G - (double)hi);
-      d.in[lane] = fast_exp2(hi) * iscale;
-      d.out[lane] = left_out ? 0.0f : fast_exp2((float)(last - G)) * sscale;
+      d.in[lane] = fast_exp2(in) * iscale;
+      d.out[lane] = left_out ? 0.0f : fast_exp2(out) * sscale;
     }
-    if (lane == 0) d.e[0] = fast_exp2((float)last);
+    if (lane == 0) d.e[0] = fast_exp2(e), d.e[1] = grow ? 1.0f : 0.0f;
+    if (STATE_ONLY) total += last;
   };
   // a chunk's dot products, of all waves
   auto flush_dots = [&](int ci) {
@@ -599,14 +640,13 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     put_decays(0, lds.dec[0]);
     fetch_decays(1);
   }
-  float total = 1.0f;
   int par = 0;
 
   for (int ci = 0; ci < nchunk; ++ci, par ^= 1) {
     const int low = low_of(ci), rows = min(C, n - low);
     // the edge before this chunk's rows, -1 if there is none
     const int edge = DOTS && ((t0 + low) & ((1 << args.edge_shift) - 1)) == 0 ? (int)((t0 + low) >> args.edge_shift) - 1 : -1;
-    if (DOTS && !rev && edge >= 0) dot_edge(edge);
+    if (DOTS && !rev && edge >= 0) dot_edge(edge, t0 + low);
     __syncthreads();  // the last chunk's readers are done
     if constexpr (!STATE_ONLY) ra.template put<true, false>(lds.a, PA, SA, rows, da, rev);
     rb.template put<false, false>(lds.b, PA, SA, rows, da, rev);
@@ -615,7 +655,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     __syncthreads();
     const DaDecays<C> &dec = lds.dec[par];
     const float e = dec.e[0];
-    total *= e;
+    const bool grow = __builtin_amdgcn_readfirstlane(__float_as_int(dec.e[1])) != 0;
     if (w == NW - 1 && ci + 1 < nchunk) {
       put_decays(ci + 1, lds.dec[par ^ 1]);
       fetch_decays(ci + 2);
@@ -654,12 +694,19 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
         const int t = tt * 16 + l15, s = st * 16 + lg * 4;
         const float th = dec.gh[t], tl = dec.gl[t];
         const f32x4 sh = *(const f32x4 *)(dec.gh + s), sl = *(const f32x4 *)(dec.gl + s);
+        f32x4 d;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[r] = (th - sh[r]) + (tl - sl[r]);
+        if (grow) {
+          const float shift = dec.shift[t];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) d[r] = in_range(((th - shift) - sh[r]) + (tl - sl[r]));
+        }
         float p[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float d = fast_exp2((th - sh[r]) + (tl - sl[r]));
           // for the dot products a step's own term is kept apart (below)
-          p[r] = s + r < t + (DOTS ? 0 : 1) ? x[r] * (d * pscale) : 0.0f;
+          p[r] = s + r < t + (DOTS ? 0 : 1) ? x[r] * (fast_exp2(d[r]) * pscale) : 0.0f;
           if (DOTS && s + r == t) lds.diag[t] = x[r] * pscale;
         }
         put4<NP>(lds.p + Lds::prow(tt, l15) + swizzled(s, Lds::swizzle(tt, l15)), PLANE, p);
@@ -740,6 +787,16 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
               for (int ct = 0; ct < NC; ++ct)
                 acc[tt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cf[kk][ct].p[j]), __builtin_bit_cast(bf16x8, pf[tt].p[0]), acc[tt][ct], 0, 0, 0);
         }
+      if (grow) {
+#pragma unroll
+        for (int tt = 0; tt < CT; ++tt) {
+          const int shift = (int)dec.shift[tt * 16 + (lp & 15)];
+#pragma unroll
+          for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[tt][ct][r] = ldexpf(acc[tt][ct][r], shift);
+        }
+      }
       if (bad) {
 #pragma unroll
         for (int ct = 0; ct < NC; ++ct) {
@@ -832,6 +889,13 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
           mma_pieces<NX, NB, G>([&](int d) { return bf[d]; }, [&](int) { return xf[ct]; }, [&](int d) -> f32x4 & { return S[d0 + d][ct]; });
       }
     }
+    if (grow) {
+      const float f = dec.e[2];
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int ct = 0; ct < NC; ++ct) S[dt][ct] *= f;
+    }
     if (DOTS && rev && edge >= 0) store_edge(edge);
   }
   if constexpr (DOTS) {
@@ -846,9 +910,9 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
       for (int ct = 0; ct < NC; ++ct) *(f32x4 *)(loc + (dt * NC + ct) * 256) = S[dt][ct];
-    if (threadIdx.x == 0 && slice == 0) R.tot[j] = total;
+    if (w == NW - 1 && lane == 0 && slice == 0) R.tot[j] = exp2_in_two(total);
   } else if (seg == (rev ? 0 : args.nseg - 1)) {
-    if (DOTS && !rev && args.last_edge) dot_edge(args.nedge - 1);
+    if (DOTS && !rev && args.last_edge) dot_edge(args.nedge - 1, args.L);
     if (R.state_out) {
       const float e = rev ? fast_exp2(decay_log2(pg[0])) : 1.0f;  // the first step's own decay
       float *s = R.state_out + (int64_t)bh * da * dc;
