@@ -49,15 +49,17 @@ int check_attn(int64_t batch, int64_t seqlen, int64_t heads, int64_t key_heads, 
   return check_dtype(io_dtype);
 }
 
-int check_view(const char *name, const ssm_view4 *v, int io_dtype) {
+// one_step: stride_step is not used
+int check_view(const char *name, const ssm_view4 *v, int io_dtype, bool one_step = false) {
   if (v == nullptr || v->ptr == nullptr) return api_fail(SSM_ERR_NULL_ARG, "%s is NULL", name);
   const int64_t es = io_dtype == SSM_F32 ? 4 : 2;
-  const int64_t st[] = {v->stride_batch, v->stride_step, v->stride_head};
+  const int64_t step = one_step ? 0 : v->stride_step;
+  const int64_t st[] = {v->stride_batch, step, v->stride_head};
   for (int64_t s : st) {
     if (s < 0 || s > kMaxElems) return api_fail(SSM_ERR_BAD_SHAPE, "%s has stride %lld", name, (long long)s);
     if (s * es % 16 != 0) return api_fail(SSM_ERR_ALIGNMENT, "%s has stride %lld, not a multiple of 16 bytes", name, (long long)s);
   }
-  if (v->stride_step > kMaxStep) return api_fail(SSM_ERR_UNSUPPORTED, "%s has a step stride over 2^23 elements", name);
+  if (step > kMaxStep) return api_fail(SSM_ERR_UNSUPPORTED, "%s has a step stride over 2^23 elements", name);
   if (((uintptr_t)v->ptr & 15u) != 0) return api_fail(SSM_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
   return SSM_OK;
 }
@@ -200,9 +202,9 @@ int ssm_decay_attn_update(int64_t batch, int64_t heads, int64_t key_heads, int64
                           const float *log_decay, int decay_per_token, float scale, void *o, void *hip_stream) {
   ssm::api_clear_error();
   SSM_TRY(check_attn(batch, 1, heads, key_heads, dk, dv, io_dtype));
-  SSM_TRY(check_view("q", q, io_dtype));
-  SSM_TRY(check_view("k", k, io_dtype));
-  SSM_TRY(check_view("v", v, io_dtype));
+  SSM_TRY(check_view("q", q, io_dtype, true));
+  SSM_TRY(check_view("k", k, io_dtype, true));
+  SSM_TRY(check_view("v", v, io_dtype, true));
   const Ptr ps[] = {{"state", state, true, 16}, {"log_decay", log_decay, true, 4}, {"o", o, true, 16}};
   SSM_TRY_PTRS(ps);
   ssm::DecayUpdateArgs a{};
