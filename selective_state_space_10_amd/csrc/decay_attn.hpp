@@ -378,14 +378,14 @@ __device__ __forceinline__ double wave_sum_scan(double v) {
   return dpp_add<0x143, 0xC>(v);
 }
 
-template <typename T, int DA, int NW, int NC, bool STATE_ONLY>
+template <typename T, int DA, int NW, bool STATE_ONLY>
 struct __attribute__((aligned(16))) DaLds {
   // Pieces of the products inside a chunk: all of fp32, for bf16 inputs too.  (Two
   // of them and of the state round one bf16 result in 500 the other way, and sums
   // that cancel lose 16 bits' worth; 8 x 2048 steps of 16 heads of 128: 117 us
   // against 124.)
   static constexpr int NP = 3;
-  static constexpr int C = Store<T>::kChunk, NX = Store<T>::NX, TV = NW * NC * 16;
+  static constexpr int C = Store<T>::kChunk, NX = Store<T>::NX, TV = NW * 16;
   static constexpr int SA = DA + kPad, SC = TV + kPad;  // rows of a and b, of c
   // Products of steps, only blocks of 32 x 32 up to the diagonal: two row tiles of
   // 32 columns, then two of 64, without padding; instead the 16-byte units of a
@@ -405,8 +405,8 @@ struct __attribute__((aligned(16))) DaLds {
   int first[TV];   // and from which step on, by column (C: nowhere)
 };
 
-// T: storage type; DA: da rounded up; NW waves of NC tiles of 16 columns of dc
-// each.  STATE_ONLY: the end state of a segment from zero (a split sequence's
+// T: storage type; DA: da rounded up; NW waves of 16 columns of dc each.
+// STATE_ONLY: the end state of a segment from zero (a split sequence's
 // first pass).  DOTS: out . e wanted.
 //
 // What bounds it is the vector ALU's issue (decays onto products, the state and
@@ -420,10 +420,10 @@ struct __attribute__((aligned(16))) DaLds {
 // read a and b, 167 us against 126.  Chunks are as long as LDS holds for two
 // workgroups per CU (fp32, 128 wide: one): longer ones have more products inside,
 // shorter ones more updates of the state.
-template <typename T, int DA, int NW, int NC, bool DOTS, bool STATE_ONLY>
-__global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_attn_kernel(DaArgs args) {
+template <typename T, int DA, int NW, bool DOTS, bool STATE_ONLY>
+__global__ void __launch_bounds__(NW * 64, DA <= 128 ? 4 : 2) decay_attn_kernel(DaArgs args) {
   typedef Store<T> M;
-  typedef DaLds<T, DA, NW, NC, STATE_ONLY> Lds;
+  typedef DaLds<T, DA, NW, STATE_ONLY> Lds;
   constexpr int C = M::kChunk, NX = M::NX, CT = C / 16, DT = DA / 16, NT = NW * 64, TV = Lds::TV;
   constexpr int SA = Lds::SA, SC = Lds::SC, PLANE = Lds::PLANE, PA = C * SA, PC = C * SC;  // rows, planes
   constexpr int ES = sizeof(T);
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
   const int bh = item / segs;
   const int h = bh % args.H;
   const int64_t b = bh / args.H;
-  const int col0 = slice * TV, wcol0 = col0 + w * NC * 16;
+  const int col0 = slice * TV, wcol0 = col0 + w * 16;
   const int64_t t0 = seg * args.seg_len;
   const int n = (int)min(args.seg_len, args.L - t0);
   const int da = (int)args.da, dc = (int)args.dc;
@@ -465,21 +465,17 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
   const float *pg = args.g + b * args.g_b + h;
   const float iscale = R.iscale, pscale = R.pscale, sscale = R.sscale;
 
-  // The state: S[dt][ct][r] is row dt * 16 + lg * 4 + r, column wcol0 + ct * 16 + l15.
-  f32x4 S[DT][NC];
+  // The state: S[dt][r] is row dt * 16 + lg * 4 + r, column wcol0 + l15.
+  f32x4 S[DT];
   constexpr int64_t kTile = (int64_t)DA * TV;
-  const int64_t wtile = (int64_t)w * DT * NC * 256 + lane * 4;
+  const int64_t wtile = (int64_t)w * DT * 256 + lane * 4;
 #pragma unroll
-  for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-    for (int ct = 0; ct < NC; ++ct) S[dt][ct] = f32x4{0, 0, 0, 0};
+  for (int dt = 0; dt < DT; ++dt) S[dt] = f32x4{0, 0, 0, 0};
   auto edge_tile = [&](int i) { return R.edge + (((int64_t)bh * args.nedge + i) * args.nslice + slice) * kTile + wtile; };
   auto store_edge = [&](int i) {
     float *o = edge_tile(i);
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int ct = 0; ct < NC; ++ct) *(f32x4 *)(o + (dt * NC + ct) * 256) = S[dt][ct];
+    for (int dt = 0; dt < DT; ++dt) *(f32x4 *)(o + dt * 256) = S[dt];
   };
   // exp(g) of the step after the edge comes to S first: <S, R> may be out of range where this is not
   auto dot_edge = [&](int i, int64_t t) {
@@ -487,13 +483,11 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     const float2 e = exp2_in_two(t < args.L ? decay_log2(pg[t * args.g_t]) : 0.0f);
     f32x4 d = {0, 0, 0, 0};
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
+    for (int dt = 0; dt < DT; ++dt) {
+      const f32x4 x = *(const f32x4 *)(o + dt * 256);
 #pragma unroll
-      for (int ct = 0; ct < NC; ++ct) {
-        const f32x4 x = *(const f32x4 *)(o + (dt * NC + ct) * 256);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) d[r] = fmaf(S[dt][ct][r] * e.x * e.y, x[r], d[r]);
-      }
+      for (int r = 0; r < 4; ++r) d[r] = fmaf(S[dt][r] * e.x * e.y, x[r], d[r]);
+    }
     float v = (d[0] + d[1]) + (d[2] + d[3]);
 #pragma unroll
     for (int k = 32; k >= 1; k >>= 1) v += __shfl_xor(v, k, 64);
@@ -505,12 +499,10 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-        for (int ct = 0; ct < NC; ++ct)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = dt * 16 + lg * 4 + r, col = wcol0 + ct * 16 + l15;
-            if (row < da && col < dc) S[dt][ct][r] = s[R.state_in_t ? col * da + row : row * dc + col];
-          }
+        for (int r = 0; r < 4; ++r) {
+          const int row = dt * 16 + lg * 4 + r, col = wcol0 + l15;
+          if (row < da && col < dc) S[dt][r] = s[R.state_in_t ? col * da + row : row * dc + col];
+        }
     }
   };
   if constexpr (!STATE_ONLY) {
@@ -526,7 +518,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
           const int y = dt * 16 + lg * 4, w_t = y % cols_t / 16;
           const float *p = R.loc + ((j * R.nslice_t + y / cols_t) * cols_t * args.dc_t) + (int64_t)(w_t * tiles_t + x / 16) * 256 + ((x % 16) / 4 * 16 + y % 16) * 4 + x % 4;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[dt][0][r] = S[dt][0][r] * e.x * e.y + (x < dc && y + r < da ? p[r * 4] : 0.0f);
+          for (int r = 0; r < 4; ++r) S[dt][r] = S[dt][r] * e.x * e.y + (x < dc && y + r < da ? p[r * 4] : 0.0f);
         }
       };
       const int before = rev ? args.nseg - 1 - seg : seg;
@@ -542,9 +534,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     } else if (args.combined) {
       const float *loc = R.loc + (((int64_t)bh * args.nseg + seg) * args.nslice + slice) * kTile + wtile;
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int ct = 0; ct < NC; ++ct) S[dt][ct] = *(const f32x4 *)(loc + (dt * NC + ct) * 256);
+      for (int dt = 0; dt < DT; ++dt) S[dt] = *(const f32x4 *)(loc + dt * 256);
     } else {
       load_state_in();
       // the segments before this one, in the order of the recurrence
@@ -554,9 +544,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
         const float2 e = R.tot[j];
         const float *loc = R.loc + (j * args.nslice + slice) * kTile + wtile;
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int ct = 0; ct < NC; ++ct) S[dt][ct] = S[dt][ct] * e.x * e.y + *(const f32x4 *)(loc + (dt * NC + ct) * 256);
+        for (int dt = 0; dt < DT; ++dt) S[dt] = S[dt] * e.x * e.y + *(const f32x4 *)(loc + dt * 256);
       }
     }
     if (DOTS && rev && args.last_edge && seg == args.nseg - 1) store_edge(args.nedge - 1);
@@ -661,8 +649,8 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
       fetch_decays(ci + 2);
     }
 
-    f32x4 acc[CT][NC];
-    typename Vec4<T>::raw ev[DOTS ? CT : 1][NC];
+    f32x4 acc[CT];
+    typename Vec4<T>::raw ev[DOTS ? CT : 1];
     if constexpr (!STATE_ONLY) {
       // products a_t . b_s of steps s <= t with their decays, 16 x 16 tiles over the waves
       constexpr int NTILE = CT * (CT + 1) / 2;
@@ -713,52 +701,42 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
       }
       if constexpr (DOTS) {
 #pragma unroll
-        for (int tt = 0; tt < CT; ++tt)
-#pragma unroll
-          for (int ct = 0; ct < NC; ++ct) {
-            const int l = here(lane), col = min(wcol0 + ct * 16 + (l >> 4) * 4, dc - 4), row = min(tt * 16 + (l & 15), rows - 1);
-            ev[tt][ct] = Vec4<T>::load_b(pe + (int64_t)low * ste, (uint32_t)(rev ? rows - 1 - row : row) * ste + col * ES);
-          }
+        for (int tt = 0; tt < CT; ++tt) {
+          const int l = here(lane), col = min(wcol0 + (l >> 4) * 4, dc - 4), row = min(tt * 16 + (l & 15), rows - 1);
+          ev[tt] = Vec4<T>::load_b(pe + (int64_t)low * ste, (uint32_t)(rev ? rows - 1 - row : row) * ste + col * ES);
+        }
       }
       // what the state gives
 #pragma unroll
-      for (int tt = 0; tt < CT; ++tt)
-#pragma unroll
-        for (int ct = 0; ct < NC; ++ct) acc[tt][ct] = f32x4{0, 0, 0, 0};
+      for (int tt = 0; tt < CT; ++tt) acc[tt] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int kk = 0; kk < DA / 32; ++kk) {
+        float x[8];
 #pragma unroll
-        for (int ct = 0; ct < NC; ++ct) {
-          float x[8];
+        for (int r = 0; r < 4; ++r) x[r] = S[2 * kk][r], x[4 + r] = S[2 * kk + 1][r];
+        const Pieces<NS> sf = split<NS>(x);
+        constexpr int G = DOTS ? CT / 2 : CT;  // row tiles at a time
 #pragma unroll
-          for (int r = 0; r < 4; ++r) x[r] = S[2 * kk][ct][r], x[4 + r] = S[2 * kk + 1][ct][r];
-          const Pieces<NS> sf = split<NS>(x);
-          constexpr int G = DOTS ? CT / 2 : CT;  // row tiles at a time
+        for (int t0 = 0; t0 < CT; t0 += G) {
+          Pieces<NX> af[G];
 #pragma unroll
-          for (int t0 = 0; t0 < CT; t0 += G) {
-            Pieces<NX> af[G];
-#pragma unroll
-            for (int i = 0; i < G; ++i) af[i] = rowfrag<NX>(lds.a, PA, SA, (t0 + i) * 16, kk * 32, lane);
-            mma_pieces<NS, NX, G>([&](int) { return sf; }, [&](int i) { return af[i]; }, [&](int i) -> f32x4 & { return acc[t0 + i][ct]; });
-          }
+          for (int i = 0; i < G; ++i) af[i] = rowfrag<NX>(lds.a, PA, SA, (t0 + i) * 16, kk * 32, lane);
+          mma_pieces<NS, NX, G>([&](int) { return sf; }, [&](int i) { return af[i]; }, [&](int i) -> f32x4 & { return acc[t0 + i]; });
         }
       }
 #pragma unroll
       for (int tt = 0; tt < CT; ++tt) {
         const float f = dec.in[tt * 16 + l15];
-#pragma unroll
-        for (int ct = 0; ct < NC; ++ct) acc[tt][ct] *= f;
+        acc[tt] *= f;
       }
     }
     // The next chunk's rows travel during the rest of this one (and hold no
     // registers before; with dot products, which need more, from the state on).
     if ((STATE_ONLY || !DOTS) && ci + 1 < nchunk) fetch(ci + 1);
     if constexpr (!STATE_ONLY) __syncthreads();  // all products are there
-    Pieces<NX> cf[C / 32][NC];
+    Pieces<NX> cf[C / 32];
 #pragma unroll
-    for (int kk = 0; kk < C / 32; ++kk)
-#pragma unroll
-      for (int ct = 0; ct < NC; ++ct) cf[kk][ct] = colfrag<NX>(lds.c, PC, SC, kk * 32, (w * NC + ct) * 16, here(lane));
+    for (int kk = 0; kk < C / 32; ++kk) cf[kk] = colfrag<NX>(lds.c, PC, SC, kk * 32, w * 16, here(lane));
     if constexpr (!STATE_ONLY) {
       if (threadIdx.x == 0) lds.bad[par ^ 1] = 0;
       // A NaN or an infinity in c must not meet the zeros of earlier steps in
@@ -766,9 +744,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
       const int bad = __builtin_amdgcn_readfirstlane(lds.bad[par]);
       if (bad) {
 #pragma unroll
-        for (int kk = 0; kk < C / 32; ++kk)
-#pragma unroll
-          for (int ct = 0; ct < NC; ++ct) make_finite(cf[kk][ct]);
+        for (int kk = 0; kk < C / 32; ++kk) make_finite(cf[kk]);
       }
       const int lp = here(lane);
       // (steps kk * 32 on meet row tiles 2 kk on; one piece of the products at a time)
@@ -783,39 +759,32 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
           for (int j = NX == 1 ? 0 : NP - 1 - i; j >= 0; --j)
 #pragma unroll
             for (int tt = 2 * kk; tt < CT; ++tt)
-#pragma unroll
-              for (int ct = 0; ct < NC; ++ct)
-                acc[tt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cf[kk][ct].p[j]), __builtin_bit_cast(bf16x8, pf[tt].p[0]), acc[tt][ct], 0, 0, 0);
+              acc[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cf[kk].p[j]), __builtin_bit_cast(bf16x8, pf[tt].p[0]), acc[tt], 0, 0, 0);
         }
       if (grow) {
 #pragma unroll
         for (int tt = 0; tt < CT; ++tt) {
           const int shift = (int)dec.shift[tt * 16 + (lp & 15)];
 #pragma unroll
-          for (int ct = 0; ct < NC; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[tt][ct][r] = ldexpf(acc[tt][ct][r], shift);
+          for (int r = 0; r < 4; ++r) acc[tt][r] = ldexpf(acc[tt][r], shift);
         }
       }
       if (bad) {
+        int *first = lds.first + w * 16;
 #pragma unroll
-        for (int ct = 0; ct < NC; ++ct) {
-          int *first = lds.first + (w * NC + ct) * 16;
+        for (int r = 0; r < 4; ++r) {
+          const int f = first[(lp >> 4) * 4 + r];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int f = first[(lp >> 4) * 4 + r];
-#pragma unroll
-            for (int tt = 0; tt < CT; ++tt)
-              if (tt * 16 + (lp & 15) >= f) acc[tt][ct][r] = NAN;
-          }
-          if (first[lp & 15] < C) {
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) S[dt][ct] = f32x4{NAN, NAN, NAN, NAN};
-          }
-          first[lp & 15] = C;  // for the next chunk; these columns are this wave's alone
+          for (int tt = 0; tt < CT; ++tt)
+            if (tt * 16 + (lp & 15) >= f) acc[tt][r] = NAN;
         }
+        if (first[lp & 15] < C) {
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) S[dt] = f32x4{NAN, NAN, NAN, NAN};
+        }
+        first[lp & 15] = C;  // for the next chunk; these columns are this wave's alone
       }
-      // out^T: column wcol0 + ct * 16 + lg * 4 + r of step tt * 16 + l15; loff: byte
+      // out^T: column wcol0 + lg * 4 + r of step tt * 16 + l15; loff: byte
       // offset of this lane's row and columns from those of row `low`
       const int lo = here(lane), l15 = lo & 15, lg = lo >> 4;
       const uint32_t loff = (uint32_t)(rev ? rows - 1 - l15 : l15) * sto + (wcol0 + lg * 4) * oes;
@@ -830,17 +799,14 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
           const bool no_dot = rev && t0 + n == args.L && ci == 0 && i == 0;
           const float own = lds.diag[i];
           float dot = 0.0f;
+          const int col = wcol0 + lg * 4;
+          const f32x4 cv = get4<NX>(lds.c + i * SC + w * 16 + lg * 4, PC);
+          const float4 x = Vec4<T>::cvt(ev[tt]);
+          const f32x4 xv = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int ct = 0; ct < NC; ++ct) {
-            const int col = wcol0 + ct * 16 + lg * 4;
-            const f32x4 cv = get4<NX>(lds.c + i * SC + (w * NC + ct) * 16 + lg * 4, PC);
-            const float4 x = Vec4<T>::cvt(ev[tt][ct]);
-            const f32x4 xv = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              if (col < dc) dot = fmaf(acc[tt][ct][r], xv[r], dot);
-              acc[tt][ct][r] = fmaf(own, cv[r], acc[tt][ct][r]);
-            }
+          for (int r = 0; r < 4; ++r) {
+            if (col < dc) dot = fmaf(acc[tt][r], xv[r], dot);
+            acc[tt][r] = fmaf(own, cv[r], acc[tt][r]);
           }
           dot += __shfl_xor(dot, 16, 64);
           dot += __shfl_xor(dot, 32, 64);
@@ -848,35 +814,25 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
         }
         if (i < rows && wcol0 + lg * 4 < dc) {
           char *p = po + (int64_t)(low + (rev ? -tt * 16 : tt * 16)) * sto + loff;
-#pragma unroll
-          for (int ct = 0; ct < NC; ++ct) {
-            if (NC > 1 && wcol0 + ct * 16 + lg * 4 >= dc) break;
-            if (out_f32)
-              *(f32x4 *)(p + ct * 64) = acc[tt][ct];
-            else
-              M::store4(p + ct * 16 * ES, acc[tt][ct]);
-          }
+          if (out_f32)
+            *(f32x4 *)p = acc[tt];
+          else
+            M::store4(p, acc[tt]);
         }
       }
     }
     if (!STATE_ONLY && DOTS && ci + 1 < nchunk) fetch(ci + 1);
     // the chunk's steps enter the state
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int ct = 0; ct < NC; ++ct) S[dt][ct] *= e;
+    for (int dt = 0; dt < DT; ++dt) S[dt] *= e;
 #pragma unroll
     for (int kk = 0; kk < C / 32; ++kk) {
-      Pieces<NB> xf[NC];
       const f32x4 y0 = *(const f32x4 *)(dec.out + kk * 32 + lg * 4), y1 = *(const f32x4 *)(dec.out + kk * 32 + 16 + lg * 4);
+      float x[8];
+      floats(cf[kk], x);
 #pragma unroll
-      for (int ct = 0; ct < NC; ++ct) {
-        float x[8];
-        floats(cf[kk][ct], x);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] *= y0[r], x[4 + r] *= y1[r];
-        xf[ct] = split<NB>(x);
-      }
+      for (int r = 0; r < 4; ++r) x[r] *= y0[r], x[4 + r] *= y1[r];
+      const Pieces<NB> xf = split<NB>(x);
       const int ls = here(lane);
       constexpr int G = (DT < 4 ? DT : 4) / (NX == 1 ? 1 : 2);  // independent products side by side
 #pragma unroll
@@ -884,17 +840,13 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
         Pieces<NX> bf[G];
 #pragma unroll
         for (int d = 0; d < G; ++d) bf[d] = colfrag<NX>(lds.b, PA, SA, kk * 32, (d0 + d) * 16, ls);
-#pragma unroll
-        for (int ct = 0; ct < NC; ++ct)
-          mma_pieces<NX, NB, G>([&](int d) { return bf[d]; }, [&](int) { return xf[ct]; }, [&](int d) -> f32x4 & { return S[d0 + d][ct]; });
+        mma_pieces<NX, NB, G>([&](int d) { return bf[d]; }, [&](int) { return xf; }, [&](int d) -> f32x4 & { return S[d0 + d]; });
       }
     }
     if (grow) {
       const float f = dec.e[2];
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int ct = 0; ct < NC; ++ct) S[dt][ct] *= f;
+      for (int dt = 0; dt < DT; ++dt) S[dt] *= f;
     }
     if (DOTS && rev && edge >= 0) store_edge(edge);
   }
@@ -907,9 +859,7 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
     const int64_t j = (int64_t)bh * args.nseg + seg;
     float *loc = R.loc + (j * args.nslice + slice) * kTile + wtile;
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int ct = 0; ct < NC; ++ct) *(f32x4 *)(loc + (dt * NC + ct) * 256) = S[dt][ct];
+    for (int dt = 0; dt < DT; ++dt) *(f32x4 *)(loc + dt * 256) = S[dt];
     if (w == NW - 1 && lane == 0 && slice == 0) R.tot[j] = exp2_in_two(total);
   } else if (seg == (rev ? 0 : args.nseg - 1)) {
     if (DOTS && !rev && args.last_edge) dot_edge(args.nedge - 1, args.L);
@@ -919,12 +869,10 @@ __global__ void __launch_bounds__(NW * 64, DA <= 128 && NC == 1 ? 4 : 2) decay_a
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-        for (int ct = 0; ct < NC; ++ct)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = dt * 16 + lg * 4 + r, col = wcol0 + ct * 16 + l15;
-            if (row < da && col < dc) s[row * dc + col] = S[dt][ct][r] * e;
-          }
+        for (int r = 0; r < 4; ++r) {
+          const int row = dt * 16 + lg * 4 + r, col = wcol0 + l15;
+          if (row < da && col < dc) s[row * dc + col] = S[dt][r] * e;
+        }
     }
   }
 }
@@ -941,7 +889,7 @@ template <typename T, int DA, int NW, bool DOTS, bool STATE_ONLY>
 hipError_t launch_da(const DaArgs &a, hipStream_t s) {
   const int64_t items = (int64_t)a.nslice * a.nroles * (STATE_ONLY ? a.nseg - 1 : a.nseg) * a.BH;
   if (items > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((decay_attn_kernel<T, DA, NW, 1, DOTS, STATE_ONLY>), dim3((unsigned)items), dim3(NW * 64), 0, s, a);
+  hipLaunchKernelGGL((decay_attn_kernel<T, DA, NW, DOTS, STATE_ONLY>), dim3((unsigned)items), dim3(NW * 64), 0, s, a);
   return hipGetLastError();
 }
 
