@@ -43,32 +43,34 @@ int64_t compute_units() {
 // Workgroups run `slots` to a CU (as LDS and registers hold them); a CU takes
 // about chunk_us for a chunk of all of them, and 0.3 more of it for a round
 // that is not full.  A first pass costs 0.4 of a main pass of its segments and a
-// launch, combining another.  Measured, forward and backward, in us (* the split taken):
+// launch, combining another, folding what the last segment reads.  Measured,
+// forward and backward, in us of GPU time (* the split taken):
 //   segments                              1           2 to 6             more
-//   8 x 2048, 16 heads of 128, bf16       152, 587    2: 137, 422        8: 162, 514
-//                                                     4*: 125, 416
-//   1 x 32768, 40 heads of 128, bf16      2117, 9235  6: 675, 2240       12*: 624, 2062  32: 651, 2155  64: 705, 2315
-//   3 x 1111, 8 heads of 72 x 96, fp32    155, 542    6: 58, 154         9*: 48, 130     18: 55, 160
-//   2 x 1537, 32 heads of 64, fp32        143, 535    4: 74, 214         12*: 59, 174    25: 67, 210
-// A second workgroup on a CU adds little where the first has one to itself (one
-// segment of the first shape takes 4.7 us per chunk on half of the CUs, two on
-// each of all CUs 5.3 us each): the vector ALU's issue and the clock, which falls
-// to 1.85 GHz under this load, bound both.
+//   8 x 2048, 16 heads of 128, bf16       165, 617    2: 130, 387        8: 143, 475
+//                                                     4*: 120, 379
+//   1 x 32768, 40 heads of 128, bf16      2522, 9735  6: 642, 2314       12*: 574, 2116  32: 598, 2184  64: 656, 2348
+//   3 x 1111, 8 heads of 72 x 96, fp32    169, 576    6: 54, 154         9*: 43, 129     18: 53, 156
+//   2 x 1537, 32 heads of 64, fp32        148, 554    4: 71, 215         9*: 53, 161     13: 56, 185
+//   1 x 512, 8 heads of 64, bf16          33, 120     4: 17, 51          8*: 13.1, 40.6
+//   1 x 512, 32 heads of 64, bf16         33, 122     4: 17.4, 52        8*: 14.0, 42.9
 constexpr int64_t kMinSegment = 64;
 // From how many segments on the states before them are computed once, by a
 // kernel of its own, and not by every workgroup from the end states before it.
-// Forward, folded and combined: 9 segments (3 x 1111, 8 heads of 72 x 96, fp32)
-// 43.5 and 47.4 us, 12 (2 x 1537, 32 heads of 64, fp32) 55 and 56, 32 (1 x 32768,
-// 40 heads of 128, bf16) 678 and 653.  Backward, where dv folds transposed states
-// and there are more passes to one combining: 131 and 127, 162 and 165, 2335 and 2155 us.
-constexpr int kCombineFwd = 16, kCombineBwd = 5;
-Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es) {
+// Folded and combined, forward: 9 segments (3 x 1111, 8 heads of 72 x 96, fp32)
+// 42.5 and 46.5 us, 16 (1 x 2048, 16 heads of 64, fp32) 28.6 and 34.5, 16 and 24
+// (1 x 16384, 4 heads of 128, bf16) 128 and 128, 98 and 94, 32 (1 x 32768, 40
+// heads of 128, bf16) 633 and 606.  Backward, where dv folds transposed states and
+// there are more passes to one combining: 9 (2 x 1537, 32 heads of 64, fp32) 162
+// and 168, 9 (3 x 1111) 129.6 and 128.0, 11 (1 x 2048) 119 and 111, 13 (2 x 1537)
+// 191 and 185.
+constexpr int kCombineFwd = 24, kCombineBwd = 10;
+Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es, int combine_from) {
   const bool wide = da_waves(dc) == 8;
   const int64_t cus = compute_units(), wgs = bh * slices_of(dc), chunk = es == 2 ? 64 : 32;
   const int64_t slots = padded(da) > 128 ? 1 : es == 4 && padded(da) == 128 ? (wide ? 1 : 2) : wide ? 2 : 3;
   const double chunk_us = wide ? 10.0 : 6.0, launch_us = 5.0;
   // a segment's states go out and in about four times, at 5 TB/s
-  const double state_us = 4.0 * padded(da) * cols_of(dc) * 4 / 5e6;
+  const double tile = padded(da) * cols_of(dc) * 4, state_us = 4.0 * tile / 5e6;
   auto rounds = [&](int64_t n) {
     const int64_t q = (n + cus - 1) / cus;
     return (double)q / slots + (q % slots ? 0.3 : 0.0);
@@ -81,7 +83,10 @@ Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es) {
     const double chunks = (double)((len + chunk - 1) / chunk);
     double us = rounds(wgs * n) * chunks * chunk_us;
     if (n > 1) us += 0.4 * rounds(wgs * (n - 1)) * chunks * chunk_us + launch_us;
-    if (n >= kCombineBwd) us += launch_us;
+    if (n >= combine_from)
+      us += launch_us;
+    else
+      us += (n - 1) * tile / 2e5;  // a workgroup folds at most that many, at 0.2 TB/s
     if (n > 1) us += n * wgs * state_us;
     if (n == 1 || us < least) best = {(int)n, len}, least = us;
   }
@@ -289,7 +294,7 @@ void take_segments(Carve &c, DaRole &r, const DaArgs &a) {
 }
 
 DaArgs fwd_args(const DecayAttnArgs &a, int io_dtype, Carve &c) {
-  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L, a.B * a.H, a.dk, a.dv, io_dtype == 0 ? 4 : 2), kCombineFwd);
+  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L, a.B * a.H, a.dk, a.dv, io_dtype == 0 ? 4 : 2, kCombineFwd), kCombineFwd);
   DaRole &o = r.role[0];
   o.a = a.q, o.b = a.k, o.c = a.v;
   o.out = a.o;
@@ -321,7 +326,7 @@ BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
   BwdSet r{};
   const int edge_len = edge_len_of(a, io_dtype == 0 ? 4 : 2, a.g_t == 0);
   r.want_g = want_g;
-  const Split sp = split_of(a.L, a.B * a.H, a.dv, a.dk, io_dtype == 0 ? 4 : 2);
+  const Split sp = split_of(a.L, a.B * a.H, a.dv, a.dk, io_dtype == 0 ? 4 : 2, kCombineBwd);
   r.q = r.k = base_args(a, a.dv, a.dk, sp, kCombineBwd), r.v = base_args(a, a.dk, a.dv, sp, kCombineBwd);
   DaRole &q = r.q.role[0], &k = r.k.role[0], &v = r.v.role[0];
   q.a = a.dout, q.b = a.v, q.c = a.k, q.e = a.q;
