@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(NT) residual_norm_fwd_kernel(ResidualNormArgs 
 template <typename T, typename R, int TPR, int V, int NT>
 __global__ void __launch_bounds__(NT) residual_norm_bwd_kernel(ResidualNormArgs a, float *part_w, float *part_s) {
   __shared__ float red[2][16];
-  __shared__ float lds[NT / TPR > 1 ? NT * 8 : 8];
+  __shared__ alignas(16) float lds[NT / TPR > 1 ? NT * 8 : 8];
   constexpr int GR = NT / TPR;
   const int l = threadIdx.x % TPR, n8 = (int)(a.dim / 8);
   F8 wt[V], sc[V], aw[V], as[V];
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(NT) gated_norm_fwd_kernel(GatedNormArgs a, int
 template <typename T, int TPR, int V, int NT>
 __global__ void __launch_bounds__(NT) gated_norm_bwd_kernel(GatedNormArgs a, int ngroups, int nrow, float *part_w) {
   __shared__ float red[2][16];
-  __shared__ float lds[NT / TPR > 1 ? NT * 8 : 8];
+  __shared__ alignas(16) float lds[NT / TPR > 1 ? NT * 8 : 8];
   constexpr int GR = NT / TPR;
   const int l = threadIdx.x % TPR, n8 = (int)(a.group / 8);
   const int gi = blockIdx.x % ngroups, rb = blockIdx.x / ngroups;
