@@ -89,6 +89,10 @@ int ssm_decay_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t key
  *           the heads that share a key head; dv: (batch, seqlen, heads, dv)
  *   dlog_decay: log_decay's shape, fp32, NULL = not wanted (0 where the state
  *           is cleared); dstate0: (batch, heads, dk, dv) fp32, NULL = not wanted
+ *
+ * The workspace is the same for every call of a shape: what dlog_decay of decays
+ * by head needs, whether it is wanted or not.  With and without dlog_decay, dq and
+ * dk are summed in another order: equal to fp32's rounding, not to the bit.
  */
 int64_t ssm_decay_attn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
                                            int64_t key_heads, int64_t dk, int64_t dv, int io_dtype);

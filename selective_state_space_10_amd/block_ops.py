@@ -153,7 +153,8 @@ def decay_attn_fwd(q, k, v, log_decay, scale=None, state0=None, return_final_sta
 def decay_attn_bwd(q, k, v, log_decay, do, scale=None, state0=None, dstate_final=None,
                    want_dlog_decay=True, want_dstate0=True):
     """Gradients of decay_attn_fwd, given do and (optionally) dstate_final.
-    Returns a dict: dq, dk, dv, dlog_decay (log_decay's shape), dstate0."""
+    Returns a dict: dq, dk, dv, dlog_decay (log_decay's shape), dstate0.  dq and
+    dk with and without dlog_decay are equal to fp32's rounding, not to the bit."""
     dev, G, H, dk, dv = _attn_sizes(q, v, 4)
     B, L = q.shape[:2]
     io, dt = _io_code(q), q.dtype

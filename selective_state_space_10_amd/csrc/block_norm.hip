@@ -1,9 +1,9 @@
 // block_norm.hip -- the RMS norms around a block, each fused with what is next
 // to it: the residual sum and its scale before a block, the gate after its
-// mixing.  All of them are bound by HBM: every tensor is read and written
-// once, 8 elements per lane and access, a row stays in registers between its
-// sum of squares and its result, and weights stay in registers over the rows
-// that a workgroup takes.
+// mixing.  Every tensor is read and written once, 8 elements per lane and access,
+// a row stays in registers between its sum of squares and its result, and weights
+// stay in registers over the rows that a workgroup takes: rows and groups of 128
+// and more are bound by HBM (below).
 //
 // Mapping: TPR lanes share a row (of one group of channels), each with V
 // pieces of 8 elements, piece i at (i TPR + lane) 8.  A workgroup stays in one
@@ -11,10 +11,15 @@
 // registers over its rows; workgroups' sums are added in order by a second
 // small kernel.
 //
-// Measured: residual norm backward, 16384 x 2048, bf16 with fp32 stream (604 MB):
+// Measured: residual norm forward, 16384 x 2048, bf16 with fp32 stream (403 MB): 78 us;
+// residual norm backward, 16384 x 2048, bf16 with fp32 stream (604 MB):
 // 115 us and 7 for the second kernel; gated norm forward, 32768 x 5120 in groups of
 // 128, bf16 (1.0 GB): 213 us; gated norm backward, 4099 x 5120 fp32 (420 MB): 82 us
-// and 6; 5.3, 4.7 and 5.1 TB/s, a large copy 5.0.  One row of 5120: 4 us, latency.
+// and 6; 5.1, 5.3, 4.7 and 5.1 TB/s, a large copy 5.0.  One row of 5120: 4 us, latency.
+// Groups of 32768 x 5120, bf16, forward and backward: 128 in 215 and 364 us, 64 in 264
+// and 426, 32 in 437 and 668, 16 in 846 and 1236, 8 in 1628 and 2950: at least 8
+// lanes share a row, so that below 64 most of them idle and a workgroup's reads are
+// parts of lines.  A group of 5120 backward takes 524 us, 3.2 TB/s.
 #include "block_kernels.hpp"
 #include "device_common.hpp"
 

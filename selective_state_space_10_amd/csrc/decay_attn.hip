@@ -106,8 +106,8 @@ Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es, int combin
 // ends of a block, and in a sum over its steps a dot product counts at most half
 // the block (from one edge: all of it).
 // One workgroup per block between edges; the running sum is fp64.  A few MB and chains
-// of dependent sums: latency (9 us for 8 x 2048 steps of 16 heads, 1024 workgroups;
-// 2% of the backward).
+// of dependent sums: latency (7 to 9 us for 8 x 2048 steps of 16 heads, 1024
+// workgroups; 2% of the backward).
 struct DaDecayGrad {
   const float *dots_q, *dots_k;   // (slices, BH, L)
   const float *edge_dot;          // (parts, BH, nblock)
@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DaDecayGrad a) {
 
 // The states before every segment from the end states of the ones before it
 // (in place): one thread per 4 elements, in the order of the recurrence, 8
-// segments' loads under way (7 us for 12 segments of 64 heads of 64 x 64 in two
-// roles, of which the bytes are 8 MB in, 18 out: latency of the chain).
+// segments' loads under way (10 us for 32 segments of 16 heads of 64 x 64, fp32, in
+// two roles, 16 MB in and 17 out: latency of the chain).
 __global__ void __launch_bounds__(256) combine_kernel(DaArgs a, int da_padded, int cols) {
   const DaRole &R = a.role[blockIdx.y];
   const int64_t tile4 = (int64_t)da_padded * cols / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;

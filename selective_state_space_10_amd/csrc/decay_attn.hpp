@@ -409,17 +409,23 @@ struct __attribute__((aligned(16))) DaLds {
 // STATE_ONLY: the end state of a segment from zero (a split sequence's
 // first pass).  DOTS: out . e wanted.
 //
-// What bounds it is the vector ALU's issue (decays onto products, the state and
-// c, and their pieces), not HBM or the matrix instructions: at 8 x 2048 steps of
-// 16 heads of 128, bf16, the main pass of 512 workgroups takes 86 us for 24 M
-// vector, 3.2 M matrix and 3.3 M LDS instructions and 304 MB, the first pass of
-// 384 workgroups 36 us for 7.8 M, 1.2 M and 1.1 M; with DOTS 129 us for 34 M.  In
-// fp32 (2 x 1537 steps, 32 heads of 64) a main pass takes 39 us, 43 with DOTS.
-// 16 columns to a wave: 32 leave one workgroup to a CU (the whole forward 124 us
-// against 117); 8 waves for 128 columns: 4 waves, in twice the workgroups that
-// read a and b, 167 us against 126.  Chunks are as long as LDS holds for two
-// workgroups per CU (fp32, 128 wide: one): longer ones have more products inside,
-// shorter ones more updates of the state.
+// What bounds it: no unit by itself.  At 8 x 2048 steps of 16 heads of 128, bf16,
+// the main pass of 512 workgroups takes 92 to 96 us.  Of that its 304 MB past L2
+// would take 61 at a large copy's rate; the 3.9 M matrix instructions keep the
+// SIMDs' matrix units busy for 41% of the clocks, and the 28 M vector
+// instructions (decays onto products, the state and c, and their pieces) fill 37%
+// of the issue slots if two waves always pair up, 74% if they never do.  Waves
+// wait 36% of their time for a slot and 37% for data and barriers: the phases of
+// a chunk (rows to LDS, products of steps, what the state gives, the update)
+// follow one another between three barriers.  The first pass of 384 workgroups
+// takes 36 us for 127 MB, 7.9 M vector and 1.2 M matrix instructions; with DOTS 112
+// to 135 us for 425 MB and 35 M.  In fp32 (2 x 1537 steps, 32 heads of 64) a main pass
+// takes 40 us, 45 to 51 with DOTS.
+// Chosen when the 8 x 2048 forward took 117 us: 16 columns to a wave (32 leave one
+// workgroup to a CU, 124 us); 8 waves for 128 columns (126 against 167 us with 4
+// waves, in twice the workgroups that read a and b).  Chunks are as long as LDS
+// holds for two workgroups per CU (fp32, 128 wide: one): longer ones have more
+// products inside, shorter ones more updates of the state.
 template <typename T, int DA, int NW, bool DOTS, bool STATE_ONLY>
 __global__ void __launch_bounds__(NW * 64, DA <= 128 ? 4 : 2) decay_attn_kernel(DaArgs args) {
   typedef Store<T> M;

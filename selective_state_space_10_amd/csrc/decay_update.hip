@@ -2,8 +2,10 @@
 // o = scale S^T q, with S (B, H, dk, dv) fp32 updated in place.  The state is
 // streamed once in and once out with 16-byte accesses and everything else is
 // small, so the kernel is bound by HBM: 256 requests of 40 heads of 128 x 128
-// (1.35 GB) take 264 us, 5.1 TB/s, where a large copy reaches 5.0; one request
-// of 16 heads takes 7 us, which is latency.
+// (1.35 GB) take 264 us, 5.1 TB/s, where a large copy reaches 5.0; of 128 x 64 143 us
+// (4.7 TB/s), of 128 x 32 67 us (from caches, 5.1).  Columns are taken 128 at a time: of 128
+// x 8, 62 us (1.5 TB/s, 30 of 32 lanes idle), of 128 x 136, 381 us (3.8 TB/s).  One
+// request of 16 heads takes 7 us, which is latency.
 //
 // Mapping: a workgroup owns a slab of columns of one (batch row, head); LPR
 // lanes cover a row of the slab, 4 columns each, and the other lanes and the
