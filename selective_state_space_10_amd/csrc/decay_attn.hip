@@ -55,16 +55,23 @@ int64_t compute_units() {
 //   1 x 512, 32 heads of 64, bf16         33, 122     4: 17.4, 52        8*: 14.0, 42.9
 constexpr int64_t kMinSegment = 64;
 // From how many segments on the states before them are computed once, by a
-// kernel of its own, and not by every workgroup from the end states before it.
-// Folded and combined, forward: 9 segments (3 x 1111, 8 heads of 72 x 96, fp32)
-// 42.5 and 46.5 us, 16 (1 x 2048, 16 heads of 64, fp32) 28.6 and 34.5, 16 and 24
-// (1 x 16384, 4 heads of 128, bf16) 128 and 128, 98 and 94, 32 (1 x 32768, 40
-// heads of 128, bf16) 633 and 606.  Backward, where dv folds transposed states and
-// there are more passes to one combining: 9 (2 x 1537, 32 heads of 64, fp32) 162
-// and 168, 9 (3 x 1111) 129.6 and 128.0, 11 (1 x 2048) 119 and 111, 13 (2 x 1537)
-// 191 and 185.
-constexpr int kCombineFwd = 24, kCombineBwd = 10;
-Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es, int combine_from) {
+// kernel of its own, and not by every workgroup from the end states before it:
+// earlier for wider states, and backward in time, where dv folds transposed
+// states and there are more passes to one combining.  Folded and combined, us:
+//   wider of dk, dv           forward                                backward
+//   64 (1 x 2048, 16 heads)   16: 28.6, 34.5   32: 29.3, 34.8        8: 137, 135   11: 119, 111
+//      (2 x 1537, 32 heads)   13: 55.5, 58.5   25: 65.3, 61.8        9: 162, 168   13: 191, 185
+//   128 (3 x 1111, 8 heads)   9: 42.5, 46.5    18: 53.4, 52.9        6: 153.6, 153.7   9: 129.6, 128.0
+//      (2 x 1500, 16 heads)   12: 32.2, 35.8   24: 42.8, 42.1        6: 108, 109   8: 95.6, 94.6
+//      (1 x 16384, 4 heads)   16: 128, 128     24: 98, 94            6: 881, 876   9: 617, 603
+//   256 (1 x 1500, 4 heads)   8: 78.7, 81.3    12: 63.3, 61.3        4: 391, 374   5: 345, 318
+//      (2 x 2048, 8 heads)    8: 67.8, 74.6    16: 98.8, 101         5: 259, 261   8: 214, 216
+// (64: fp32; 128: fp32, bf16 with dv 64, bf16; 256: fp32, bf16.)
+int combine_from(int64_t dk, int64_t dv, bool backward) {
+  const int wide = padded(dk > dv ? dk : dv);
+  return wide <= 64 ? (backward ? 10 : 24) : wide == 128 ? (backward ? 8 : 20) : (backward ? 5 : 12);
+}
+Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es, int combine) {
   const bool wide = da_waves(dc) == 8;
   const int64_t cus = compute_units(), wgs = bh * slices_of(dc), chunk = es == 2 ? 64 : 32;
   const int64_t slots = padded(da) > 128 ? 1 : es == 4 && padded(da) == 128 ? (wide ? 1 : 2) : wide ? 2 : 3;
@@ -83,7 +90,7 @@ Split split_of(int64_t L, int64_t bh, int64_t da, int64_t dc, int es, int combin
     const double chunks = (double)((len + chunk - 1) / chunk);
     double us = rounds(wgs * n) * chunks * chunk_us;
     if (n > 1) us += 0.4 * rounds(wgs * (n - 1)) * chunks * chunk_us + launch_us;
-    if (n >= combine_from)
+    if (n >= combine)
       us += launch_us;
     else
       us += (n - 1) * tile / 2e5;  // a workgroup folds at most that many, at 0.2 TB/s
@@ -275,9 +282,9 @@ hipError_t launch_first_pass(const DaArgs &a, int io_dtype, hipStream_t s) {
   return e;
 }
 
-DaArgs base_args(const DecayAttnArgs &a, int64_t da, int64_t dc, Split sp, int combine_from) {
+DaArgs base_args(const DecayAttnArgs &a, int64_t da, int64_t dc, Split sp, int combine) {
   DaArgs r{};
-  r.combined = sp.nseg >= combine_from;
+  r.combined = sp.nseg >= combine;
   r.L = a.L, r.da = da, r.dc = dc, r.g = a.g, r.g_b = a.g_b, r.g_t = a.g_t;
   r.nroles = 1;
   r.H = (int)a.H, r.BH = (int)(a.B * a.H), r.nseg = sp.nseg, r.seg_len = sp.seg_len;
@@ -294,7 +301,8 @@ void take_segments(Carve &c, DaRole &r, const DaArgs &a) {
 }
 
 DaArgs fwd_args(const DecayAttnArgs &a, int io_dtype, Carve &c) {
-  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L, a.B * a.H, a.dk, a.dv, io_dtype == 0 ? 4 : 2, kCombineFwd), kCombineFwd);
+  const int combine = combine_from(a.dk, a.dv, false);
+  DaArgs r = base_args(a, a.dk, a.dv, split_of(a.L, a.B * a.H, a.dk, a.dv, io_dtype == 0 ? 4 : 2, combine), combine);
   DaRole &o = r.role[0];
   o.a = a.q, o.b = a.k, o.c = a.v;
   o.out = a.o;
@@ -326,8 +334,9 @@ BwdSet bwd_args(const DecayAttnArgs &a, int io_dtype, bool want_g, Carve &c) {
   BwdSet r{};
   const int edge_len = edge_len_of(a, io_dtype == 0 ? 4 : 2, a.g_t == 0);
   r.want_g = want_g;
-  const Split sp = split_of(a.L, a.B * a.H, a.dv, a.dk, io_dtype == 0 ? 4 : 2, kCombineBwd);
-  r.q = r.k = base_args(a, a.dv, a.dk, sp, kCombineBwd), r.v = base_args(a, a.dk, a.dv, sp, kCombineBwd);
+  const int combine = combine_from(a.dk, a.dv, true);
+  const Split sp = split_of(a.L, a.B * a.H, a.dv, a.dk, io_dtype == 0 ? 4 : 2, combine);
+  r.q = r.k = base_args(a, a.dv, a.dk, sp, combine), r.v = base_args(a, a.dk, a.dv, sp, combine);
   DaRole &q = r.q.role[0], &k = r.k.role[0], &v = r.v.role[0];
   q.a = a.dout, q.b = a.v, q.c = a.k, q.e = a.q;
   k.a = a.v, k.b = a.dout, k.c = a.q, k.e = a.k;

@@ -1,5 +1,6 @@
-"""Decay attention split into as many segments as the workgroups of the backward
-fold the states of, dv's transposed ones among them.
+"""Decay attention split into so many segments that the workgroups of the backward
+fold the states before them (dv's transposed) where states are narrow, and a
+kernel of its own computes them where they are wide.
 
 References and tolerances are those of tests/test_gpu_decay_attn.py."""
 from __future__ import annotations
@@ -26,7 +27,8 @@ def ssm():
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("B,L,H,G,dk,dv", [(1, 512, 8, 4, 64, 64), (2, 500, 3, 1, 24, 136), (1, 330, 4, 2, 136, 40), (1, 576, 2, 2, 72, 200)])
+@pytest.mark.parametrize("B,L,H,G,dk,dv", [(1, 512, 8, 4, 64, 64), (2, 500, 3, 1, 24, 136), (1, 330, 4, 2, 136, 40), (1, 576, 2, 2, 72, 200),
+                                           (1, 570, 3, 1, 48, 40), (1, 440, 4, 2, 72, 104)])
 @pytest.mark.parametrize("decay,per_token", [("weak", True), ("reset", True), ("mixed", False)])
 def test_five_to_nine_segments(ssm, dtype, B, L, H, G, dk, dv, decay, per_token):
     n = _segments(ssm, B, L, H, G, dk, dv, dtype)
