@@ -38,11 +38,11 @@ __device__ __forceinline__ float decay_log2(float g) {
   return g < kMinLog2Decay * kLn2 ? kMinLog2Decay : g * kLog2e;  // NaN passes
 }
 
-// 2^x in two factors, each in fp32's range for |x| up to 240 (beyond, what
-// they multiply is zero or out of range itself).
+// 2^x in two factors, each in fp32's range for |x| up to 240.  Beyond, what they
+// multiply is out of range itself, or a state that was cleared: zero.
 __device__ __forceinline__ float2 exp2_in_two(double x) {
   const double n = rint(x);
-  const int k = (int)fmin(fmax(n, -300.0), 240.0), k1 = k >> 1;
+  const int k = n < -240.0 ? -400 : (int)fmin(n, 240.0), k1 = k >> 1;
   return make_float2(ldexpf(fast_exp2((float)(x - n)), k1), ldexpf(1.0f, k - k1));
 }
 

@@ -105,3 +105,16 @@ def test_infinite_growth_reaches_no_earlier_step(ssm, dtype, bad):
     o, _ = ssm.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], None, d["state0"])
     _check(o[:, :70], ro[:, :70], dtype)
     assert not torch.isfinite(o[:, 70:]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L,at", [(60, 10), (700, 10), (700, 500), (5000, 10)])
+def test_a_cleared_state_leaves_nothing(ssm, dtype, L, at):
+    """However large it was: not 2^-256 of it."""
+    d = _gpu(ref.attn_inputs(1, L, 2, 2, 32, 40, seed=3, decay="none", dtype=dtype))
+    d["g"][:, at] = -math.inf
+    d["k"].zero_()
+    large = torch.full_like(d["state0"], 2.0 ** 110)
+    o, s = ssm.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], None, large, return_final_state=True)
+    assert o[:, at - 1].any()
+    assert not o[:, at:].any() and not s.any()
