@@ -32,10 +32,12 @@ typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 
 // Decays below this many powers of two are zero in fp32 whatever they meet
-// (smallest fp32 2^-149): -inf is held at it, so that sums of decays stay finite.
-constexpr float kMinLog2Decay = -256.0f;
+// (smallest fp32 2^-149) and clear the state, as -inf does: they are held at a
+// finite one, so that sums of decays stay finite, far below what growth after
+// them can make up for.
+constexpr float kMinLog2Decay = -256.0f, kClearLog2 = -4096.0f;
 __device__ __forceinline__ float decay_log2(float g) {
-  return g < kMinLog2Decay * kLn2 ? kMinLog2Decay : g * kLog2e;  // NaN passes
+  return g < kMinLog2Decay * kLn2 ? kClearLog2 : g * kLog2e;  // NaN passes
 }
 
 // 2^x in two factors, each in fp32's range for |x| up to 240.  Beyond, what they

@@ -118,3 +118,21 @@ def test_a_cleared_state_leaves_nothing(ssm, dtype, L, at):
     o, s = ssm.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], None, large, return_final_state=True)
     assert o[:, at - 1].any()
     assert not o[:, at:].any() and not s.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L", [64, 700])
+def test_growth_after_a_cleared_state(ssm, dtype, L):
+    """By more than 2^256, which is how small a cleared state may be counted."""
+    p = ref.attn_inputs(1, L, 2, 1, 32, 40, seed=3, dtype=dtype)
+    p["g"][:, 10] = -math.inf
+    p["g"][:, 11:51] = 6.0
+    _quiet(p, slice(10, 51), "k", "do")
+    ro, rs = ref.attn_fwd(p, 32 ** -0.5)
+    rg = ref.attn_bwd(p, 32 ** -0.5)
+    d = _gpu(p)
+    o, s = ssm.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], None, d["state0"], return_final_state=True)
+    g = ssm.decay_attn_bwd(d["q"], d["k"], d["v"], d["g"], d["do"], None, d["state0"], want_dlog_decay=False, want_dstate0=False)
+    _check(o, ro, dtype)
+    _check(s, rs, F32)
+    _check(g["dq"], rg["dq"], dtype)
