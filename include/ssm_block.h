@@ -8,7 +8,14 @@
  *   - residual norm: the RMS norm before a block, fused with the residual sum
  *     and its scale, and its gradients;
  *   - gated norm: the RMS norm after a block's mixing, by groups of channels,
- *     fused with the SiLU gate, and its gradients.
+ *     fused with the SiLU gate, and its gradients;
+ *   - gated recurrence: a scan whose state is one number per channel, with gates
+ *     for its decay and its input, over whole sequences, its gradients, and one
+ *     token of it;
+ *   - causal convolution: the short depthwise convolution in front of a mixing,
+ *     with a state of the last inputs, its gradients, and one token of it;
+ *   - head norm and rotation: the RMS norm of every head of queries and keys and
+ *     the rotation of its elements by position, in one pass, and its gradients.
  *
  * Conventions are those of ssm_scan.h: io_dtype is SSM_F32 or SSM_BF16,
  * arithmetic and states are fp32, bf16 results are rounded once to nearest
@@ -29,7 +36,7 @@
 extern "C" {
 #endif
 
-#define SSM_BLOCK_ABI_VERSION 1
+#define SSM_BLOCK_ABI_VERSION 2
 
 /* SSM_BLOCK_ABI_VERSION of the built library. */
 int ssm_block_abi_version(void);
@@ -165,6 +172,170 @@ int ssm_gated_norm_bwd(int64_t rows, int64_t dim, int64_t group, int io_dtype, c
                        const void *x, int64_t x_row_stride, const void *z, int64_t z_row_stride,
                        const float *weight, const float *rstd, int gate_first, void *dx, void *dz,
                        float *dweight, void *workspace, int64_t workspace_bytes, void *hip_stream);
+
+/*
+ * A read-only tensor indexed (batch, step, channel).  Strides are in elements;
+ * channels are adjacent.  A stride may be zero (a broadcast input) but not
+ * negative; a step's is at most 2^23.  ptr and every stride must keep 16-byte
+ * alignment.  For one token stride_step is not used.
+ */
+typedef struct ssm_view3 {
+  const void *ptr;
+  int64_t stride_batch, stride_step;
+} ssm_view3;
+
+/*
+ * Gated recurrence.  Per batch row and channel:
+ *
+ *   h_t = a_t h_{t-1} + s_t sigmoid(input_gate_t) x_t     h_{-1} = state0 or 0
+ *   y_t = h_t (silu(z_t))
+ *
+ *   decay given:  a = exp(-sharpness softplus(decay) sigmoid(decay_gate_t)),  s = sqrt(1 - a^2)
+ *   decay NULL:   a = sigmoid(decay_gate_t),                                  s = 1 - a
+ *
+ *   x, decay_gate, input_gate, z: (batch, seqlen, dim) views in io_dtype;
+ *              input_gate NULL = 1, z NULL = no gate
+ *   decay:     (dim) fp32; sharpness > 0 and finite (not used without decay)
+ *   state0:    (batch, dim) fp32 or NULL
+ *   starts:    (batch, seqlen) bytes, NULL = none: where not zero, a document
+ *              starts: a = 0 and s = 1.  Nothing crosses it, infinities and NaN
+ *              included, in either direction.
+ *   lengths:   (batch), NULL = seqlen: the rows' lengths in a padded batch
+ *              (taken as 0 below 0 and as seqlen above).  Inputs behind a row's
+ *              length are not used, y is zero there, and the state stays that
+ *              of the row's last token.
+ *   y:         (batch, seqlen, dim) contiguous, io_dtype
+ *   state_final: (batch, dim) fp32, NULL = not wanted
+ *   states:    (batch, ceil(seqlen / SSM_RECURRENCE_CHUNK), dim) fp32, NULL = not
+ *              wanted: the state before every chunk, which the backward needs
+ *
+ * dim: a multiple of 8 up to 2^23; batch <= 2^16.
+ */
+#define SSM_RECURRENCE_CHUNK 128
+
+int64_t ssm_gated_recurrence_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io_dtype);
+
+int ssm_gated_recurrence_fwd(int64_t batch, int64_t seqlen, int64_t dim, int io_dtype, const ssm_view3 *x,
+                             const ssm_view3 *decay_gate, const ssm_view3 *input_gate, const ssm_view3 *z,
+                             const float *decay, float sharpness, const float *state0,
+                             const uint8_t *starts, const int32_t *lengths, void *y,
+                             float *state_final, float *states, void *workspace,
+                             int64_t workspace_bytes, void *hip_stream);
+
+/*
+ * Its gradients, given dy (a view) and dstate_final (optional, NULL = 0).  With
+ * e_t = dy_t (silu(z_t)) and w_t = e_t + a_{t+1} w_{t+1} (beyond the end: dstate_final):
+ *
+ *   dx_t = w_t s_t sigmoid(input_gate_t)     ddecay_gate_t = w_t (h_{t-1} da + sigmoid(input_gate_t) x_t ds)
+ *   dinput_gate_t = w_t s_t x_t sigmoid'(input_gate_t)      dz_t = dy_t h_t silu'(z_t)
+ *
+ * dx, ddecay_gate, dinput_gate, dz (batch, seqlen, dim) contiguous, io_dtype,
+ * zero behind a row's length; dinput_gate and dz are required iff their inputs
+ * are given; ddecay (dim) fp32, required iff decay is given; dstate0 (batch, dim)
+ * fp32, NULL = not wanted.  states: as the forward wrote them (state0 is their first).
+ */
+int64_t ssm_gated_recurrence_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io_dtype);
+
+int ssm_gated_recurrence_bwd(int64_t batch, int64_t seqlen, int64_t dim, int io_dtype, const ssm_view3 *dy,
+                             const ssm_view3 *x, const ssm_view3 *decay_gate,
+                             const ssm_view3 *input_gate, const ssm_view3 *z, const float *decay,
+                             float sharpness, const float *states, const uint8_t *starts,
+                             const int32_t *lengths, const float *dstate_final, void *dx,
+                             void *ddecay_gate, void *dinput_gate, void *dz, float *ddecay,
+                             float *dstate0, void *workspace, int64_t workspace_bytes,
+                             void *hip_stream);
+
+/*
+ * One token: state (batch, dim) fp32 is updated in place; y (batch, dim)
+ * contiguous, io_dtype.
+ */
+int ssm_gated_recurrence_update(int64_t batch, int64_t dim, int io_dtype, float *state, const ssm_view3 *x,
+                                const ssm_view3 *decay_gate, const ssm_view3 *input_gate,
+                                const ssm_view3 *z, const float *decay, float sharpness, void *y,
+                                void *hip_stream);
+
+/*
+ * Causal depthwise convolution, per batch row and channel:
+ *
+ *   y_t = act(bias + sum_k weight[k] x_{t - (width - 1) + k}),  act = silu or (silu = 0) the identity
+ *
+ *   x:       (batch, seqlen, dim) view in io_dtype; y contiguous
+ *   weight:  (dim, width) fp32, width 1 to 4; bias (dim) fp32 or NULL
+ *   state0:  (batch, width - 1, dim) in io_dtype, the inputs before the first,
+ *            oldest first; NULL = 0 (and must be NULL if width is 1)
+ *   starts, lengths: as of the gated recurrence; taps that reach before the
+ *            document of their step are zero, and so is y behind a row's length
+ *   state_final: as state0: the last width - 1 inputs of each row, zero where
+ *            they are not of the row's last document; NULL = not wanted
+ *
+ * dim: a multiple of 8 up to 2^23; batch <= 2^16.
+ */
+int ssm_causal_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int width, int io_dtype,
+                        const ssm_view3 *x, const float *weight, const float *bias, const void *state0,
+                        const uint8_t *starts, const int32_t *lengths, int silu, void *y,
+                        void *state_final, void *hip_stream);
+
+/*
+ * Its gradients, given dy (a view) and dstate_final (as state_final, optional,
+ * NULL = 0): dx (batch, seqlen, dim) contiguous, io_dtype; dweight (dim, width)
+ * and dbias (dim) fp32, dbias NULL = not wanted; dstate0 as state0, NULL = not wanted.
+ */
+int64_t ssm_causal_conv_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int width);
+
+int ssm_causal_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int width, int io_dtype,
+                        const ssm_view3 *dy, const ssm_view3 *x, const float *weight, const float *bias,
+                        const void *state0, const uint8_t *starts, const int32_t *lengths, int silu,
+                        const void *dstate_final, void *dx, float *dweight, float *dbias, void *dstate0,
+                        void *workspace, int64_t workspace_bytes, void *hip_stream);
+
+/* One token: state (batch, width - 1, dim) in io_dtype moves on by one input, in
+ * place (NULL if width is 1); y (batch, dim) contiguous. */
+int ssm_causal_conv_update(int64_t batch, int64_t dim, int width, int io_dtype, void *state,
+                           const ssm_view3 *x, const float *weight, const float *bias, int silu, void *y,
+                           void *hip_stream);
+
+/*
+ * Norm and rotation of heads.  For every head of q (q_heads of them) and k:
+ *
+ *   n = x rstd weight,  rstd = (mean x^2 + eps)^-1/2   (norm = 0: n = x)
+ *   (n_i, n_j) <- (n_i cos - n_j sin, n_j cos + n_i sin),  angle = position * inv_freq[p]
+ *
+ *   pair p < rotary / 2 is (i, j) = (p, p + rotary / 2), or with interleaved
+ *   (2p, 2p + 1); elements from rotary on are not rotated
+ *   q, k:      (batch, seqlen, heads, dim) views in io_dtype; k NULL = none (k_heads = 0)
+ *   q_weight, k_weight: fp32, (heads, dim) if weight_per_head, else (dim);
+ *              NULL = 1 (both or neither; NULL if norm = 0)
+ *   positions: (batch, seqlen), or with positions_per_batch = 0 (seqlen), int64,
+ *              NULL = no rotation (rotary = 0)
+ *   inv_freq:  (rotary / 2) fp64, radians per position; the angle is formed in
+ *              fp64, so that far positions keep their digits
+ *   q_out, k_out: contiguous, io_dtype
+ *
+ * dim: a multiple of 8 from 8 to 256; rotary: a multiple of 8 up to dim; heads
+ * in all <= 65536; batch * seqlen <= 2^40.
+ */
+int ssm_head_norm_rotary_fwd(int64_t batch, int64_t seqlen, int64_t q_heads, int64_t k_heads, int64_t dim,
+                             int64_t rotary, int io_dtype, const ssm_view4 *q, const ssm_view4 *k,
+                             const float *q_weight, const float *k_weight, int weight_per_head,
+                             const int64_t *positions, int positions_per_batch, const double *inv_freq,
+                             float eps, int norm, int interleaved, void *q_out, void *k_out,
+                             void *hip_stream);
+
+/*
+ * Its gradients, given dq_out and dk_out (views): dq, dk contiguous, io_dtype;
+ * dq_weight, dk_weight as the weights, fp32, required iff those are given.
+ */
+int64_t ssm_head_norm_rotary_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t q_heads,
+                                                 int64_t k_heads, int64_t dim);
+
+int ssm_head_norm_rotary_bwd(int64_t batch, int64_t seqlen, int64_t q_heads, int64_t k_heads, int64_t dim,
+                             int64_t rotary, int io_dtype, const ssm_view4 *dq_out,
+                             const ssm_view4 *dk_out, const ssm_view4 *q, const ssm_view4 *k,
+                             const float *q_weight, const float *k_weight, int weight_per_head,
+                             const int64_t *positions, int positions_per_batch, const double *inv_freq,
+                             float eps, int norm, int interleaved, void *dq, void *dk, float *dq_weight,
+                             float *dk_weight, void *workspace, int64_t workspace_bytes,
+                             void *hip_stream);
 
 #ifdef __cplusplus
 }

@@ -22,13 +22,28 @@ BLOCK_EXPORTS = ("ssm_block_abi_version", "ssm_decay_attn_fwd_workspace_bytes",
                  "ssm_decay_attn_fwd", "ssm_decay_attn_bwd_workspace_bytes", "ssm_decay_attn_bwd",
                  "ssm_decay_attn_update", "ssm_residual_norm_fwd",
                  "ssm_residual_norm_bwd_workspace_bytes", "ssm_residual_norm_bwd",
-                 "ssm_gated_norm_fwd", "ssm_gated_norm_bwd_workspace_bytes", "ssm_gated_norm_bwd")
+                 "ssm_gated_norm_fwd", "ssm_gated_norm_bwd_workspace_bytes", "ssm_gated_norm_bwd",
+                 "ssm_gated_recurrence_fwd_workspace_bytes", "ssm_gated_recurrence_fwd",
+                 "ssm_gated_recurrence_bwd_workspace_bytes", "ssm_gated_recurrence_bwd",
+                 "ssm_gated_recurrence_update", "ssm_causal_conv_fwd",
+                 "ssm_causal_conv_bwd_workspace_bytes", "ssm_causal_conv_bwd",
+                 "ssm_causal_conv_update", "ssm_head_norm_rotary_fwd",
+                 "ssm_head_norm_rotary_bwd_workspace_bytes", "ssm_head_norm_rotary_bwd")
+
+# SSM_RECURRENCE_CHUNK: steps between the states that the gated recurrence keeps
+RECURRENCE_CHUNK = 128
 
 
 class View4(ctypes.Structure):
     """ssm_view4: a (batch, step, head, element) tensor's pointer and strides."""
     _fields_ = [("ptr", ctypes.c_void_p), ("stride_batch", ctypes.c_int64),
                 ("stride_step", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class View3(ctypes.Structure):
+    """ssm_view3: a (batch, step, channel) tensor's pointer and strides."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_batch", ctypes.c_int64),
+                ("stride_step", ctypes.c_int64)]
 
 
 class FwdPlan(ctypes.Structure):
@@ -129,6 +144,33 @@ def load() -> ctypes.CDLL:
     lib.ssm_gated_norm_bwd.restype = INT
     lib.ssm_gated_norm_bwd.argtypes = [I64] * 3 + [INT, P, P, I64, P, I64, P, P, INT] + [P] * 4 \
         + [I64, P]
+    W = ctypes.POINTER(View3)
+    for name in ("ssm_gated_recurrence_fwd", "ssm_gated_recurrence_bwd"):
+        getattr(lib, name + "_workspace_bytes").restype = I64
+        getattr(lib, name + "_workspace_bytes").argtypes = [I64] * 3 + [INT]
+        getattr(lib, name).restype = INT
+    lib.ssm_gated_recurrence_fwd.argtypes = [I64] * 3 + [INT, W, W, W, W, P, F] + [P] * 7 + [I64, P]
+    lib.ssm_gated_recurrence_bwd.argtypes = [I64] * 3 + [INT, W, W, W, W, W, P, F] + [P] * 11 \
+        + [I64, P]
+    lib.ssm_gated_recurrence_update.restype = INT
+    lib.ssm_gated_recurrence_update.argtypes = [I64, I64, INT, P, W, W, W, W, P, F, P, P]
+    lib.ssm_causal_conv_fwd.restype = INT
+    lib.ssm_causal_conv_fwd.argtypes = [I64] * 3 + [INT, INT, W] + [P] * 5 + [INT, P, P, P]
+    lib.ssm_causal_conv_bwd_workspace_bytes.restype = I64
+    lib.ssm_causal_conv_bwd_workspace_bytes.argtypes = [I64] * 3 + [INT]
+    lib.ssm_causal_conv_bwd.restype = INT
+    lib.ssm_causal_conv_bwd.argtypes = [I64] * 3 + [INT, INT, W, W] + [P] * 5 + [INT] + [P] * 6 \
+        + [I64, P]
+    lib.ssm_causal_conv_update.restype = INT
+    lib.ssm_causal_conv_update.argtypes = [I64, I64, INT, INT, P, W, P, P, INT, P, P]
+    lib.ssm_head_norm_rotary_fwd.restype = INT
+    lib.ssm_head_norm_rotary_fwd.argtypes = [I64] * 6 + [INT, V, V, P, P, INT, P, INT, P, F, INT,
+                                                         INT, P, P, P]
+    lib.ssm_head_norm_rotary_bwd_workspace_bytes.restype = I64
+    lib.ssm_head_norm_rotary_bwd_workspace_bytes.argtypes = [I64] * 5
+    lib.ssm_head_norm_rotary_bwd.restype = INT
+    lib.ssm_head_norm_rotary_bwd.argtypes = [I64] * 6 + [INT, V, V, V, V, P, P, INT, P, INT, P, F, INT,
+                                                         INT] + [P] * 5 + [I64, P]
     _lib = lib
     return lib
 

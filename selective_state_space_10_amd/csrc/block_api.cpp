@@ -4,31 +4,22 @@
 #include <stdarg.h>
 #include <stdio.h>
 
-#include "../../include/ssm_block.h"
-#include "api_error.hpp"
+#include "api_checks.hpp"
 #include "block_kernels.hpp"
 
 using ssm::api_fail;
 using ssm::api_hip_status;
+using ssm::check_dtype;
+using ssm::check_workspace;
+using ssm::kMaxElems;
+using ssm::kMaxStep;
+using ssm::product_ok;
+using ssm::Ptr;
 
 namespace {
 
-constexpr int64_t kMaxElems = (int64_t)1 << 40;      // of one tensor
 constexpr int64_t kMaxBatchHeads = (int64_t)1 << 26; // workgroups of one launch stay below 2^31
 constexpr int64_t kMaxRow = 16384;
-constexpr int64_t kMaxStep = (int64_t)1 << 23;       // elements from one step to the next
-
-bool product_ok(int64_t a, int64_t b, int64_t *out) {
-  if (b > kMaxElems / a) return false;
-  *out = a * b;
-  return true;
-}
-
-int check_dtype(int io_dtype) {
-  if (io_dtype != SSM_F32 && io_dtype != SSM_BF16)
-    return api_fail(SSM_ERR_UNSUPPORTED, "io_dtype=%d is neither SSM_F32 (0) nor SSM_BF16 (1)", io_dtype);
-  return SSM_OK;
-}
 
 int check_attn(int64_t batch, int64_t seqlen, int64_t heads, int64_t key_heads, int64_t dk, int64_t dv, int io_dtype) {
   if (batch < 1 || seqlen < 1 || heads < 1 || key_heads < 1 || dk < 1 || dv < 1)
@@ -51,40 +42,11 @@ int check_attn(int64_t batch, int64_t seqlen, int64_t heads, int64_t key_heads, 
 
 // one_step: stride_step is not used
 int check_view(const char *name, const ssm_view4 *v, int io_dtype, bool one_step = false) {
-  if (v == nullptr || v->ptr == nullptr) return api_fail(SSM_ERR_NULL_ARG, "%s is NULL", name);
-  const int64_t es = io_dtype == SSM_F32 ? 4 : 2;
+  SSM_TRY(ssm::check_view_ptr(name, v, v ? v->ptr : nullptr));
   const int64_t step = one_step ? 0 : v->stride_step;
   const int64_t st[] = {v->stride_batch, step, v->stride_head};
-  for (int64_t s : st) {
-    if (s < 0 || s > kMaxElems) return api_fail(SSM_ERR_BAD_SHAPE, "%s has stride %lld", name, (long long)s);
-    if (s * es % 16 != 0) return api_fail(SSM_ERR_ALIGNMENT, "%s has stride %lld, not a multiple of 16 bytes", name, (long long)s);
-  }
+  for (int64_t s : st) SSM_TRY(ssm::check_stride(name, s, io_dtype));
   if (step > kMaxStep) return api_fail(SSM_ERR_UNSUPPORTED, "%s has a step stride over 2^23 elements", name);
-  if (((uintptr_t)v->ptr & 15u) != 0) return api_fail(SSM_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
-  return SSM_OK;
-}
-
-struct Ptr {
-  const char *name;
-  const void *p;
-  bool required;
-  unsigned align;
-};
-
-int check_ptrs(const Ptr *ps, int n) {
-  for (int i = 0; i < n; ++i) {
-    if (ps[i].required && ps[i].p == nullptr) return api_fail(SSM_ERR_NULL_ARG, "%s is NULL", ps[i].name);
-    if (((uintptr_t)ps[i].p & (ps[i].align - 1)) != 0)
-      return api_fail(SSM_ERR_ALIGNMENT, "%s is not %u-byte aligned", ps[i].name, ps[i].align);
-  }
-  return SSM_OK;
-}
-
-int check_workspace(const void *workspace, int64_t got, int64_t need) {
-  if (need == 0) return SSM_OK;
-  if (workspace == nullptr || got < need)
-    return api_fail(SSM_ERR_WORKSPACE, "needs %lld workspace bytes, got %lld", (long long)need, workspace ? (long long)got : 0LL);
-  if (((uintptr_t)workspace & 15u) != 0) return api_fail(SSM_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
   return SSM_OK;
 }
 
@@ -128,13 +90,6 @@ int check_residual_dtype(int io_dtype, int residual_dtype) {
 }
 
 }  // namespace
-
-#define SSM_TRY(call)              \
-  do {                             \
-    const int st_ = (call);        \
-    if (st_ != SSM_OK) return st_; \
-  } while (0)
-#define SSM_TRY_PTRS(ps) SSM_TRY(check_ptrs(ps, (int)(sizeof(ps) / sizeof(ps[0]))))
 
 extern "C" {
 

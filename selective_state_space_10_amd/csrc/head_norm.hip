@@ -1,0 +1,270 @@
+// head_norm.hip -- the RMS norm of every head of queries and keys and the
+// rotation of its elements by position, in one pass, and its gradients.
+//
+// A group of TPR lanes owns one head: 8 elements per lane in two pieces of 4, so
+// that both elements of a rotated pair are in one lane (pieces p and p + rotary / 8
+// where pairs are half a rotation apart, 8 adjacent elements where they are
+// interleaved).  A workgroup takes up to 256 / TPR heads, all heads of as many
+// tokens as fit, over a run of tokens; it stays with its heads, so that their
+// weights are in registers, and so are the sums for the weights' gradients.  The
+// cosines and sines of a few tokens are formed once per workgroup, into LDS, while
+// the tokens' rows are on their way.
+#include "mixer_device.hpp"
+#include "mixer_kernels.hpp"
+
+namespace ssm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTable = 2048;  // angles in LDS
+constexpr int kMaxRows = 8;      // rows of a group under way together
+
+struct Plan {
+  int tpr, nblk, hb, tsub, rows;  // lanes per head, blocks of heads, heads per block, tokens at once, rows per group of a chunk of tokens
+  int64_t nchunk, nruns;
+};
+
+// cos and sin of 2 pi turns, |turns| <= 1/2: to the nearest quarter, then the
+// series of an angle up to pi / 4; what they leave out is below 2^-28.
+__device__ __forceinline__ float2 cos_sin(double turns) {
+  const double q = rint(4.0 * turns);
+  const float x = (float)((turns - 0.25 * q) * 6.283185307179586), x2 = x * x;
+  const float s = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f);
+  const float c = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  const int n = (int)q & 3;
+  const float u = n & 1 ? s : c, v = n & 1 ? c : s;
+  return make_float2(n == 1 || n == 2 ? -u : u, n >= 2 ? -v : v);
+}
+
+// The elements one[i], two[i] of a lane are a pair; x holds its two pieces.
+__device__ __forceinline__ void to_pairs(const float (&x)[8], bool interleaved, float (&one)[4], float (&two)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) one[i] = interleaved ? x[2 * i] : x[i], two[i] = interleaved ? x[2 * i + 1] : x[4 + i];
+}
+__device__ __forceinline__ void from_pairs(const float (&one)[4], const float (&two)[4], bool interleaved, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = interleaved ? (i & 1 ? two[i / 2] : one[i / 2]) : (i < 4 ? one[i] : two[i - 4]);
+}
+
+template <int TPR>
+__device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+  for (int d = TPR / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// The cosines and sines of tokens t0 .. t0 + n of a batch row.
+__device__ __forceinline__ void fill_table(const HeadNormArgs &a, int64_t b, int64_t t0, int n, float2 *table) {
+  const int half = a.rot / 2;
+  for (int i = threadIdx.x; i < n * half; i += kThreads) {
+    const int tok = i / half, p = i - tok * half;
+    const double turns = (double)a.pos[b * a.pos_b + t0 + tok] * (a.inv_freq[p] * 0.15915494309189535);
+    table[i] = cos_sin(turns - rint(turns));
+  }
+}
+
+template <typename T, int TPR, bool BWD>
+__global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadNormArgs a, Plan plan, float *part) {
+  __shared__ alignas(16) float2 table[kMaxTable];
+  const int half = a.rot / 2, HT = a.Hq + a.Hk;
+  const int blk = (int)(blockIdx.x % plan.nblk), grp = threadIdx.x / TPR, p = threadIdx.x % TPR;
+  const int64_t run = blockIdx.x / plan.nblk;
+  const int hl = grp % plan.hb, sub = grp / plan.hb, h = blk * plan.hb + hl;
+  const bool mine = sub < plan.tsub && h < HT && hl < plan.hb, on = mine && p < a.d / 8;
+  const bool is_q = h < a.Hq;
+  const int hh = is_q ? h : h - a.Hq;
+  const HeadView &src = is_q ? a.q : a.k, &up = is_q ? a.dq_out : a.dk_out;
+  T *dst = (T *)(BWD ? (is_q ? a.dq : a.dk) : (is_q ? a.q_out : a.k_out));
+  const int nh = is_q ? a.Hq : a.Hk;
+  const bool rotated = p < a.rot / 8, inter = a.interleaved && rotated;
+  // where the lane's two pieces begin
+  const int o1 = rotated && !inter ? 4 * p : 8 * p, o2 = rotated && !inter ? 4 * p + half : 8 * p + 4;
+  float x[8], w1[4], w2[4], acc1[4], acc2[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w1[i] = w2[i] = 1.0f, acc1[i] = acc2[i] = 0.0f;
+  auto load_row = [&](const T *q, float (&v)[8]) {
+    float lo[4], hi[4];
+    load_vec(q + o1, lo);
+    load_vec(q + o2, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+  };
+  const float *wp = is_q ? a.wq : a.wk;
+  if (on && wp) {
+    float lo[4], hi[4];
+    load_vec(wp + hh * a.w_h + o1, lo);
+    load_vec(wp + hh * a.w_h + o2, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
+    to_pairs(x, inter, w1, w2);
+  }
+  const int tt = plan.tsub * plan.rows;  // tokens of a chunk
+  const int64_t row_chunks = (a.L + tt - 1) / tt;
+  for (int64_t ch = run; ch < plan.nchunk; ch += plan.nruns) {
+    const int64_t b = ch / row_chunks, t0 = ch % row_chunks * tt;
+    const int n = (int)(a.L - t0 < tt ? a.L - t0 : tt);
+    const T *xp = (const T *)src.p + b * src.sb + t0 * src.st + hh * src.sh;
+    const T *up_p = BWD ? (const T *)up.p + b * up.sb + t0 * up.st + hh * up.sh : nullptr;
+    T *out = dst + ((b * a.L + t0) * nh + hh) * a.d;
+    __syncthreads();  // the table's last readers are done
+    fill_table(a, b, t0, n, table);
+    __syncthreads();
+    for (int tok = sub; tok < n; tok += plan.tsub) {
+      if (!mine) break;
+      float one[4], two[4], g1[4], g2[4], ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) one[i] = two[i] = g1[i] = g2[i] = 0.0f;
+      if (on) {
+        load_row(xp + tok * src.st, x);
+        to_pairs(x, inter, one, two);
+        if constexpr (BWD) {
+          load_row(up_p + tok * up.st, x);
+          to_pairs(x, inter, g1, g2);
+        }
+      }
+      float rstd = 1.0f;
+      if (a.norm) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss = fmaf(one[i], one[i], fmaf(two[i], two[i], ss));
+        rstd = rsqrtf(head_sum<TPR>(ss) / (float)a.d + a.eps);
+      }
+      float2 cs[4];
+      if (rotated)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cs[i] = table[tok * half + 4 * p + i];
+      if constexpr (!BWD) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float n1 = one[i] * rstd * w1[i], n2 = two[i] * rstd * w2[i];
+          one[i] = rotated ? fmaf(n1, cs[i].x, -n2 * cs[i].y) : n1;
+          two[i] = rotated ? fmaf(n2, cs[i].x, n1 * cs[i].y) : n2;
+        }
+      } else {
+        // u = the gradient of n, turned back; with hat = x rstd: dx = rstd (u w - hat mean(u w hat))
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u1 = rotated ? fmaf(g1[i], cs[i].x, g2[i] * cs[i].y) : g1[i];
+          const float u2 = rotated ? fmaf(g2[i], cs[i].x, -g1[i] * cs[i].y) : g2[i];
+          one[i] *= rstd, two[i] *= rstd;
+          acc1[i] = fmaf(u1, one[i], acc1[i]), acc2[i] = fmaf(u2, two[i], acc2[i]);
+          g1[i] = u1 * w1[i], g2[i] = u2 * w2[i];
+          s = fmaf(g1[i], one[i], fmaf(g2[i], two[i], s));
+        }
+        s = a.norm ? head_sum<TPR>(s) / (float)a.d : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          one[i] = a.norm ? rstd * (g1[i] - one[i] * s) : g1[i];
+          two[i] = a.norm ? rstd * (g2[i] - two[i] * s) : g2[i];
+        }
+      }
+      if (on) {
+        from_pairs(one, two, inter, x);
+        float lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lo[i] = x[i], hi[i] = x[4 + i];
+        store_vec(out + (int64_t)tok * nh * a.d + o1, lo);
+        store_vec(out + (int64_t)tok * nh * a.d + o2, hi);
+      }
+    }
+  }
+  if constexpr (BWD) {
+    if (!a.dwq) return;
+    // sums over the workgroup's groups, in their order: for a head's own weight
+    // over its tokens at once, for a shared one over the heads too (rows: one per
+    // workgroup, columns: q's elements, then k's)
+    float *lds = (float *)table;
+    static_assert(sizeof(table) >= kThreads * 8 * sizeof(float), "the sums fit where the angles were");
+    __syncthreads();
+    from_pairs(acc1, acc2, inter, x);
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds[grp * a.d + o1 + i] = x[i], lds[grp * a.d + o2 + i] = x[4 + i];
+    }
+    __syncthreads();
+    if (a.w_h) {
+      for (int i = threadIdx.x; i < plan.hb * a.d; i += kThreads) {
+        const int head = blk * plan.hb + i / a.d;
+        if (head >= HT) break;
+        float v = lds[i];
+        for (int k = 1; k < plan.tsub; ++k) v += lds[k * plan.hb * a.d + i];
+        part[(run * HT + head) * a.d + i % a.d] = v;
+      }
+    } else {
+      for (int i = threadIdx.x; i < 2 * a.d; i += kThreads) {
+        float v = 0.0f;
+        for (int k = 0; k < plan.hb * plan.tsub; ++k) {
+          const int head = blk * plan.hb + k % plan.hb;
+          if (head < HT && (head < a.Hq) == (i < a.d)) v += lds[k * a.d + i % a.d];
+        }
+        part[(int64_t)blockIdx.x * 2 * a.d + i] = v;
+      }
+    }
+  }
+}
+
+constexpr int64_t kFwdWorkgroups = 2048, kBwdWorkgroups = 1024;
+
+int64_t most_runs(int nblk, int64_t workgroups) { return nblk < workgroups ? workgroups / nblk : 1; }
+
+Plan plan_of(int64_t B, int64_t L, int HT, int d, int rot, int64_t workgroups) {
+  Plan p;
+  p.tpr = d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32;
+  const int groups = kThreads / p.tpr;
+  p.nblk = (HT + groups - 1) / groups;
+  p.hb = (HT + p.nblk - 1) / p.nblk;
+  p.tsub = groups / p.hb;
+  p.rows = kMaxRows;
+  while (p.rows > 1 && (p.tsub * p.rows * (rot / 2) > kMaxTable)) p.rows /= 2;
+  const int64_t tt = p.tsub * p.rows;
+  p.nchunk = B * ((L + tt - 1) / tt);
+  const int64_t most = most_runs(p.nblk, workgroups);
+  p.nruns = p.nchunk < most ? p.nchunk : most;
+  return p;
+}
+
+// Batch rows that follow each other evenly are one row; so are rows of one token.
+HeadNormArgs merged(HeadNormArgs a, bool bwd) {
+  auto even = [&](const HeadView &v) { return a.L == 1 || v.sb == v.st * a.L; };
+  const bool all = even(a.q) && (a.Hk == 0 || even(a.k)) && (!bwd || (even(a.dq_out) && (a.Hk == 0 || even(a.dk_out))));
+  if (a.B == 1 || !all || (a.pos && a.pos_b != a.L)) return a;
+  if (a.L == 1) a.q.st = a.q.sb, a.k.st = a.k.sb, a.dq_out.st = a.dq_out.sb, a.dk_out.st = a.dk_out.sb;
+  a.L *= a.B, a.B = 1;
+  return a;
+}
+
+template <typename T, bool BWD>
+hipError_t launch(const HeadNormArgs &given, hipStream_t s) {
+  const HeadNormArgs a = merged(given, BWD);
+  const Plan p = plan_of(a.B, a.L, a.Hq + a.Hk, a.d, a.rot, BWD ? kBwdWorkgroups : kFwdWorkgroups);
+  const dim3 grid((unsigned)(p.nblk * p.nruns));
+  float *part = (float *)a.workspace;
+  if (p.tpr == 4)
+    hipLaunchKernelGGL((head_norm_kernel<T, 4, BWD>), grid, dim3(kThreads), 0, s, a, p, part);
+  else if (p.tpr == 8)
+    hipLaunchKernelGGL((head_norm_kernel<T, 8, BWD>), grid, dim3(kThreads), 0, s, a, p, part);
+  else if (p.tpr == 16)
+    hipLaunchKernelGGL((head_norm_kernel<T, 16, BWD>), grid, dim3(kThreads), 0, s, a, p, part);
+  else
+    hipLaunchKernelGGL((head_norm_kernel<T, 32, BWD>), grid, dim3(kThreads), 0, s, a, p, part);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !BWD || !a.dwq) return e;
+  return a.w_h ? launch_sum_rows(part, p.nruns, (int64_t)(a.Hq + a.Hk) * a.d, (int64_t)a.Hq * a.d, a.dwq, a.dwk, s)
+               : launch_sum_rows(part, p.nruns * p.nblk, 2 * a.d, a.d, a.dwq, a.dwk, s);
+}
+
+}  // namespace
+
+// The largest that any rotation and any strides of these sizes need.
+int64_t head_norm_bwd_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d) {
+  const Plan p = plan_of(1, 1, (int)(Hq + Hk), (int)d, 0, kBwdWorkgroups);
+  const int64_t most = most_runs(p.nblk, kBwdWorkgroups), runs = B * L < most ? B * L : most;
+  const int64_t row = 2 * p.nblk > Hq + Hk ? 2 * p.nblk : Hq + Hk;
+  return runs * row * d * 4;
+}
+
+hipError_t launch_head_norm_fwd(const HeadNormArgs &a, int io_dtype, hipStream_t s) { return io_dtype == 0 ? launch<float, false>(a, s) : launch<bf16, false>(a, s); }
+hipError_t launch_head_norm_bwd(const HeadNormArgs &a, int io_dtype, hipStream_t s) { return io_dtype == 0 ? launch<float, true>(a, s) : launch<bf16, true>(a, s); }
+
+}  // namespace ssm

@@ -1,0 +1,84 @@
+// mixer_device.hpp -- device helpers of the gated recurrence, the causal
+// convolution and the norm and rotation of heads: vectors of the io types and
+// the gates.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace ssm {
+
+// Two fp32 values as bf16, round to nearest even, in one instruction of gfx950.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const f2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));
+}
+
+// N adjacent elements, a multiple of 4, at a 16-byte aligned address (8-byte for 4 of bf16).
+template <int N>
+__device__ __forceinline__ void load_vec(const float *p, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 a = *(const float4 *)(p + i);
+    v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_vec(const bf16 *p, float (&v)[N]) {
+  uint32_t w[N / 2];
+  if constexpr (N == 4) {
+    const uint2 a = *(const uint2 *)p;
+    w[0] = a.x, w[1] = a.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+      const uint4 a = *(const uint4 *)(p + i);
+      w[i / 2] = a.x, w[i / 2 + 1] = a.y, w[i / 2 + 2] = a.z, w[i / 2 + 3] = a.w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+template <int N>
+__device__ __forceinline__ void store_vec(float *p, const float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) *(float4 *)(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int N>
+__device__ __forceinline__ void store_vec(bf16 *p, const float (&v)[N]) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  if constexpr (N == 4) {
+    *(uint2 *)p = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) *(uint4 *)(p + i) = make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
+  }
+}
+__device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(bf16 *p, float v) { p->bits = (uint16_t)pack_bf16(v, v); }
+
+// sigmoid(v) and 1 - sigmoid(v), neither from the other by a subtraction: e^-v
+// over 1 + e^-v keeps the digits of a nearly open gate's complement.
+__device__ __forceinline__ void sigmoid_both(float v, float &one, float &other) {
+  const float e = fast_exp2(-v * kLog2e);
+  one = fast_rcp(1.0f + e);
+  other = v < -64.0f ? 1.0f : e * one;  // (e is infinite from about -88 on)
+}
+
+// z sigmoid(z) and its derivative
+__device__ __forceinline__ void silu_both(float z, float &f, float &df) {
+  float g, o;
+  sigmoid_both(z, g, o);
+  f = z * g;
+  df = g * fmaf(z, o, 1.0f);
+}
+
+__device__ __forceinline__ int row_length(const int32_t *lengths, int64_t b, int64_t L) {
+  const int64_t n = lengths ? (int64_t)lengths[b] : L;
+  return (int)(n < 0 ? 0 : n < L ? n : L);
+}
+
+}  // namespace ssm

@@ -1,0 +1,142 @@
+"""The C ABI of the gated recurrence, the causal convolution and the norm and rotation of
+heads (include/ssm_block.h) without a GPU: workspace queries and refusals.  No kernel
+is launched: every call here fails validation."""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+import re
+
+import pytest
+
+from tests.conftest import ROOT
+
+OK, NULL_ARG, BAD_SHAPE, UNSUPPORTED, ALIGNMENT, WORKSPACE, HIP = range(7)
+FAKE = 0x10000  # aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from selective_state_space_10_amd import _lib
+    return _lib.load()
+
+
+def v3(ptr=FAKE, sb=4096, st=64):
+    from selective_state_space_10_amd import _lib
+    return ctypes.byref(_lib.View3(ptr, sb, st))
+
+
+def v4(ptr=FAKE, sb=4096, st=64, sh=32):
+    from selective_state_space_10_amd import _lib
+    return ctypes.byref(_lib.View4(ptr, sb, st, sh))
+
+
+def test_constants():
+    from selective_state_space_10_amd import _lib
+    text = open(os.path.join(ROOT, "include", "ssm_block.h")).read()
+    assert _lib.RECURRENCE_CHUNK == int(re.search(r"SSM_RECURRENCE_CHUNK (\d+)", text).group(1))
+
+
+VIEWS = [(dict(ptr=0), NULL_ARG), (dict(ptr=FAKE + 4), ALIGNMENT), (dict(sb=66), ALIGNMENT), (dict(st=-64), BAD_SHAPE), (dict(st=1 << 24), UNSUPPORTED),
+         (dict(sb=1 << 41), BAD_SHAPE)]
+SIZES = [(dict(B=0), BAD_SHAPE), (dict(L=0), BAD_SHAPE), (dict(D=0), BAD_SHAPE), (dict(L=-1), BAD_SHAPE), (dict(D=12), UNSUPPORTED), (dict(D=1 << 24), UNSUPPORTED),
+         (dict(B=65537), UNSUPPORTED), (dict(L=1 << 40), BAD_SHAPE), (dict(io=2), UNSUPPORTED)]
+
+
+def rec_fwd(lib, B=2, L=16, D=64, io=0, x=None, g=None, i=None, z=None, decay=FAKE, sharp=8.0, s0=None, st=None, ln=None, y=FAKE, fin=None, states=None,
+            ws=FAKE, wsb=1 << 50):
+    return lib.ssm_gated_recurrence_fwd(B, L, D, io, x or v3(), g or v3(), i, z, decay, sharp, s0, st, ln, y, fin, states, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,want", SIZES + [
+    (dict(B=65536, L=1, D=1 << 21), UNSUPPORTED), (dict(y=None), NULL_ARG), (dict(y=FAKE + 8), ALIGNMENT),
+    (dict(decay=FAKE + 4), ALIGNMENT), (dict(s0=FAKE + 8), ALIGNMENT), (dict(ln=FAKE + 2), ALIGNMENT), (dict(fin=FAKE + 4), ALIGNMENT), (dict(states=FAKE + 4), ALIGNMENT),
+    (dict(sharp=0.0), UNSUPPORTED), (dict(sharp=-1.0), UNSUPPORTED), (dict(sharp=math.inf), UNSUPPORTED), (dict(sharp=math.nan), UNSUPPORTED)])
+def test_recurrence_refusals(lib, kw, want):
+    assert rec_fwd(lib, **kw) == want
+    assert lib.ssm_last_error()
+
+
+@pytest.mark.parametrize("name", ["x", "g", "i", "z"])
+@pytest.mark.parametrize("kw,want", VIEWS)
+def test_recurrence_views(lib, name, kw, want):
+    assert rec_fwd(lib, **{name: v3(**kw)}) == want
+
+
+def test_recurrence_backward_and_token(lib):
+    def bwd(x=None, i=None, z=None, decay=FAKE, states=FAKE, dx=FAKE, dg=FAKE, di=None, dz=None, dd=FAKE, ds=None, ws=FAKE, wsb=1 << 50):
+        return lib.ssm_gated_recurrence_bwd(2, 16, 64, 0, v3(), x or v3(), v3(), i, z, decay, 8.0, states, None, None, None, dx, dg, di, dz, dd, ds, ws, wsb, None)
+    assert bwd(states=None) == NULL_ARG and bwd(dx=None) == NULL_ARG and bwd(dg=None) == NULL_ARG and bwd(x=v3(FAKE + 2)) == ALIGNMENT
+    assert bwd(i=v3()) == NULL_ARG and bwd(di=FAKE) == NULL_ARG and bwd(z=v3()) == NULL_ARG and bwd(dz=FAKE) == NULL_ARG
+    assert bwd(decay=None) == NULL_ARG and bwd(dd=None) == NULL_ARG and bwd(ds=FAKE + 4) == ALIGNMENT
+    need = lib.ssm_gated_recurrence_bwd_workspace_bytes(2, 16, 64, 0)
+    assert need > 0 and bwd(ws=None) == WORKSPACE and bwd(wsb=need - 1) == WORKSPACE and bwd(ws=FAKE + 8) == ALIGNMENT
+    assert lib.ssm_gated_recurrence_bwd_workspace_bytes(2, 16, 60, 0) == -1 and lib.ssm_gated_recurrence_fwd_workspace_bytes(2, 16, 64, 5) == -1
+    assert lib.ssm_gated_recurrence_fwd_workspace_bytes(2, 0, 64, 0) == -1
+    upd = lambda B=2, D=64, state=FAKE, x=None, y=FAKE, sharp=8.0: lib.ssm_gated_recurrence_update(B, D, 1, state, x or v3(), v3(), None, None, FAKE, sharp, y, None)  # noqa: E731
+    assert upd(state=None) == NULL_ARG and upd(state=FAKE + 4) == ALIGNMENT and upd(y=None) == NULL_ARG and upd(D=4) == UNSUPPORTED and upd(B=0) == BAD_SHAPE
+    assert upd(x=v3(sb=4)) == ALIGNMENT and upd(sharp=-1.0) == UNSUPPORTED
+
+
+def conv_fwd(lib, B=2, L=16, D=64, K=4, io=0, x=None, w=FAKE, b=None, s0=None, ln=None, y=FAKE, fin=None):
+    return lib.ssm_causal_conv_fwd(B, L, D, K, io, x or v3(), w, b, s0, None, ln, 1, y, fin, None)
+
+
+@pytest.mark.parametrize("kw,want", SIZES + [
+    (dict(K=0), UNSUPPORTED), (dict(K=5), UNSUPPORTED), (dict(w=None), NULL_ARG), (dict(w=FAKE + 4), ALIGNMENT), (dict(b=FAKE + 4), ALIGNMENT),
+    (dict(s0=FAKE + 8), ALIGNMENT), (dict(y=None), NULL_ARG), (dict(y=FAKE + 8), ALIGNMENT), (dict(fin=FAKE + 8), ALIGNMENT), (dict(ln=FAKE + 1), ALIGNMENT),
+    (dict(K=1, s0=FAKE), NULL_ARG), (dict(K=1, fin=FAKE), NULL_ARG)])
+def test_conv_refusals(lib, kw, want):
+    assert conv_fwd(lib, **kw) == want
+    assert lib.ssm_last_error()
+
+
+@pytest.mark.parametrize("kw,want", VIEWS)
+def test_conv_views(lib, kw, want):
+    assert conv_fwd(lib, x=v3(**kw)) == want
+
+
+def test_conv_backward_and_token(lib):
+    def bwd(K=4, dy=None, x=None, s0=None, df=None, dx=FAKE, dw=FAKE, ds=None, ws=FAKE, wsb=1 << 50):
+        return lib.ssm_causal_conv_bwd(2, 16, 64, K, 0, dy or v3(), x or v3(), FAKE, None, s0, None, None, 1, df, dx, dw, None, ds, ws, wsb, None)
+    assert bwd(dx=None) == NULL_ARG and bwd(dw=None) == NULL_ARG and bwd(dy=v3(0)) == NULL_ARG and bwd(x=v3(st=2)) == ALIGNMENT and bwd(df=FAKE + 8) == ALIGNMENT
+    assert bwd(K=1, ds=FAKE) == NULL_ARG and bwd(K=1, df=FAKE) == NULL_ARG and bwd(K=9) == UNSUPPORTED
+    need = lib.ssm_causal_conv_bwd_workspace_bytes(2, 16, 64, 4)
+    assert need > 0 and bwd(ws=None) == WORKSPACE and bwd(wsb=need - 1) == WORKSPACE and bwd(ws=FAKE + 4) == ALIGNMENT
+    assert lib.ssm_causal_conv_bwd_workspace_bytes(2, 16, 64, 5) == -1 and lib.ssm_causal_conv_bwd_workspace_bytes(2, 16, 63, 4) == -1
+    upd = lambda K=4, state=FAKE, y=FAKE, D=64: lib.ssm_causal_conv_update(2, D, K, 1, state, v3(), FAKE, None, 1, y, None)  # noqa: E731
+    assert upd(state=None) == NULL_ARG and upd(K=1) == NULL_ARG and upd(y=FAKE + 8) == ALIGNMENT and upd(D=4) == UNSUPPORTED and upd(K=0) == UNSUPPORTED
+
+
+def heads_fwd(lib, B=2, L=16, Hq=4, Hk=2, d=64, rot=64, io=0, q=None, k=None, qw=FAKE, kw=FAKE, pos=FAKE, inv=FAKE, eps=1e-6, norm=1, qo=FAKE, ko=FAKE):
+    return lib.ssm_head_norm_rotary_fwd(B, L, Hq, Hk, d, rot, io, q or v4(), k or v4(), qw, kw, 0, pos, 1, inv, eps, norm, 0, qo, ko, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=0), BAD_SHAPE), (dict(L=0), BAD_SHAPE), (dict(Hq=0), BAD_SHAPE), (dict(Hk=-1), BAD_SHAPE), (dict(d=0), BAD_SHAPE), (dict(d=12), UNSUPPORTED),
+    (dict(d=264), UNSUPPORTED), (dict(Hq=65536), UNSUPPORTED), (dict(B=1 << 30, L=1 << 30), BAD_SHAPE), (dict(io=7), UNSUPPORTED), (dict(rot=72), UNSUPPORTED),
+    (dict(rot=4), UNSUPPORTED), (dict(rot=-8), UNSUPPORTED), (dict(rot=0), NULL_ARG), (dict(pos=None), NULL_ARG), (dict(inv=None), NULL_ARG),
+    (dict(rot=0, pos=None), NULL_ARG), (dict(qw=None), NULL_ARG), (dict(kw=None), NULL_ARG), (dict(norm=0), NULL_ARG), (dict(Hk=0), NULL_ARG),
+    (dict(eps=-1.0), UNSUPPORTED), (dict(eps=math.nan), UNSUPPORTED), (dict(qo=None), NULL_ARG), (dict(ko=None), NULL_ARG), (dict(ko=FAKE + 8), ALIGNMENT),
+    (dict(pos=FAKE + 4), ALIGNMENT), (dict(inv=FAKE + 4), ALIGNMENT), (dict(qw=FAKE + 4), ALIGNMENT)])
+def test_head_refusals(lib, kw, want):
+    assert heads_fwd(lib, **kw) == want
+    assert lib.ssm_last_error()
+
+
+@pytest.mark.parametrize("name", ["q", "k"])
+@pytest.mark.parametrize("kw,want", [(dict(ptr=0), NULL_ARG), (dict(ptr=FAKE + 8), ALIGNMENT), (dict(sh=34), ALIGNMENT), (dict(st=-64), BAD_SHAPE)])
+def test_head_views(lib, name, kw, want):
+    assert heads_fwd(lib, **{name: v4(**kw)}) == want
+
+
+def test_head_backward(lib):
+    def bwd(dqo=None, dko=None, Hk=2, qw=FAKE, kw=FAKE, dq=FAKE, dk=FAKE, dqw=FAKE, dkw=FAKE, ws=FAKE, wsb=1 << 50):
+        return lib.ssm_head_norm_rotary_bwd(2, 16, 4, Hk, 64, 64, 0, dqo or v4(), dko or v4(), v4(), v4(), qw, kw, 0, FAKE, 1, FAKE, 1e-6, 1, 0, dq, dk, dqw, dkw, ws,
+                                            wsb, None)
+    assert bwd(dqo=v4(0)) == NULL_ARG and bwd(dko=v4(FAKE + 2)) == ALIGNMENT and bwd(dq=None) == NULL_ARG and bwd(dk=None) == NULL_ARG
+    assert bwd(dqw=None) == NULL_ARG and bwd(dkw=None) == NULL_ARG and bwd(qw=None, kw=None) == NULL_ARG and bwd(Hk=0) == NULL_ARG
+    need = lib.ssm_head_norm_rotary_bwd_workspace_bytes(2, 16, 4, 2, 64)
+    assert need > 0 and bwd(ws=None) == WORKSPACE and bwd(wsb=need - 1) == WORKSPACE and bwd(ws=FAKE + 8) == ALIGNMENT
+    assert lib.ssm_head_norm_rotary_bwd_workspace_bytes(2, 16, 4, 2, 60) == -1
