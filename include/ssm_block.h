@@ -209,7 +209,8 @@ typedef struct ssm_view3 {
  *   states:    (batch, ceil(seqlen / SSM_RECURRENCE_CHUNK), dim) fp32, NULL = not
  *              wanted: the state before every chunk, which the backward needs
  *
- * dim: a multiple of 8 up to 2^23; batch <= 2^16.
+ * dim: a multiple of 8 up to 2^23; batch <= 2^16; batch * ceil(dim / 64) *
+ * ceil(seqlen / 128) <= 2^22.
  */
 #define SSM_RECURRENCE_CHUNK 128
 
@@ -247,7 +248,7 @@ int ssm_gated_recurrence_bwd(int64_t batch, int64_t seqlen, int64_t dim, int io_
 
 /*
  * One token: state (batch, dim) fp32 is updated in place; y (batch, dim)
- * contiguous, io_dtype.
+ * contiguous, io_dtype.  batch * dim <= 2^33.
  */
 int ssm_gated_recurrence_update(int64_t batch, int64_t dim, int io_dtype, float *state, const ssm_view3 *x,
                                 const ssm_view3 *decay_gate, const ssm_view3 *input_gate,
@@ -268,7 +269,8 @@ int ssm_gated_recurrence_update(int64_t batch, int64_t dim, int io_dtype, float 
  *   state_final: as state0: the last width - 1 inputs of each row, zero where
  *            they are not of the row's last document; NULL = not wanted
  *
- * dim: a multiple of 8 up to 2^23; batch <= 2^16.
+ * dim: a multiple of 8 up to 2^23; batch <= 2^16; batch * dim / 8 *
+ * (ceil(seqlen / 32) + 1) <= 2^31 (and for one token the same with seqlen 1).
  */
 int ssm_causal_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int width, int io_dtype,
                         const ssm_view3 *x, const float *weight, const float *bias, const void *state0,

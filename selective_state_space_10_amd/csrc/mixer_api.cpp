@@ -28,12 +28,20 @@ int check_seq(int64_t batch, int64_t seqlen, int64_t dim) {
   return SSM_OK;
 }
 
-// Workgroups of one launch: one for 64 channels of a chunk, or fewer.
+// Tensors of at most 2^40 elements, in workgroups for 64 channels of a chunk: a
+// launch has fewer than 2^32 threads.
 int check_recurrence(int64_t batch, int64_t seqlen, int64_t dim) {
   SSM_TRY(check_seq(batch, seqlen, dim));
-  int64_t n;
-  if (!ssm::product_ok(batch * ((dim + 63) / 64), (seqlen + SSM_RECURRENCE_CHUNK - 1) / SSM_RECURRENCE_CHUNK, &n) || n > ((int64_t)1 << 30))
-    return api_fail(SSM_ERR_UNSUPPORTED, "batch * dim / 64 * seqlen / 128 exceeds 2^30");
+  if (batch * ((dim + 63) / 64) > ((int64_t)1 << 22) / ((seqlen + SSM_RECURRENCE_CHUNK - 1) / SSM_RECURRENCE_CHUNK))
+    return api_fail(SSM_ERR_UNSUPPORTED, "batch * ceil(dim / 64) * ceil(seqlen / 128) exceeds 2^22");
+  return SSM_OK;
+}
+
+// The same for threads of 8 channels and up to 32 steps, and of 8 channels of a last state.
+int check_conv(int64_t batch, int64_t seqlen, int64_t dim) {
+  SSM_TRY(check_seq(batch, seqlen, dim));
+  if (batch * (dim / 8) > ((int64_t)1 << 31) / ((seqlen + 31) / 32 + 1))
+    return api_fail(SSM_ERR_UNSUPPORTED, "batch * dim / 8 * (ceil(seqlen / 32) + 1) exceeds 2^31");
   return SSM_OK;
 }
 
@@ -108,7 +116,7 @@ extern "C" {
 
 int64_t ssm_gated_recurrence_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io_dtype) {
   if (check_recurrence(batch, seqlen, dim) != SSM_OK || check_dtype(io_dtype) != SSM_OK) return -1;
-  return ssm::recurrence_fwd_workspace_bytes(batch, seqlen, dim);
+  return ssm::recurrence_fwd_workspace_bytes(batch, seqlen, dim, io_dtype);
 }
 
 int ssm_gated_recurrence_fwd(int64_t batch, int64_t seqlen, int64_t dim, int io_dtype, const ssm_view3 *x,
@@ -126,7 +134,7 @@ int ssm_gated_recurrence_fwd(int64_t batch, int64_t seqlen, int64_t dim, int io_
   const Ptr ps[] = {{"decay", decay, false, 16}, {"state0", state0, false, 16},           {"lengths", lengths, false, 4},
                     {"y", y, true, 16},          {"state_final", state_final, false, 16}, {"states", states, false, 16}};
   SSM_TRY_PTRS(ps);
-  SSM_TRY(check_workspace(workspace, workspace_bytes, ssm::recurrence_fwd_workspace_bytes(batch, seqlen, dim)));
+  SSM_TRY(check_workspace(workspace, workspace_bytes, ssm::recurrence_fwd_workspace_bytes(batch, seqlen, dim, io_dtype)));
   ssm::RecurrenceArgs a{};
   a.B = batch, a.L = seqlen, a.D = dim, a.x = view(x), a.g = view(decay_gate), a.ig = view(input_gate), a.z = view(z);
   a.decay = decay, a.sharpness = sharpness, a.state0 = state0, a.starts = starts, a.lengths = lengths;
@@ -174,7 +182,7 @@ int ssm_gated_recurrence_update(int64_t batch, int64_t dim, int io_dtype, float 
                                 const ssm_view3 *decay_gate, const ssm_view3 *input_gate, const ssm_view3 *z, const float *decay,
                                 float sharpness, void *y, void *hip_stream) {
   ssm::api_clear_error();
-  SSM_TRY(check_seq(batch, 1, dim));
+  SSM_TRY(check_conv(batch, 1, dim));
   SSM_TRY(check_dtype(io_dtype));
   SSM_TRY(check_sharpness(decay, sharpness));
   SSM_TRY(check_view3("x", x, io_dtype, false, true));
@@ -193,7 +201,7 @@ int ssm_causal_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int width, i
                         const float *weight, const float *bias, const void *state0, const uint8_t *starts, const int32_t *lengths,
                         int silu, void *y, void *state_final, void *hip_stream) {
   ssm::api_clear_error();
-  SSM_TRY(check_seq(batch, seqlen, dim));
+  SSM_TRY(check_conv(batch, seqlen, dim));
   SSM_TRY(check_width(width));
   SSM_TRY(check_dtype(io_dtype));
   SSM_TRY(check_view3("x", x, io_dtype));
@@ -208,7 +216,7 @@ int ssm_causal_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int width, i
 }
 
 int64_t ssm_causal_conv_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int width) {
-  if (check_seq(batch, seqlen, dim) != SSM_OK || check_width(width) != SSM_OK) return -1;
+  if (check_conv(batch, seqlen, dim) != SSM_OK || check_width(width) != SSM_OK) return -1;
   return ssm::conv_bwd_workspace_bytes(batch, seqlen, dim, width);
 }
 
@@ -217,7 +225,7 @@ int ssm_causal_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int width, i
                         const int32_t *lengths, int silu, const void *dstate_final, void *dx, float *dweight, float *dbias,
                         void *dstate0, void *workspace, int64_t workspace_bytes, void *hip_stream) {
   ssm::api_clear_error();
-  SSM_TRY(check_seq(batch, seqlen, dim));
+  SSM_TRY(check_conv(batch, seqlen, dim));
   SSM_TRY(check_width(width));
   SSM_TRY(check_dtype(io_dtype));
   SSM_TRY(check_view3("dy", dy, io_dtype));
@@ -238,7 +246,7 @@ int ssm_causal_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int width, i
 int ssm_causal_conv_update(int64_t batch, int64_t dim, int width, int io_dtype, void *state, const ssm_view3 *x,
                            const float *weight, const float *bias, int silu, void *y, void *hip_stream) {
   ssm::api_clear_error();
-  SSM_TRY(check_seq(batch, 1, dim));
+  SSM_TRY(check_conv(batch, 1, dim));
   SSM_TRY(check_width(width));
   SSM_TRY(check_dtype(io_dtype));
   SSM_TRY(check_view3("x", x, io_dtype, false, true));

@@ -13,6 +13,11 @@ namespace {
 struct Gate {
   float a, s, r, o, la2;  // o = 1 - r
 };
+__device__ __forceinline__ float scale_of(float la2, float a) {
+  const float v = 2.0f * kLn2 * la2;
+  const float p = fmaf(v, fmaf(v, fmaf(v, fmaf(v, 1.0f / 120, 1.0f / 24), 1.0f / 6), 0.5f), 1.0f);
+  return __builtin_amdgcn_sqrtf(fabsf(v) < 0.125f ? -v * p : fmaf(-a, a, 1.0f));
+}
 template <bool POWER>
 __device__ __forceinline__ Gate gate_of(float g, float rate2) {
   Gate q;
@@ -20,10 +25,7 @@ __device__ __forceinline__ Gate gate_of(float g, float rate2) {
   if constexpr (POWER) {
     q.la2 = rate2 * q.r;
     q.a = fast_exp2(q.la2);
-    const float v = 2.0f * kLn2 * q.la2;
-    const float p = fmaf(v, fmaf(v, fmaf(v, fmaf(v, 1.0f / 120, 1.0f / 24), 1.0f / 6), 0.5f), 1.0f);
-    const float m = fabsf(v) < 0.125f ? -v * p : fmaf(-q.a, q.a, 1.0f);
-    q.s = __builtin_amdgcn_sqrtf(m);
+    q.s = scale_of(q.la2, q.a);
   } else {
     q.la2 = 0.0f;
     q.a = q.r;
@@ -39,103 +41,411 @@ __device__ __forceinline__ float rate_of(const RecurrenceArgs &a, int64_t c) {
   return POWER ? -a.sharpness * softplus_exact(a.decay[c]) * kLog2e : 0.0f;
 }
 
-template <typename T, bool POWER>
-__global__ void __launch_bounds__(64) recurrence_fwd_kernel(RecurrenceArgs a) {
-  const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
-  if (c >= a.D) return;
-  const float rate2 = rate_of<POWER>(a, c);
-  const int len = row_length(a.lengths, b, a.L);
-  const int64_t K = (a.L + kRecurrenceChunk - 1) / kRecurrenceChunk;
-  float h = a.state0 ? a.state0[b * a.D + c] : 0.0f;
-  for (int64_t t = 0; t < a.L; ++t) {
-    if (a.states && t % kRecurrenceChunk == 0) a.states[(b * K + t / kRecurrenceChunk) * a.D + c] = h;
-    float y = 0.0f;
-    if (t < len) {
-      const Gate q = gate_of<POWER>(load_io((const T *)a.g.p, b * a.g.sb + t * a.g.st + c), rate2);
-      float u = load_io((const T *)a.x.p, b * a.x.sb + t * a.x.st + c), o;
-      if (a.ig.p) {
-        float i;
-        sigmoid_both(load_io((const T *)a.ig.p, b * a.ig.sb + t * a.ig.st + c), i, o);
-        u *= i;
-      }
-      h = a.starts && a.starts[b * a.L + t] ? u : fmaf(q.a, h, q.s * u);
-      y = h;
-      if (a.z.p) y *= silu_f(load_io((const T *)a.z.p, b * a.z.sb + t * a.z.st + c));
-    }
-    store_one((T *)a.y + (b * a.L + t) * a.D + c, y);
+// ---- whole sequences
+//
+// A workgroup takes a chunk of 128 steps of a tile of channels, a wave 16 of the
+// steps, a lane CPL channels.  What a stretch of steps does to the state is an affine
+// map h -> P h + H: a wave forms that of its steps in registers, the workgroup
+// composes its waves' over LDS and hands the chunk's map on in the workspace; with the state
+// before its chunk a wave walks its steps again and writes.  So every input is read
+// once and every output written once.
+//
+// The state before a chunk comes from the workgroups of the chunks before it, all of
+// which have started: a workgroup draws its chunk of the tile from a counter.  It
+// waits for words that hold a value and say that they do, each published by one
+// 64-bit store.  Every `group` chunks a state is published; in between a workgroup
+// composes the maps of the chunks before its own since then, always in the same
+// order, so that results do not depend on who was first.  A wait that is not served
+// within about a second (a workspace written to meanwhile) ends with NaN.
+
+constexpr int kWaves = 8, kSteps = 16;
+static_assert(kWaves * kSteps == kRecurrenceChunk, "a wave takes kSteps steps of a chunk");
+constexpr int kMaxGroup = 2 * kWaves;  // two words per wave: a state and the maps of 15 chunks
+
+// A map whose P is minus zero has met a document's start: h -> H, whatever h is.
+constexpr uint32_t kCleared = 0x80000000u;
+struct Map {
+  float p, h;
+};
+__device__ __forceinline__ bool cleared(float p) { return __float_as_uint(p) == kCleared; }
+__device__ __forceinline__ float apply(const Map &m, float h) { return cleared(m.p) ? m.h : fmaf(m.p, h, m.h); }
+// first, then m
+__device__ __forceinline__ Map compose(const Map &first, const Map &m) { return cleared(m.p) ? m : Map{m.p * first.p, fmaf(m.p, first.h, m.h)}; }
+
+struct Chain {
+  uint32_t tiles, tiles_c;  // tiles of channels, of them a batch row's
+  int chunks, groups, group;  // chunks per published state
+  uint32_t *counter;        // one per tile, 64 bytes apart
+  uint64_t *maps, *states;  // (tiles, chunks, tile's channels), (tiles, groups, tile's channels)
+};
+
+// Words: the upper half is not zero once the word holds something.
+__device__ __forceinline__ void publish(uint64_t *p, uint32_t hi, float lo) {
+  __hip_atomic_store(p, ((uint64_t)hi << 32) | __float_as_uint(lo), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish_map(uint64_t *p, const Map &m) { publish(p, (m.p != m.p ? 0x7fc00000u : __float_as_uint(m.p)) + 1, m.h); }
+__device__ __forceinline__ uint64_t wait_word(const uint64_t *p) {
+  for (int n = 0; n < (1 << 20); ++n) {
+    const uint64_t v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (v >> 32) return v;
+    __builtin_amdgcn_s_sleep(1);
   }
-  if (a.state_final) a.state_final[b * a.D + c] = h;
+  return 0x7fc000017fc00000ull;
+}
+__device__ __forceinline__ Map map_of(uint64_t v) { return {__uint_as_float((uint32_t)(v >> 32) - 1), __uint_as_float((uint32_t)v)}; }
+
+// What lies between the last published state and chunk k (in the order of the
+// walk), composed by the waves two words each; then, after a barrier, applied in order.
+template <int CPL>
+__device__ __forceinline__ void collect(const Chain &n, int64_t tile, int k, int w, int lane, const float (&first)[CPL], Map (*pre)[CPL][64]) {
+  const int g = k / n.group, words = 1 + k - g * n.group;
+  if (2 * w >= words) return;
+#pragma unroll
+  for (int q = 0; q < CPL; ++q) {
+    Map m;
+    const uint64_t *maps = n.maps + (tile * n.chunks + g * n.group) * (64 * CPL) + q * 64 + lane;
+    if (w == 0) {
+      const float h = g == 0 ? first[q] : __uint_as_float((uint32_t)wait_word(n.states + (tile * n.groups + g - 1) * (64 * CPL) + q * 64 + lane));
+      m = {__uint_as_float(kCleared), h};
+    } else {
+      m = map_of(wait_word(maps + (int64_t)(2 * w - 1) * (64 * CPL)));
+    }
+    if (2 * w + 1 < words) m = compose(m, map_of(wait_word(maps + (int64_t)(2 * w) * (64 * CPL))));
+    pre[w][q][lane] = m;
+  }
+}
+template <int CPL>
+__device__ __forceinline__ void collected(const Chain &n, int k, int lane, const Map (*pre)[CPL][64], float (&h)[CPL]) {
+  const int words = 1 + k % n.group;
+#pragma unroll
+  for (int q = 0; q < CPL; ++q) {
+    h[q] = pre[0][q][lane].h;
+    for (int i = 1; 2 * i < words; ++i) h[q] = apply(pre[i][q][lane], h[q]);
+  }
 }
 
-template <typename T, bool POWER>
-__global__ void __launch_bounds__(64) recurrence_bwd_kernel(RecurrenceArgs a) {
-  __shared__ float before[kRecurrenceChunk][64];
-  const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
-  if (c >= a.D) return;
+// A lane's channels of one step as they lie in memory.
+template <typename T, int CPL>
+struct Raw;
+template <>
+struct Raw<float, 1> {
+  float v;
+  __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = v; }
+  static __device__ __forceinline__ void put(char *p, const float (&o)[1]) { *(float *)p = o[0]; }
+};
+template <>
+struct Raw<bf16, 1> {
+  uint16_t v;
+  __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = __uint_as_float((uint32_t)v << 16); }
+  static __device__ __forceinline__ void put(char *p, const float (&o)[1]) { *(uint16_t *)p = (uint16_t)pack_bf16(o[0], o[0]); }
+};
+template <>
+struct Raw<bf16, 2> {
+  uint32_t v;
+  __device__ __forceinline__ void get(float (&o)[2]) const { o[0] = __uint_as_float(v << 16), o[1] = __uint_as_float(v & 0xffff0000u); }
+  static __device__ __forceinline__ void put(char *p, const float (&o)[2]) { *(uint32_t *)p = pack_bf16(o[0], o[1]); }
+};
+
+// The wave's steps of a tensor; steps from L on repeat the last.
+template <typename T, int CPL>
+__device__ __forceinline__ void load_steps(const View3 &v, int64_t b, int64_t t0, int64_t L, uint32_t lane_bytes, Raw<T, CPL> (&r)[kSteps]) {
+  const char *base = (const char *)v.p + b * v.sb * (int64_t)sizeof(T);
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    const int64_t t = t0 + j < L ? t0 + j : L - 1;
+    r[j] = *(const Raw<T, CPL> *)(base + t * v.st * (int64_t)sizeof(T) + lane_bytes);
+  }
+}
+
+// Bit j: a document starts at the wave's step j, before the row's length.
+__device__ __forceinline__ uint32_t start_bits(const uint8_t *starts, int64_t b, int64_t t0, int64_t L, int64_t len, int lane) {
+  if (!starts) return 0;
+  const bool on = lane < kSteps && t0 + lane < len && starts[b * L + t0 + lane] != 0;
+  return (uint32_t)__ballot(on);
+}
+
+// MARKS: document starts or lengths of rows are given.
+template <typename T, int CPL, bool POWER, bool IG, bool Z, bool MARKS>
+__global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceArgs a, Chain n) {
+  __shared__ Map agg[kWaves][CPL][64], pre[kWaves][CPL][64];
+  __shared__ int drawn;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile32 = blockIdx.x % n.tiles;
+  const int64_t tile = tile32, b = tile32 / n.tiles_c;
+  const int64_t c_lane = (int64_t)(tile32 % n.tiles_c) * (64 * CPL) + lane * CPL;
+  const bool on = c_lane < a.D;
+  const int64_t c = on ? c_lane : a.D - CPL;
+  const uint32_t lane_bytes = (uint32_t)(c * sizeof(T));
+  const bool chain = n.chunks > 1;
+  if (chain && threadIdx.x == 0) drawn = (int)atomicAdd(n.counter + tile * 16, 1u);
+  // loads for the chunk that it will almost always be
+  int k = (int)(blockIdx.x / n.tiles);
+  int64_t t0 = (int64_t)k * kRecurrenceChunk + w * kSteps;
+  Raw<T, CPL> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps];
+  auto load = [&] {
+    load_steps<T, CPL>(a.g, b, t0, a.L, lane_bytes, rg);
+    if (IG) load_steps<T, CPL>(a.ig, b, t0, a.L, lane_bytes, ri);
+    load_steps<T, CPL>(a.x, b, t0, a.L, lane_bytes, rx);
+    if (Z) load_steps<T, CPL>(a.z, b, t0, a.L, lane_bytes, rz);
+  };
+  load();
+  float rate2[CPL];
+#pragma unroll
+  for (int q = 0; q < CPL; ++q) rate2[q] = rate_of<POWER>(a, c + q);
+  if (chain) {
+    __syncthreads();
+    const int mine = __builtin_amdgcn_readfirstlane(drawn);
+    if ((uint32_t)mine >= (uint32_t)n.chunks) return;  // (the workspace was written to meanwhile)
+    if (mine != k) {
+      k = mine, t0 = (int64_t)k * kRecurrenceChunk + w * kSteps;
+      load();
+    }
+  }
+  const int64_t len = MARKS ? row_length(a.lengths, b, a.L) : a.L;
+  const int nv = (int)(len - t0 < 0 ? 0 : len - t0 < kSteps ? len - t0 : kSteps);
+  const uint32_t first = MARKS ? start_bits(a.starts, b, t0, a.L, len, lane) : 0;
+
+  float da[kSteps][CPL], in[kSteps][CPL];
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    float g[CPL], x[CPL], i[CPL];
+    rg[j].get(g);
+    rx[j].get(x);
+    if (IG) ri[j].get(i);
+#pragma unroll
+    for (int q = 0; q < CPL; ++q) {
+      Gate t = gate_of<POWER>(g[q], rate2[q]);
+      if (MARKS && (first >> j & 1)) t.a = 0.0f, t.s = 1.0f;
+      da[j][q] = t.a;
+      in[j][q] = t.s * (IG ? x[q] * sigmoid_f(i[q]) : x[q]);
+    }
+  }
+  if (nv < kSteps)
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j)
+      if (j >= nv)
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) da[j][q] = 1.0f, in[j][q] = 0.0f;
+#pragma unroll
+  for (int q = 0; q < CPL; ++q) {
+    Map m = {1.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      m.h = MARKS && (first >> j & 1) ? in[j][q] : fmaf(da[j][q], m.h, in[j][q]);
+      m.p *= da[j][q];
+    }
+    if (MARKS && first) m.p = __uint_as_float(kCleared);
+    agg[w][q][lane] = m;
+  }
+  float h0[CPL];  // the state before the first chunk
+#pragma unroll
+  for (int q = 0; q < CPL; ++q) h0[q] = a.state0 && k < n.group ? a.state0[b * a.D + c + q] : 0.0f;
+  __syncthreads();
+  Map before[CPL];  // what the waves before this one do
+#pragma unroll
+  for (int q = 0; q < CPL; ++q) {
+    before[q] = {1.0f, 0.0f};
+    for (int i = 0; i < w; ++i) before[q] = compose(before[q], agg[i][q][lane]);
+  }
+  const bool last = (k + 1) % n.group == 0, more = k + 1 < n.chunks;
+  if (more && !last && w == kWaves - 1)
+#pragma unroll
+    for (int q = 0; q < CPL; ++q) publish_map(n.maps + (tile * n.chunks + k) * (64 * CPL) + q * 64 + lane, compose(before[q], agg[w][q][lane]));
+  float h[CPL];
+  if (chain) {
+    collect<CPL>(n, tile, k, w, lane, h0, pre);
+    __syncthreads();
+    collected<CPL>(n, k, lane, pre, h);
+  } else {
+#pragma unroll
+    for (int q = 0; q < CPL; ++q) h[q] = h0[q];
+  }
+  if (a.states && w == 0 && on)
+#pragma unroll
+    for (int q = 0; q < CPL; ++q) a.states[(b * n.chunks + k) * a.D + c + q] = h[q];
+#pragma unroll
+  for (int q = 0; q < CPL; ++q) {
+    h[q] = apply(before[q], h[q]);
+    if (w == kWaves - 1) {
+      const float end = apply(agg[w][q][lane], h[q]);
+      if (more && last) publish(n.states + (tile * n.groups + k / n.group) * (64 * CPL) + q * 64 + lane, 1, end);
+      if (!more && a.state_final && on) a.state_final[b * a.D + c + q] = end;
+    }
+  }
+  char *y = (char *)a.y + (b * a.L + t0) * a.D * (int64_t)sizeof(T) + lane_bytes;
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    float o[CPL];
+    if (Z) rz[j].get(o);
+#pragma unroll
+    for (int q = 0; q < CPL; ++q) {
+      h[q] = MARKS && (first >> j & 1) ? in[j][q] : fmaf(da[j][q], h[q], in[j][q]);
+      o[q] = Z ? h[q] * silu_f(o[q]) : h[q];
+      if (MARKS && j >= nv) o[q] = 0.0f;
+    }
+    if (on && t0 + j < a.L) Raw<T, CPL>::put(y + j * a.D * (int64_t)sizeof(T), o);
+  }
+}
+
+// Backward: the chunks in reverse, w_t = e_t + a_{t+1} w_{t+1}.  What flows from step t
+// to t - 1 is q = a_t w_t, and a stretch of steps is q -> P q + Q with the P of the
+// forward map.  The states inside a chunk are formed again from the one before it, its
+// maps and those of the adjoint in one exchange.  For a step's gradients a lane keeps
+// log2 a (power form; its sigmoid is log2 a over rate2, its scale is formed again) or 1 - a.
+template <typename T, bool POWER, bool IG, bool Z, bool MARKS>
+__global__ void __launch_bounds__(64 * kWaves) recurrence_bwd_kernel(RecurrenceArgs a, Chain n, float *part) {
+  __shared__ Map agg[kWaves][1][64], pre[kWaves][1][64];
+  __shared__ float back[kWaves][64];
+  __shared__ int drawn;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile32 = blockIdx.x % n.tiles;
+  const int64_t tile = tile32, b = tile32 / n.tiles_c;
+  const int64_t c_lane = (int64_t)(tile32 % n.tiles_c) * 64 + lane;
+  const bool on = c_lane < a.D;
+  const int64_t c = on ? c_lane : a.D - 1;
+  const uint32_t lane_bytes = (uint32_t)(c * sizeof(T));
+  const bool chain = n.chunks > 1;
+  if (chain && threadIdx.x == 0) drawn = (int)atomicAdd(n.counter + tile * 16, 1u);
+  int kr = (int)(blockIdx.x / n.tiles), k = n.chunks - 1 - kr;
+  int64_t t0 = (int64_t)k * kRecurrenceChunk + w * kSteps;
+  Raw<T, 1> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps], rd[kSteps];
+  auto load = [&] {
+    load_steps<T, 1>(a.g, b, t0, a.L, lane_bytes, rg);
+    if (IG) load_steps<T, 1>(a.ig, b, t0, a.L, lane_bytes, ri);
+    load_steps<T, 1>(a.x, b, t0, a.L, lane_bytes, rx);
+    load_steps<T, 1>(a.dy, b, t0, a.L, lane_bytes, rd);
+    if (Z) load_steps<T, 1>(a.z, b, t0, a.L, lane_bytes, rz);
+  };
+  load();
   const float rate2 = rate_of<POWER>(a, c);
-  const int len = row_length(a.lengths, b, a.L);
-  const int64_t K = (a.L + kRecurrenceChunk - 1) / kRecurrenceChunk;
-  float w = a.dstate_final ? a.dstate_final[b * a.D + c] : 0.0f, acc = 0.0f;
-  for (int64_t k = K - 1; k >= 0; --k) {
-    const int64_t t0 = k * kRecurrenceChunk, t1 = t0 + kRecurrenceChunk < a.L ? t0 + kRecurrenceChunk : a.L;
-    float h = a.states[(b * K + k) * a.D + c];
-    for (int64_t t = t0; t < t1; ++t) {
-      before[t - t0][threadIdx.x] = h;
-      if (t < len) {
-        const Gate q = gate_of<POWER>(load_io((const T *)a.g.p, b * a.g.sb + t * a.g.st + c), rate2);
-        float u = load_io((const T *)a.x.p, b * a.x.sb + t * a.x.st + c), i, o;
-        if (a.ig.p) {
-          sigmoid_both(load_io((const T *)a.ig.p, b * a.ig.sb + t * a.ig.st + c), i, o);
-          u *= i;
-        }
-        h = a.starts && a.starts[b * a.L + t] ? u : fmaf(q.a, h, q.s * u);
-      }
-    }
-    for (int64_t t = t1 - 1; t >= t0; --t) {
-      const int64_t out = (b * a.L + t) * a.D + c;
-      float dx = 0.0f, dg = 0.0f, dig = 0.0f, dz = 0.0f;
-      if (t < len) {
-        Gate q = gate_of<POWER>(load_io((const T *)a.g.p, b * a.g.sb + t * a.g.st + c), rate2);
-        const float x = load_io((const T *)a.x.p, b * a.x.sb + t * a.x.st + c);
-        float i = 1.0f, o = 0.0f;
-        if (a.ig.p) sigmoid_both(load_io((const T *)a.ig.p, b * a.ig.sb + t * a.ig.st + c), i, o);
-        const bool first = a.starts && a.starts[b * a.L + t];
-        if (first) q.a = 0.0f, q.s = 1.0f;
-        const float u = i * x, hp = before[t - t0][threadIdx.x];
-        float e = load_io((const T *)a.dy.p, b * a.dy.sb + t * a.dy.st + c);
-        if (a.z.p) {
-          float f, df;
-          silu_both(load_io((const T *)a.z.p, b * a.z.sb + t * a.z.st + c), f, df);
-          dz = e * (first ? u : fmaf(q.a, hp, q.s * u)) * df;
-          e *= f;
-        }
-        w += e;
-        const float ws = w * q.s;
-        dx = ws * i;
-        dig = ws * u * o;
-        if (!first) {
-          if constexpr (POWER) {
-            const float la = kLn2 * q.la2;
-            const float f = w * q.a * (la * hp - u * q.a * (q.s > 0.0f ? la * fast_rcp(q.s) : 0.0f));
-            acc += f;
-            dg = f * q.o;
-          } else {
-            dg = w * q.a * q.s * (hp - u);
-          }
-        }
-        w = first ? 0.0f : q.a * w;
-      }
-      store_one((T *)a.dx + out, dx);
-      store_one((T *)a.dg + out, dg);
-      if (a.dig) store_one((T *)a.dig + out, dig);
-      if (a.dz) store_one((T *)a.dz + out, dz);
+  if (chain) {
+    __syncthreads();
+    const int mine = __builtin_amdgcn_readfirstlane(drawn);
+    if ((uint32_t)mine >= (uint32_t)n.chunks) return;  // (the workspace was written to meanwhile)
+    if (mine != kr) {
+      kr = mine, k = n.chunks - 1 - kr, t0 = (int64_t)k * kRecurrenceChunk + w * kSteps;
+      load();
     }
   }
-  if (a.dstate0) a.dstate0[b * a.D + c] = w;
-  if constexpr (POWER) {
-    const float v = a.decay[c], sp = softplus_exact(v);  // sigmoid / softplus goes to 1 where both vanish
-    ((float *)a.workspace)[b * a.D + c] = acc * (v < -40.0f ? 1.0f : sigmoid_f(v) / sp);
+  const int64_t len = MARKS ? row_length(a.lengths, b, a.L) : a.L;
+  const int nv = (int)(len - t0 < 0 ? 0 : len - t0 < kSteps ? len - t0 : kSteps);
+  const uint32_t first = MARKS ? start_bits(a.starts, b, t0, a.L, len, lane) : 0;
+  float h = a.states[(b * n.chunks + k) * a.D + c];
+
+  // keep: log2 a or 1 - a; steps behind the end: a = 1, nothing comes in
+  float da[kSteps], keep[kSteps], in[kSteps], ii[kSteps], xs[kSteps], dys[kSteps], zs[kSteps];
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    float g[1], v[1];
+    rg[j].get(g);
+    const Gate t = gate_of<POWER>(g[0], rate2);
+    da[j] = t.a, keep[j] = POWER ? t.la2 : t.o;
+    rx[j].get(v), xs[j] = v[0];
+    rd[j].get(v), dys[j] = v[0];
+    if (Z) rz[j].get(v), zs[j] = v[0];
+    ii[j] = 1.0f;
+    if (IG) ri[j].get(v), ii[j] = sigmoid_f(v[0]);
+    float s = t.s;
+    if (MARKS && (first >> j & 1)) da[j] = 0.0f, s = 1.0f;
+    in[j] = s * (ii[j] * xs[j]);
   }
+  if (nv < kSteps)
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j)
+      if (j >= nv) da[j] = 1.0f, keep[j] = in[j] = ii[j] = xs[j] = dys[j] = zs[j] = 0.0f;
+  Map m = {1.0f, 0.0f};
+  float q = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    m.h = MARKS && (first >> j & 1) ? in[j] : fmaf(da[j], m.h, in[j]);
+    m.p *= da[j];
+  }
+#pragma unroll
+  for (int j = kSteps - 1; j >= 0; --j) q = MARKS && (first >> j & 1) ? 0.0f : da[j] * ((Z ? dys[j] * silu_f(zs[j]) : dys[j]) + q);
+  if (MARKS && first) m.p = __uint_as_float(kCleared);
+  agg[w][0][lane] = m;
+  back[w][lane] = q;
+  const float q0[1] = {a.dstate_final && kr < n.group ? a.dstate_final[b * a.D + c] : 0.0f};
+  __syncthreads();
+  for (int i = 0; i < w; ++i) h = apply(agg[i][0][lane], h);
+  Map after = {1.0f, 0.0f};  // what the waves behind this one do
+  for (int i = kWaves - 1; i > w; --i) after = compose(after, Map{agg[i][0][lane].p, back[i][lane]});
+  const bool last = (kr + 1) % n.group == 0, more = kr + 1 < n.chunks;
+  if (more && !last && w == 0) publish_map(n.maps + (tile * n.chunks + kr) * 64 + lane, compose(after, Map{m.p, q}));
+  float from[1] = {q0[0]};
+  if (chain) {
+    collect<1>(n, tile, kr, w, lane, q0, pre);
+    __syncthreads();
+    collected<1>(n, kr, lane, pre, from);
+  }
+  q = apply(after, from[0]);
+  if (w == 0) {
+    const float end = apply(Map{m.p, back[0][lane]}, q);
+    if (more && last) publish(n.states + (tile * n.groups + kr / n.group) * 64 + lane, 1, end);
+    if (!more && a.dstate0 && on) a.dstate0[b * a.D + c] = end;
+  }
+  // in[j] becomes the state before step j
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    const float next = MARKS && (first >> j & 1) ? in[j] : fmaf(da[j], h, in[j]);
+    in[j] = h;
+    h = next;
+  }
+  const int64_t row0 = ((b * a.L + t0) * a.D) * (int64_t)sizeof(T) + lane_bytes;
+  // (a rate whose reciprocal leaves fp32 has no gradient either)
+  const float over = POWER && rate2 < -0x1p-120f ? fast_rcp(rate2) : 0.0f;
+  float sum = 0.0f;
+#pragma unroll
+  for (int j = kSteps - 1; j >= 0; --j) {
+    const bool start = MARKS && (first >> j & 1);
+    float dz[1] = {0.0f}, e = dys[j];
+    if (Z) {
+      float f, df;
+      silu_both(zs[j], f, df);
+      dz[0] = e * h * df;
+      e *= f;
+    }
+    h = in[j];
+    const float wt = e + q, u = ii[j] * xs[j];
+    float s, dg[1];
+    if constexpr (POWER) {
+      s = scale_of(keep[j], da[j]);
+      const float la = kLn2 * keep[j];
+      const float f = start ? 0.0f : wt * da[j] * (la * h - u * da[j] * (s > 0.0f ? la * fast_rcp(s) : 0.0f));
+      if (start) s = 1.0f;
+      sum += f;
+      dg[0] = f * fmaf(-keep[j], over, 1.0f);
+    } else {
+      s = start ? 1.0f : keep[j];
+      dg[0] = start ? 0.0f : wt * da[j] * s * (h - u);
+    }
+    const float ws = wt * s;
+    float dx[1] = {ws * ii[j]}, di[1] = {ws * u * (1.0f - ii[j])};
+    q = start ? 0.0f : da[j] * wt;
+    if (MARKS && j >= nv) dx[0] = dg[0] = di[0] = dz[0] = 0.0f;
+    if (on && t0 + j < a.L) {
+      const int64_t row = row0 + j * a.D * (int64_t)sizeof(T);
+      Raw<T, 1>::put((char *)a.dx + row, dx);
+      Raw<T, 1>::put((char *)a.dg + row, dg);
+      if (IG) Raw<T, 1>::put((char *)a.dig + row, di);
+      if (Z) Raw<T, 1>::put((char *)a.dz + row, dz);
+    }
+  }
+  if constexpr (POWER) {  // the chunk's part of ddecay, waves in order
+    __syncthreads();
+    back[w][lane] = sum;
+    __syncthreads();
+    if (w == 0 && on) {
+      sum = 0.0f;
+      for (int i = 0; i < kWaves; ++i) sum += back[i][lane];
+      const float v = a.decay[c];  // sigmoid / softplus goes to 1 where both vanish
+      part[(b * n.chunks + k) * a.D + c] = sum * (v < -40.0f ? 1.0f : sigmoid_f(v) / softplus_exact(v));
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) recurrence_clear_kernel(uint4 *p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = make_uint4(0, 0, 0, 0);
 }
 
 // One token: 8 channels per lane.
@@ -161,25 +471,75 @@ __global__ void __launch_bounds__(256) recurrence_update_kernel(RecurrenceUpdate
   store_vec((T *)a.y + b * a.D + c, x);
 }
 
-template <typename T>
-hipError_t fwd(const RecurrenceArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.D + 63) / 64), (unsigned)a.B);
-  if (a.decay)
-    hipLaunchKernelGGL((recurrence_fwd_kernel<T, true>), grid, dim3(64), 0, s, a);
-  else
-    hipLaunchKernelGGL((recurrence_fwd_kernel<T, false>), grid, dim3(64), 0, s, a);
+template <int X>
+struct Int {
+  static constexpr int v = X;
+};
+// Calls f with the four switches as integral constants.
+template <typename F>
+hipError_t by_switches(bool power, bool ig, bool z, bool marks, F f) {
+  auto m = [&](auto p, auto i, auto zz) { return marks ? f(p, i, zz, Int<1>{}) : f(p, i, zz, Int<0>{}); };
+  auto l = [&](auto p, auto i) { return z ? m(p, i, Int<1>{}) : m(p, i, Int<0>{}); };
+  auto o = [&](auto p) { return ig ? l(p, Int<1>{}) : l(p, Int<0>{}); };
+  return power ? o(Int<1>{}) : o(Int<0>{});
+}
+
+#ifndef GROUP
+#define GROUP 4
+#endif
+int group_of(int64_t, int64_t) { return GROUP; }
+
+// cpl: channels per lane
+Chain chain_of(int64_t B, int64_t L, int64_t D, int cpl, void *workspace) {
+  Chain n;
+  n.tiles_c = (uint32_t)((D + 64 * cpl - 1) / (64 * cpl));
+  n.tiles = (uint32_t)B * n.tiles_c;
+  n.chunks = (int)((L + kRecurrenceChunk - 1) / kRecurrenceChunk);
+  n.group = group_of(n.chunks, n.tiles);
+  n.groups = (n.chunks + n.group - 1) / n.group;
+  n.counter = (uint32_t *)workspace;
+  n.states = (uint64_t *)((char *)workspace + (int64_t)n.tiles * 64);
+  n.maps = n.states + (int64_t)n.tiles * n.groups * 64 * cpl;
+  return n;
+}
+int64_t chain_bytes(const Chain &n, int cpl) {
+  return n.chunks == 1 ? 0 : (int64_t)n.tiles * (64 + (int64_t)(n.groups + (n.group > 1 ? n.chunks : 0)) * 64 * cpl * 8);
+}
+hipError_t clear(void *p, int64_t bytes, hipStream_t s) {
+  const int64_t n = bytes / 16, grid = (n + 255) / 256;
+  hipLaunchKernelGGL(recurrence_clear_kernel, dim3((unsigned)(grid < 2048 ? grid : 2048)), dim3(256), 0, s, (uint4 *)p, n);
   return hipGetLastError();
+}
+
+template <typename T, int CPL>
+hipError_t fwd(const RecurrenceArgs &a, hipStream_t s) {
+  const Chain n = chain_of(a.B, a.L, a.D, CPL, a.workspace);
+  if (n.chunks > 1) {
+    const hipError_t e = clear(a.workspace, chain_bytes(n, CPL), s);
+    if (e != hipSuccess) return e;
+  }
+  return by_switches(a.decay, a.ig.p, a.z.p, a.starts || a.lengths, [&](auto p, auto i, auto z, auto m) {
+    hipLaunchKernelGGL((recurrence_fwd_kernel<T, CPL, decltype(p)::v, decltype(i)::v, decltype(z)::v, decltype(m)::v>), dim3(n.tiles * n.chunks),
+                       dim3(64 * kWaves), 0, s, a, n);
+    return hipGetLastError();
+  });
 }
 
 template <typename T>
 hipError_t bwd(const RecurrenceArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.D + 63) / 64), (unsigned)a.B);
-  if (a.decay)
-    hipLaunchKernelGGL((recurrence_bwd_kernel<T, true>), grid, dim3(64), 0, s, a);
-  else
-    hipLaunchKernelGGL((recurrence_bwd_kernel<T, false>), grid, dim3(64), 0, s, a);
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess && a.decay ? launch_sum_rows((const float *)a.workspace, a.B, a.D, a.D, a.ddecay, nullptr, s) : e;
+  const Chain n = chain_of(a.B, a.L, a.D, 1, a.workspace);
+  const int64_t bytes = chain_bytes(n, 1);
+  float *part = (float *)((char *)a.workspace + bytes);
+  if (n.chunks > 1) {
+    const hipError_t e = clear(a.workspace, bytes, s);
+    if (e != hipSuccess) return e;
+  }
+  const hipError_t e = by_switches(a.decay, a.ig.p, a.z.p, a.starts || a.lengths, [&](auto p, auto i, auto z, auto m) {
+    hipLaunchKernelGGL((recurrence_bwd_kernel<T, decltype(p)::v, decltype(i)::v, decltype(z)::v, decltype(m)::v>), dim3(n.tiles * n.chunks),
+                       dim3(64 * kWaves), 0, s, a, n, part);
+    return hipGetLastError();
+  });
+  return e == hipSuccess && a.decay ? launch_sum_rows(part, a.B * n.chunks, a.D, a.D, a.ddecay, nullptr, s) : e;
 }
 
 template <typename T>
@@ -194,11 +554,17 @@ hipError_t update(const RecurrenceUpdateArgs &a, hipStream_t s) {
 
 }  // namespace
 
-int64_t recurrence_fwd_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
-int64_t recurrence_bwd_workspace_bytes(int64_t B, int64_t, int64_t D) { return B * D * 4; }
+int64_t recurrence_fwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int io_dtype) {
+  const int cpl = io_dtype == 0 ? 1 : 2;
+  return chain_bytes(chain_of(B, L, D, cpl, nullptr), cpl);
+}
+int64_t recurrence_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D) {
+  const Chain n = chain_of(B, L, D, 1, nullptr);
+  return chain_bytes(n, 1) + B * n.chunks * D * 4;
+}
 
 hipError_t launch_recurrence_fwd(const RecurrenceArgs &a, int io_dtype, hipStream_t s) {
-  return io_dtype == 0 ? fwd<float>(a, s) : fwd<bf16>(a, s);
+  return io_dtype == 0 ? fwd<float, 1>(a, s) : fwd<bf16, 2>(a, s);
 }
 hipError_t launch_recurrence_bwd(const RecurrenceArgs &a, int io_dtype, hipStream_t s) {
   return io_dtype == 0 ? bwd<float>(a, s) : bwd<bf16>(a, s);
