@@ -144,7 +144,7 @@ int ssm_gated_recurrence_fwd(int64_t batch, int64_t seqlen, int64_t dim, int io_
 
 int64_t ssm_gated_recurrence_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io_dtype) {
   if (check_recurrence(batch, seqlen, dim) != SSM_OK || check_dtype(io_dtype) != SSM_OK) return -1;
-  return ssm::recurrence_bwd_workspace_bytes(batch, seqlen, dim);
+  return ssm::recurrence_bwd_workspace_bytes(batch, seqlen, dim, io_dtype);
 }
 
 int ssm_gated_recurrence_bwd(int64_t batch, int64_t seqlen, int64_t dim, int io_dtype, const ssm_view3 *dy, const ssm_view3 *x,
@@ -169,7 +169,7 @@ int ssm_gated_recurrence_bwd(int64_t batch, int64_t seqlen, int64_t dim, int io_
   if ((input_gate == nullptr) != (dinput_gate == nullptr)) return api_fail(SSM_ERR_NULL_ARG, "dinput_gate must be given if and only if input_gate is");
   if ((z == nullptr) != (dz == nullptr)) return api_fail(SSM_ERR_NULL_ARG, "dz must be given if and only if z is");
   if ((decay == nullptr) != (ddecay == nullptr)) return api_fail(SSM_ERR_NULL_ARG, "ddecay must be given if and only if decay is");
-  SSM_TRY(check_workspace(workspace, workspace_bytes, ssm::recurrence_bwd_workspace_bytes(batch, seqlen, dim)));
+  SSM_TRY(check_workspace(workspace, workspace_bytes, ssm::recurrence_bwd_workspace_bytes(batch, seqlen, dim, io_dtype)));
   ssm::RecurrenceArgs a{};
   a.B = batch, a.L = seqlen, a.D = dim, a.x = view(x), a.g = view(decay_gate), a.ig = view(input_gate), a.z = view(z), a.dy = view(dy);
   a.decay = decay, a.sharpness = sharpness, a.states = const_cast<float *>(states), a.starts = starts, a.lengths = lengths;

@@ -78,7 +78,7 @@ struct HeadNormArgs {
 };
 
 int64_t recurrence_fwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int io_dtype);
-int64_t recurrence_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D);
+int64_t recurrence_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int io_dtype);
 int64_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int width);
 int64_t head_norm_bwd_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d);
 

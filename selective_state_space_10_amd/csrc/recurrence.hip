@@ -34,12 +34,18 @@ __device__ __forceinline__ Gate gate_of(float g, float rate2) {
   return q;
 }
 
-__device__ __forceinline__ float softplus_exact(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
-// log2 of the smallest decay
-template <bool POWER>
-__device__ __forceinline__ float rate_of(const RecurrenceArgs &a, int64_t c) {
-  return POWER ? -a.sharpness * softplus_exact(a.decay[c]) * kLog2e : 0.0f;
+// softplus to fp32's rounding: e^-|v| by the exponent's rounded product and what that
+// leaves out, log1p by the logarithm of the rounded 1 + w and what that leaves out.
+__device__ __forceinline__ float softplus_full(float v) {
+  const float m = -fabsf(v), t = m * kLog2e;
+  const float rest = fmaf(m, kLog2e, -t) + m * 1.9259629911266175e-8f;  // log2 e = kLog2e + 1.93e-8
+  float w = fast_exp2(t);
+  w = fmaf(w, rest * kLn2, w);
+  const float u = 1.0f + w;
+  return fmaxf(v, 0.0f) + (fast_log2(u) * kLn2 - ((u - 1.0f) - w));
 }
+// log2 of the smallest decay, of the parameter v
+__device__ __forceinline__ float rate_of(float sharpness, float v) { return -sharpness * kLog2e * softplus_full(v); }
 
 // ---- whole sequences
 //
@@ -61,6 +67,9 @@ __device__ __forceinline__ float rate_of(const RecurrenceArgs &a, int64_t c) {
 constexpr int kWaves = 8, kSteps = 16;
 static_assert(kWaves * kSteps == kRecurrenceChunk, "a wave takes kSteps steps of a chunk");
 constexpr int kMaxGroup = 2 * kWaves;  // two words per wave: a state and the maps of 15 chunks
+
+// A value that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ int uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
 
 // A map whose P is minus zero has met a document's start: h -> H, whatever h is.
 constexpr uint32_t kCleared = 0x80000000u;
@@ -85,6 +94,7 @@ __device__ __forceinline__ void publish(uint64_t *p, uint32_t hi, float lo) {
 }
 __device__ __forceinline__ void publish_map(uint64_t *p, const Map &m) { publish(p, (m.p != m.p ? 0x7fc00000u : __float_as_uint(m.p)) + 1, m.h); }
 __device__ __forceinline__ uint64_t wait_word(const uint64_t *p) {
+#pragma unroll 1
   for (int n = 0; n < (1 << 20); ++n) {
     const uint64_t v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (v >> 32) return v;
@@ -120,45 +130,64 @@ __device__ __forceinline__ void collected(const Chain &n, int k, int lane, const
 #pragma unroll
   for (int q = 0; q < CPL; ++q) {
     h[q] = pre[0][q][lane].h;
+#pragma unroll 1
     for (int i = 1; 2 * i < words; ++i) h[q] = apply(pre[i][q][lane], h[q]);
   }
 }
 
-// A lane's channels of one step as they lie in memory.
+// A lane's channels of one step as they lie in memory, at a byte offset of a buffer.
+// A buffer is the wave's steps of a tensor: an address is a base and a step's offset in
+// scalar registers and the lane's offset in one vector register, and what is read or
+// written behind the last step (or by a lane whose offset is kNoLane) is zero or dropped.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr uint32_t kNoLane = 0x80000000u;
+__device__ __forceinline__ Buffer buffer_of(const void *p, int64_t offset, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((char *)p + offset, 0, bytes, 0x00027000);
+}
 template <typename T, int CPL>
 struct Raw;
 template <>
 struct Raw<float, 1> {
-  float v;
-  __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = v; }
-  static __device__ __forceinline__ void put(char *p, const float (&o)[1]) { *(float *)p = o[0]; }
+  uint32_t v;
+  __device__ __forceinline__ void load(Buffer p, uint32_t lane, uint32_t step) { v = __builtin_amdgcn_raw_buffer_load_b32(p, lane, step, 0); }
+  __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = __uint_as_float(v); }
+  static __device__ __forceinline__ void put(Buffer p, uint32_t lane, uint32_t step, const float (&o)[1]) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o[0]), p, lane, step, 0);
+  }
 };
 template <>
 struct Raw<bf16, 1> {
   uint16_t v;
+  __device__ __forceinline__ void load(Buffer p, uint32_t lane, uint32_t step) { v = __builtin_amdgcn_raw_buffer_load_b16(p, lane, step, 0); }
   __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = __uint_as_float((uint32_t)v << 16); }
-  static __device__ __forceinline__ void put(char *p, const float (&o)[1]) { *(uint16_t *)p = (uint16_t)pack_bf16(o[0], o[0]); }
+  static __device__ __forceinline__ void put(Buffer p, uint32_t lane, uint32_t step, const float (&o)[1]) {
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(o[0], o[0]), p, lane, step, 0);
+  }
 };
 template <>
 struct Raw<bf16, 2> {
   uint32_t v;
+  __device__ __forceinline__ void load(Buffer p, uint32_t lane, uint32_t step) { v = __builtin_amdgcn_raw_buffer_load_b32(p, lane, step, 0); }
   __device__ __forceinline__ void get(float (&o)[2]) const { o[0] = __uint_as_float(v << 16), o[1] = __uint_as_float(v & 0xffff0000u); }
-  static __device__ __forceinline__ void put(char *p, const float (&o)[2]) { *(uint32_t *)p = pack_bf16(o[0], o[1]); }
+  static __device__ __forceinline__ void put(Buffer p, uint32_t lane, uint32_t step, const float (&o)[2]) {
+    __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(o[0], o[1]), p, lane, step, 0);
+  }
 };
 
-// The wave's steps of a tensor; steps from L on repeat the last.
+// Of the wave's steps, those before the end of the sequence.
+__device__ __forceinline__ int rows_of(int t0, int L) { return L - t0 < 0 ? 0 : L - t0 < kSteps ? L - t0 : kSteps; }
+
+// The wave's steps of a tensor; a step's stride and 16 of them stay below 2^29 bytes.
 template <typename T, int CPL>
-__device__ __forceinline__ void load_steps(const View3 &v, int64_t b, int64_t t0, int64_t L, uint32_t lane_bytes, Raw<T, CPL> (&r)[kSteps]) {
-  const char *base = (const char *)v.p + b * v.sb * (int64_t)sizeof(T);
+__device__ __forceinline__ void load_steps(const View3 &v, int D, int64_t b, int t0, int rows, uint32_t lane_bytes, Raw<T, CPL> (&r)[kSteps]) {
+  const int step = (int)v.st * (int)sizeof(T);
+  const Buffer p = buffer_of(v.p, (b * v.sb + t0 * v.st) * (int64_t)sizeof(T), rows ? (rows - 1) * step + D * (int)sizeof(T) : 0);
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j) {
-    const int64_t t = t0 + j < L ? t0 + j : L - 1;
-    r[j] = *(const Raw<T, CPL> *)(base + t * v.st * (int64_t)sizeof(T) + lane_bytes);
-  }
+  for (int j = 0; j < kSteps; ++j) r[j].load(p, lane_bytes, j * step);
 }
 
 // Bit j: a document starts at the wave's step j, before the row's length.
-__device__ __forceinline__ uint32_t start_bits(const uint8_t *starts, int64_t b, int64_t t0, int64_t L, int64_t len, int lane) {
+__device__ __forceinline__ uint32_t start_bits(const uint8_t *starts, int64_t b, int t0, int L, int len, int lane) {
   if (!starts) return 0;
   const bool on = lane < kSteps && t0 + lane < len && starts[b * L + t0 + lane] != 0;
   return (uint32_t)__ballot(on);
@@ -169,41 +198,44 @@ template <typename T, int CPL, bool POWER, bool IG, bool Z, bool MARKS>
 __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceArgs a, Chain n) {
   __shared__ Map agg[kWaves][CPL][64], pre[kWaves][CPL][64];
   __shared__ int drawn;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tile32 = blockIdx.x % n.tiles;
-  const int64_t tile = tile32, b = tile32 / n.tiles_c;
-  const int64_t c_lane = (int64_t)(tile32 % n.tiles_c) * (64 * CPL) + lane * CPL;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const uint32_t tile32 = uniform(blockIdx.x % n.tiles), b32 = uniform(tile32 / n.tiles_c);
+  const int64_t tile = tile32, b = b32;
+  const int64_t c_lane = (int64_t)(tile32 - b32 * n.tiles_c) * (64 * CPL) + lane * CPL;
   const bool on = c_lane < a.D;
   const int64_t c = on ? c_lane : a.D - CPL;
   const uint32_t lane_bytes = (uint32_t)(c * sizeof(T));
   const bool chain = n.chunks > 1;
+  const int D = (int)a.D, L = (int)a.L;  // (both below 2^30: a launch's workgroups)
   if (chain && threadIdx.x == 0) drawn = (int)atomicAdd(n.counter + tile * 16, 1u);
   // loads for the chunk that it will almost always be
-  int k = (int)(blockIdx.x / n.tiles);
-  int64_t t0 = (int64_t)k * kRecurrenceChunk + w * kSteps;
+  int k = uniform(blockIdx.x / n.tiles);
+  int t0 = k * kRecurrenceChunk + w * kSteps;
   Raw<T, CPL> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps];
   auto load = [&] {
-    load_steps<T, CPL>(a.g, b, t0, a.L, lane_bytes, rg);
-    if (IG) load_steps<T, CPL>(a.ig, b, t0, a.L, lane_bytes, ri);
-    load_steps<T, CPL>(a.x, b, t0, a.L, lane_bytes, rx);
-    if (Z) load_steps<T, CPL>(a.z, b, t0, a.L, lane_bytes, rz);
+    const int rows = rows_of(t0, L);
+    load_steps<T, CPL>(a.g, D, b, t0, rows, lane_bytes, rg);
+    if (IG) load_steps<T, CPL>(a.ig, D, b, t0, rows, lane_bytes, ri);
+    load_steps<T, CPL>(a.x, D, b, t0, rows, lane_bytes, rx);
+    if (Z) load_steps<T, CPL>(a.z, D, b, t0, rows, lane_bytes, rz);
   };
-  load();
   float rate2[CPL];
 #pragma unroll
-  for (int q = 0; q < CPL; ++q) rate2[q] = rate_of<POWER>(a, c + q);
+  for (int q = 0; q < CPL; ++q) rate2[q] = POWER ? a.decay[c + q] : 0.0f;
+  load();
+#pragma unroll
+  for (int q = 0; q < CPL; ++q) rate2[q] = POWER ? rate_of(a.sharpness, rate2[q]) : 0.0f;
   if (chain) {
     __syncthreads();
-    const int mine = __builtin_amdgcn_readfirstlane(drawn);
+    const int mine = uniform(drawn);
     if ((uint32_t)mine >= (uint32_t)n.chunks) return;  // (the workspace was written to meanwhile)
     if (mine != k) {
-      k = mine, t0 = (int64_t)k * kRecurrenceChunk + w * kSteps;
+      k = mine, t0 = k * kRecurrenceChunk + w * kSteps;
       load();
     }
   }
-  const int64_t len = MARKS ? row_length(a.lengths, b, a.L) : a.L;
-  const int nv = (int)(len - t0 < 0 ? 0 : len - t0 < kSteps ? len - t0 : kSteps);
-  const uint32_t first = MARKS ? start_bits(a.starts, b, t0, a.L, len, lane) : 0;
+  const int len = MARKS ? uniform(row_length(a.lengths, b, L)) : L, nv = rows_of(t0, len);
+  const uint32_t first = MARKS ? start_bits(a.starts, b, t0, L, len, lane) : 0;
 
   float da[kSteps][CPL], in[kSteps][CPL];
 #pragma unroll
@@ -245,6 +277,7 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
 #pragma unroll
   for (int q = 0; q < CPL; ++q) {
     before[q] = {1.0f, 0.0f};
+#pragma unroll 1
     for (int i = 0; i < w; ++i) before[q] = compose(before[q], agg[i][q][lane]);
   }
   const bool last = (k + 1) % n.group == 0, more = k + 1 < n.chunks;
@@ -272,7 +305,9 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
       if (!more && a.state_final && on) a.state_final[b * a.D + c + q] = end;
     }
   }
-  char *y = (char *)a.y + (b * a.L + t0) * a.D * (int64_t)sizeof(T) + lane_bytes;
+  const int row = D * (int)sizeof(T);
+  const Buffer y = buffer_of(a.y, (b * L + t0) * row, rows_of(t0, L) * row);
+  const uint32_t out = on ? lane_bytes : kNoLane;
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
     float o[CPL];
@@ -283,7 +318,7 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
       o[q] = Z ? h[q] * silu_f(o[q]) : h[q];
       if (MARKS && j >= nv) o[q] = 0.0f;
     }
-    if (on && t0 + j < a.L) Raw<T, CPL>::put(y + j * a.D * (int64_t)sizeof(T), o);
+    Raw<T, CPL>::put(y, out, j * row, o);
   }
 }
 
@@ -293,47 +328,50 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
 // maps and those of the adjoint in one exchange.  For a step's gradients a lane keeps
 // log2 a (power form; its sigmoid is log2 a over rate2, its scale is formed again) or 1 - a.
 template <typename T, bool POWER, bool IG, bool Z, bool MARKS>
-__global__ void __launch_bounds__(64 * kWaves) recurrence_bwd_kernel(RecurrenceArgs a, Chain n, float *part) {
+__global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(RecurrenceArgs a, Chain n, float *part) {
   __shared__ Map agg[kWaves][1][64], pre[kWaves][1][64];
   __shared__ float back[kWaves][64];
+  __shared__ float gate_grad[Z ? kWaves : 1][Z ? kSteps : 1][64];  // dy silu'(z) of each lane, which registers do not hold
   __shared__ int drawn;
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tile32 = blockIdx.x % n.tiles;
-  const int64_t tile = tile32, b = tile32 / n.tiles_c;
-  const int64_t c_lane = (int64_t)(tile32 % n.tiles_c) * 64 + lane;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const uint32_t tile32 = uniform(blockIdx.x % n.tiles), b32 = uniform(tile32 / n.tiles_c);
+  const int64_t tile = tile32, b = b32;
+  const int64_t c_lane = (int64_t)(tile32 - b32 * n.tiles_c) * 64 + lane;
   const bool on = c_lane < a.D;
   const int64_t c = on ? c_lane : a.D - 1;
   const uint32_t lane_bytes = (uint32_t)(c * sizeof(T));
   const bool chain = n.chunks > 1;
+  const int D = (int)a.D, L = (int)a.L;  // (both below 2^30: a launch's workgroups)
   if (chain && threadIdx.x == 0) drawn = (int)atomicAdd(n.counter + tile * 16, 1u);
-  int kr = (int)(blockIdx.x / n.tiles), k = n.chunks - 1 - kr;
-  int64_t t0 = (int64_t)k * kRecurrenceChunk + w * kSteps;
+  int kr = uniform(blockIdx.x / n.tiles), k = n.chunks - 1 - kr;
+  int t0 = k * kRecurrenceChunk + w * kSteps;
   Raw<T, 1> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps], rd[kSteps];
   auto load = [&] {
-    load_steps<T, 1>(a.g, b, t0, a.L, lane_bytes, rg);
-    if (IG) load_steps<T, 1>(a.ig, b, t0, a.L, lane_bytes, ri);
-    load_steps<T, 1>(a.x, b, t0, a.L, lane_bytes, rx);
-    load_steps<T, 1>(a.dy, b, t0, a.L, lane_bytes, rd);
-    if (Z) load_steps<T, 1>(a.z, b, t0, a.L, lane_bytes, rz);
+    const int rows = rows_of(t0, L);
+    load_steps<T, 1>(a.g, D, b, t0, rows, lane_bytes, rg);
+    if (IG) load_steps<T, 1>(a.ig, D, b, t0, rows, lane_bytes, ri);
+    load_steps<T, 1>(a.x, D, b, t0, rows, lane_bytes, rx);
+    load_steps<T, 1>(a.dy, D, b, t0, rows, lane_bytes, rd);
+    if (Z) load_steps<T, 1>(a.z, D, b, t0, rows, lane_bytes, rz);
   };
+  const float param = POWER ? a.decay[c] : 0.0f;
   load();
-  const float rate2 = rate_of<POWER>(a, c);
+  const float rate2 = POWER ? rate_of(a.sharpness, param) : 0.0f;
   if (chain) {
     __syncthreads();
-    const int mine = __builtin_amdgcn_readfirstlane(drawn);
+    const int mine = uniform(drawn);
     if ((uint32_t)mine >= (uint32_t)n.chunks) return;  // (the workspace was written to meanwhile)
     if (mine != kr) {
-      kr = mine, k = n.chunks - 1 - kr, t0 = (int64_t)k * kRecurrenceChunk + w * kSteps;
+      kr = mine, k = n.chunks - 1 - kr, t0 = k * kRecurrenceChunk + w * kSteps;
       load();
     }
   }
-  const int64_t len = MARKS ? row_length(a.lengths, b, a.L) : a.L;
-  const int nv = (int)(len - t0 < 0 ? 0 : len - t0 < kSteps ? len - t0 : kSteps);
-  const uint32_t first = MARKS ? start_bits(a.starts, b, t0, a.L, len, lane) : 0;
+  const int len = MARKS ? uniform(row_length(a.lengths, b, L)) : L, nv = rows_of(t0, len);
+  const uint32_t first = MARKS ? start_bits(a.starts, b, t0, L, len, lane) : 0;
   float h = a.states[(b * n.chunks + k) * a.D + c];
 
   // keep: log2 a or 1 - a; steps behind the end: a = 1, nothing comes in
-  float da[kSteps], keep[kSteps], in[kSteps], ii[kSteps], xs[kSteps], dys[kSteps], zs[kSteps];
+  float da[kSteps], keep[kSteps], in[kSteps], ii[kSteps], xs[kSteps], es[kSteps];
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
     float g[1], v[1];
@@ -341,8 +379,14 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_bwd_kernel(RecurrenceA
     const Gate t = gate_of<POWER>(g[0], rate2);
     da[j] = t.a, keep[j] = POWER ? t.la2 : t.o;
     rx[j].get(v), xs[j] = v[0];
-    rd[j].get(v), dys[j] = v[0];
-    if (Z) rz[j].get(v), zs[j] = v[0];
+    rd[j].get(v), es[j] = v[0];
+    if (Z) {
+      float f, df;
+      rz[j].get(v);
+      silu_both(v[0], f, df);
+      gate_grad[w][j][lane] = es[j] * df;
+      es[j] *= f;
+    }
     ii[j] = 1.0f;
     if (IG) ri[j].get(v), ii[j] = sigmoid_f(v[0]);
     float s = t.s;
@@ -352,7 +396,7 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_bwd_kernel(RecurrenceA
   if (nv < kSteps)
 #pragma unroll
     for (int j = 0; j < kSteps; ++j)
-      if (j >= nv) da[j] = 1.0f, keep[j] = in[j] = ii[j] = xs[j] = dys[j] = zs[j] = 0.0f;
+      if (j >= nv) da[j] = 1.0f, keep[j] = in[j] = ii[j] = xs[j] = es[j] = 0.0f;
   Map m = {1.0f, 0.0f};
   float q = 0.0f;
 #pragma unroll
@@ -361,14 +405,16 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_bwd_kernel(RecurrenceA
     m.p *= da[j];
   }
 #pragma unroll
-  for (int j = kSteps - 1; j >= 0; --j) q = MARKS && (first >> j & 1) ? 0.0f : da[j] * ((Z ? dys[j] * silu_f(zs[j]) : dys[j]) + q);
+  for (int j = kSteps - 1; j >= 0; --j) q = MARKS && (first >> j & 1) ? 0.0f : da[j] * (es[j] + q);
   if (MARKS && first) m.p = __uint_as_float(kCleared);
   agg[w][0][lane] = m;
   back[w][lane] = q;
   const float q0[1] = {a.dstate_final && kr < n.group ? a.dstate_final[b * a.D + c] : 0.0f};
   __syncthreads();
+#pragma unroll 1
   for (int i = 0; i < w; ++i) h = apply(agg[i][0][lane], h);
   Map after = {1.0f, 0.0f};  // what the waves behind this one do
+#pragma unroll 1
   for (int i = kWaves - 1; i > w; --i) after = compose(after, Map{agg[i][0][lane].p, back[i][lane]});
   const bool last = (kr + 1) % n.group == 0, more = kr + 1 < n.chunks;
   if (more && !last && w == 0) publish_map(n.maps + (tile * n.chunks + kr) * 64 + lane, compose(after, Map{m.p, q}));
@@ -391,22 +437,20 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_bwd_kernel(RecurrenceA
     in[j] = h;
     h = next;
   }
-  const int64_t row0 = ((b * a.L + t0) * a.D) * (int64_t)sizeof(T) + lane_bytes;
+  const int row = D * (int)sizeof(T), rows_bytes = rows_of(t0, L) * row;
+  const int64_t row0 = (b * L + t0) * row;
+  const Buffer bx = buffer_of(a.dx, row0, rows_bytes), bg = buffer_of(a.dg, row0, rows_bytes), bi = buffer_of(a.dig, row0, rows_bytes);
+  const Buffer bz = buffer_of(a.dz, row0, rows_bytes);
+  const uint32_t out = on ? lane_bytes : kNoLane;
   // (a rate whose reciprocal leaves fp32 has no gradient either)
   const float over = POWER && rate2 < -0x1p-120f ? fast_rcp(rate2) : 0.0f;
   float sum = 0.0f;
 #pragma unroll
   for (int j = kSteps - 1; j >= 0; --j) {
     const bool start = MARKS && (first >> j & 1);
-    float dz[1] = {0.0f}, e = dys[j];
-    if (Z) {
-      float f, df;
-      silu_both(zs[j], f, df);
-      dz[0] = e * h * df;
-      e *= f;
-    }
+    float dz[1] = {Z ? gate_grad[w][j][lane] * h : 0.0f};
     h = in[j];
-    const float wt = e + q, u = ii[j] * xs[j];
+    const float wt = es[j] + q, u = ii[j] * xs[j];
     float s, dg[1];
     if constexpr (POWER) {
       s = scale_of(keep[j], da[j]);
@@ -423,13 +467,10 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_bwd_kernel(RecurrenceA
     float dx[1] = {ws * ii[j]}, di[1] = {ws * u * (1.0f - ii[j])};
     q = start ? 0.0f : da[j] * wt;
     if (MARKS && j >= nv) dx[0] = dg[0] = di[0] = dz[0] = 0.0f;
-    if (on && t0 + j < a.L) {
-      const int64_t row = row0 + j * a.D * (int64_t)sizeof(T);
-      Raw<T, 1>::put((char *)a.dx + row, dx);
-      Raw<T, 1>::put((char *)a.dg + row, dg);
-      if (IG) Raw<T, 1>::put((char *)a.dig + row, di);
-      if (Z) Raw<T, 1>::put((char *)a.dz + row, dz);
-    }
+    Raw<T, 1>::put(bx, out, j * row, dx);
+    Raw<T, 1>::put(bg, out, j * row, dg);
+    if (IG) Raw<T, 1>::put(bi, out, j * row, di);
+    if (Z) Raw<T, 1>::put(bz, out, j * row, dz);
   }
   if constexpr (POWER) {  // the chunk's part of ddecay, waves in order
     __syncthreads();
@@ -438,8 +479,8 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_bwd_kernel(RecurrenceA
     if (w == 0 && on) {
       sum = 0.0f;
       for (int i = 0; i < kWaves; ++i) sum += back[i][lane];
-      const float v = a.decay[c];  // sigmoid / softplus goes to 1 where both vanish
-      part[(b * n.chunks + k) * a.D + c] = sum * (v < -40.0f ? 1.0f : sigmoid_f(v) / softplus_exact(v));
+      // sigmoid / softplus goes to 1 where both vanish
+      part[(b * n.chunks + k) * a.D + c] = sum * (param < -40.0f ? 1.0f : sigmoid_f(param) / softplus_full(param));
     }
   }
 }
@@ -463,7 +504,7 @@ __global__ void __launch_bounds__(256) recurrence_update_kernel(RecurrenceUpdate
   load_vec(a.state + b * a.D + c, h);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const Gate q = gate_of<POWER>(g[j], POWER ? -a.sharpness * softplus_f(l[j]) * kLog2e : 0.0f);
+    const Gate q = gate_of<POWER>(g[j], POWER ? rate_of(a.sharpness, l[j]) : 0.0f);
     h[j] = fmaf(q.a, h[j], q.s * (a.ig.p ? x[j] * sigmoid_f(i[j]) : x[j]));
     x[j] = a.z.p ? h[j] * silu_f(z[j]) : h[j];
   }
@@ -484,18 +525,24 @@ hipError_t by_switches(bool power, bool ig, bool z, bool marks, F f) {
   return power ? o(Int<1>{}) : o(Int<0>{});
 }
 
-#ifndef GROUP
-#define GROUP 4
-#endif
-int group_of(int64_t, int64_t) { return GROUP; }
+// Chunks per published state.  A state's way from one workgroup to the next takes
+// about 1.25 us, and the maps between states are words to read in every workgroup
+// behind: as few maps as keep the states' way through the sequence below 3/4 of the
+// time that the tensors need (x, both gates and y at 4 TB/s).
+int group_of(int64_t B, int64_t L, int64_t D, int es) {
+  const double us = (double)(B * L) * (double)(4 * D * es) / 4e6, way = (double)((L + kRecurrenceChunk - 1) / kRecurrenceChunk) * 1.25;
+  int g = 1;
+  while (g < kMaxGroup && way > 0.75 * us * g) g *= 2;
+  return g;
+}
 
-// cpl: channels per lane
-Chain chain_of(int64_t B, int64_t L, int64_t D, int cpl, void *workspace) {
+// cpl: channels per lane, es: bytes of an element
+Chain chain_of(int64_t B, int64_t L, int64_t D, int cpl, int es, void *workspace) {
   Chain n;
   n.tiles_c = (uint32_t)((D + 64 * cpl - 1) / (64 * cpl));
   n.tiles = (uint32_t)B * n.tiles_c;
   n.chunks = (int)((L + kRecurrenceChunk - 1) / kRecurrenceChunk);
-  n.group = group_of(n.chunks, n.tiles);
+  n.group = group_of(B, L, D, es);
   n.groups = (n.chunks + n.group - 1) / n.group;
   n.counter = (uint32_t *)workspace;
   n.states = (uint64_t *)((char *)workspace + (int64_t)n.tiles * 64);
@@ -513,7 +560,7 @@ hipError_t clear(void *p, int64_t bytes, hipStream_t s) {
 
 template <typename T, int CPL>
 hipError_t fwd(const RecurrenceArgs &a, hipStream_t s) {
-  const Chain n = chain_of(a.B, a.L, a.D, CPL, a.workspace);
+  const Chain n = chain_of(a.B, a.L, a.D, CPL, sizeof(T), a.workspace);
   if (n.chunks > 1) {
     const hipError_t e = clear(a.workspace, chain_bytes(n, CPL), s);
     if (e != hipSuccess) return e;
@@ -527,7 +574,7 @@ hipError_t fwd(const RecurrenceArgs &a, hipStream_t s) {
 
 template <typename T>
 hipError_t bwd(const RecurrenceArgs &a, hipStream_t s) {
-  const Chain n = chain_of(a.B, a.L, a.D, 1, a.workspace);
+  const Chain n = chain_of(a.B, a.L, a.D, 1, sizeof(T), a.workspace);
   const int64_t bytes = chain_bytes(n, 1);
   float *part = (float *)((char *)a.workspace + bytes);
   if (n.chunks > 1) {
@@ -556,10 +603,10 @@ hipError_t update(const RecurrenceUpdateArgs &a, hipStream_t s) {
 
 int64_t recurrence_fwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int io_dtype) {
   const int cpl = io_dtype == 0 ? 1 : 2;
-  return chain_bytes(chain_of(B, L, D, cpl, nullptr), cpl);
+  return chain_bytes(chain_of(B, L, D, cpl, io_dtype == 0 ? 4 : 2, nullptr), cpl);
 }
-int64_t recurrence_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D) {
-  const Chain n = chain_of(B, L, D, 1, nullptr);
+int64_t recurrence_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int io_dtype) {
+  const Chain n = chain_of(B, L, D, 1, io_dtype == 0 ? 4 : 2, nullptr);
   return chain_bytes(n, 1) + B * n.chunks * D * 4;
 }
 
