@@ -178,12 +178,18 @@ struct Raw<bf16, 2> {
 __device__ __forceinline__ int rows_of(int t0, int L) { return L - t0 < 0 ? 0 : L - t0 < kSteps ? L - t0 : kSteps; }
 
 // The wave's steps of a tensor; a step's stride and 16 of them stay below 2^29 bytes.
-template <typename T, int CPL>
+// RUNNING: one offset in a scalar register that moves on, instead of all steps' at once:
+// they do not fit beside each other (forward 8 x 2048 x 2048 bf16: 69.8 -> 68.1 us; the
+// backward, which waits for them in other places, 32K x 5120 with z: 751 -> 784 us).
+template <bool RUNNING, typename T, int CPL>
 __device__ __forceinline__ void load_steps(const View3 &v, int D, int64_t b, int t0, int rows, uint32_t lane_bytes, Raw<T, CPL> (&r)[kSteps]) {
   const int step = (int)v.st * (int)sizeof(T);
   const Buffer p = buffer_of(v.p, (b * v.sb + t0 * v.st) * (int64_t)sizeof(T), rows ? (rows - 1) * step + D * (int)sizeof(T) : 0);
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j) r[j].load(p, lane_bytes, j * step);
+  for (int j = 0, at = 0; j < kSteps; ++j, at += step) {
+    if constexpr (RUNNING) asm("" : "+s"(at));
+    r[j].load(p, lane_bytes, at);
+  }
 }
 
 // Bit j: a document starts at the wave's step j, before the row's length.
@@ -214,10 +220,10 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
   Raw<T, CPL> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps];
   auto load = [&] {
     const int rows = rows_of(t0, L);
-    load_steps<T, CPL>(a.g, D, b, t0, rows, lane_bytes, rg);
-    if (IG) load_steps<T, CPL>(a.ig, D, b, t0, rows, lane_bytes, ri);
-    load_steps<T, CPL>(a.x, D, b, t0, rows, lane_bytes, rx);
-    if (Z) load_steps<T, CPL>(a.z, D, b, t0, rows, lane_bytes, rz);
+    load_steps<true, T, CPL>(a.g, D, b, t0, rows, lane_bytes, rg);
+    if (IG) load_steps<true, T, CPL>(a.ig, D, b, t0, rows, lane_bytes, ri);
+    load_steps<true, T, CPL>(a.x, D, b, t0, rows, lane_bytes, rx);
+    if (Z) load_steps<true, T, CPL>(a.z, D, b, t0, rows, lane_bytes, rz);
   };
   float rate2[CPL];
 #pragma unroll
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
     }
   }
   const int row = D * (int)sizeof(T);
-  const Buffer y = buffer_of(a.y, (b * L + t0) * row, rows_of(t0, L) * row);
+  const Buffer y = buffer_of(a.y, (b * L + t0) * row, uniform(rows_of(t0, L)) * row);
   const uint32_t out = on ? lane_bytes : kNoLane;
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
@@ -326,12 +332,14 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
 // to t - 1 is q = a_t w_t, and a stretch of steps is q -> P q + Q with the P of the
 // forward map.  The states inside a chunk are formed again from the one before it, its
 // maps and those of the adjoint in one exchange.  For a step's gradients a lane keeps
-// log2 a (power form; its sigmoid is log2 a over rate2, its scale is formed again) or 1 - a.
+// log2 a (power form; its sigmoid is log2 a over rate2) or 1 - a, and s in LDS:
+//   log a da/d(log a) w (h_{t-1} - u a / s) = dLoss / d(log a) log a,  u = sigmoid(i) x.
 template <typename T, bool POWER, bool IG, bool Z, bool MARKS>
 __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(RecurrenceArgs a, Chain n, float *part) {
   __shared__ Map agg[kWaves][1][64], pre[kWaves][1][64];
   __shared__ float back[kWaves][64];
-  __shared__ float gate_grad[Z ? kWaves : 1][Z ? kSteps : 1][64];  // dy silu'(z) of each lane, which registers do not hold
+  // of each lane's steps, what registers do not hold: s, and dy silu'(z)
+  __shared__ float scale[POWER ? kWaves : 1][POWER ? kSteps : 1][64], gate_grad[Z ? kWaves : 1][Z ? kSteps : 1][64];
   __shared__ int drawn;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const uint32_t tile32 = uniform(blockIdx.x % n.tiles), b32 = uniform(tile32 / n.tiles_c);
@@ -348,11 +356,11 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
   Raw<T, 1> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps], rd[kSteps];
   auto load = [&] {
     const int rows = rows_of(t0, L);
-    load_steps<T, 1>(a.g, D, b, t0, rows, lane_bytes, rg);
-    if (IG) load_steps<T, 1>(a.ig, D, b, t0, rows, lane_bytes, ri);
-    load_steps<T, 1>(a.x, D, b, t0, rows, lane_bytes, rx);
-    load_steps<T, 1>(a.dy, D, b, t0, rows, lane_bytes, rd);
-    if (Z) load_steps<T, 1>(a.z, D, b, t0, rows, lane_bytes, rz);
+    load_steps<false, T, 1>(a.g, D, b, t0, rows, lane_bytes, rg);
+    if (IG) load_steps<false, T, 1>(a.ig, D, b, t0, rows, lane_bytes, ri);
+    load_steps<false, T, 1>(a.x, D, b, t0, rows, lane_bytes, rx);
+    load_steps<false, T, 1>(a.dy, D, b, t0, rows, lane_bytes, rd);
+    if (Z) load_steps<false, T, 1>(a.z, D, b, t0, rows, lane_bytes, rz);
   };
   const float param = POWER ? a.decay[c] : 0.0f;
   load();
@@ -391,7 +399,9 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
     if (IG) ri[j].get(v), ii[j] = sigmoid_f(v[0]);
     float s = t.s;
     if (MARKS && (first >> j & 1)) da[j] = 0.0f, s = 1.0f;
+    if (POWER) scale[w][j][lane] = s;
     in[j] = s * (ii[j] * xs[j]);
+    if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (more steps at once do not fit registers)
   }
   if (nv < kSteps)
 #pragma unroll
@@ -437,35 +447,31 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
     in[j] = h;
     h = next;
   }
-  const int row = D * (int)sizeof(T), rows_bytes = rows_of(t0, L) * row;
+  const int row = D * (int)sizeof(T), rows_bytes = uniform(rows_of(t0, L)) * row;
   const int64_t row0 = (b * L + t0) * row;
   const Buffer bx = buffer_of(a.dx, row0, rows_bytes), bg = buffer_of(a.dg, row0, rows_bytes), bi = buffer_of(a.dig, row0, rows_bytes);
   const Buffer bz = buffer_of(a.dz, row0, rows_bytes);
   const uint32_t out = on ? lane_bytes : kNoLane;
   // (a rate whose reciprocal leaves fp32 has no gradient either)
-  const float over = POWER && rate2 < -0x1p-120f ? fast_rcp(rate2) : 0.0f;
+  const float over = POWER && rate2 < -0x1p-120f ? kLn2 * fast_rcp(rate2) : 0.0f;
   float sum = 0.0f;
 #pragma unroll
   for (int j = kSteps - 1; j >= 0; --j) {
     const bool start = MARKS && (first >> j & 1);
     float dz[1] = {Z ? gate_grad[w][j][lane] * h : 0.0f};
     h = in[j];
-    const float wt = es[j] + q, u = ii[j] * xs[j];
-    float s, dg[1];
+    const float wt = es[j] + q, flow = wt * da[j], u = ii[j] * xs[j];
+    const float s = POWER ? scale[w][j][lane] : start ? 1.0f : keep[j], ws = wt * s;
+    float dx[1] = {ws * ii[j]}, di[1] = {dx[0] * (xs[j] - u)}, dg[1];
     if constexpr (POWER) {
-      s = scale_of(keep[j], da[j]);
-      const float la = kLn2 * keep[j];
-      const float f = start ? 0.0f : wt * da[j] * (la * h - u * da[j] * (s > 0.0f ? la * fast_rcp(s) : 0.0f));
-      if (start) s = 1.0f;
+      // with log2 a for log a: log 2 comes in with the sigmoid's slope and at the end
+      const float f = start ? 0.0f : flow * keep[j] * fmaf(-u * da[j], s > 0.0f ? fast_rcp(s) : 0.0f, h);
       sum += f;
-      dg[0] = f * fmaf(-keep[j], over, 1.0f);
+      dg[0] = f * fmaf(-keep[j], over, kLn2);
     } else {
-      s = start ? 1.0f : keep[j];
-      dg[0] = start ? 0.0f : wt * da[j] * s * (h - u);
+      dg[0] = start ? 0.0f : flow * s * (h - u);
     }
-    const float ws = wt * s;
-    float dx[1] = {ws * ii[j]}, di[1] = {ws * u * (1.0f - ii[j])};
-    q = start ? 0.0f : da[j] * wt;
+    q = start ? 0.0f : flow;
     if (MARKS && j >= nv) dx[0] = dg[0] = di[0] = dz[0] = 0.0f;
     Raw<T, 1>::put(bx, out, j * row, dx);
     Raw<T, 1>::put(bg, out, j * row, dg);
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
       sum = 0.0f;
       for (int i = 0; i < kWaves; ++i) sum += back[i][lane];
       // sigmoid / softplus goes to 1 where both vanish
-      part[(b * n.chunks + k) * a.D + c] = sum * (param < -40.0f ? 1.0f : sigmoid_f(param) / softplus_full(param));
+      part[(b * n.chunks + k) * a.D + c] = kLn2 * sum * (param < -40.0f ? 1.0f : sigmoid_f(param) / softplus_full(param));
     }
   }
 }
@@ -527,12 +533,12 @@ hipError_t by_switches(bool power, bool ig, bool z, bool marks, F f) {
 
 // Chunks per published state.  A state's way from one workgroup to the next takes
 // about 1.25 us, and the maps between states are words to read in every workgroup
-// behind: as few maps as keep the states' way through the sequence below 3/4 of the
+// behind: as few maps as keep the states' way through the sequence below 2/5 of the
 // time that the tensors need (x, both gates and y at 4 TB/s).
 int group_of(int64_t B, int64_t L, int64_t D, int es) {
   const double us = (double)(B * L) * (double)(4 * D * es) / 4e6, way = (double)((L + kRecurrenceChunk - 1) / kRecurrenceChunk) * 1.25;
   int g = 1;
-  while (g < kMaxGroup && way > 0.75 * us * g) g *= 2;
+  while (g < kMaxGroup && way > 0.4 * us * g) g *= 2;
   return g;
 }
 
