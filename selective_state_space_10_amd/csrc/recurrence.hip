@@ -137,8 +137,10 @@ __device__ __forceinline__ void collected(const Chain &n, int k, int lane, const
 
 // A lane's channels of one step as they lie in memory, at a byte offset of a buffer.
 // A buffer is the wave's steps of a tensor: an address is a base and a step's offset in
-// scalar registers and the lane's offset in one vector register, and what is read or
-// written behind the last step (or by a lane whose offset is kNoLane) is zero or dropped.
+// scalar registers and the lane's offset in one vector register.  Loads stay inside by
+// their offsets.  A store of a lane that has nothing to store takes kNoLane as the
+// lane's offset, behind any buffer's end, and is dropped; the end is that of all
+// kSteps steps, so that no step's offset lies behind it.
 typedef __amdgpu_buffer_rsrc_t Buffer;
 constexpr uint32_t kNoLane = 0x80000000u;
 __device__ __forceinline__ Buffer buffer_of(const void *p, int64_t offset, int bytes) {
@@ -177,18 +179,20 @@ struct Raw<bf16, 2> {
 // Of the wave's steps, those before the end of the sequence.
 __device__ __forceinline__ int rows_of(int t0, int L) { return L - t0 < 0 ? 0 : L - t0 < kSteps ? L - t0 : kSteps; }
 
-// The wave's steps of a tensor; a step's stride and 16 of them stay below 2^29 bytes.
+// The wave's steps of a tensor, the sequence's last step again for those behind it; a
+// step's stride and 16 of them stay below 2^29 bytes.
 // RUNNING: one offset in a scalar register that moves on, instead of all steps' at once:
 // they do not fit beside each other (forward 8 x 2048 x 2048 bf16: 69.8 -> 68.1 us; the
 // backward, which waits for them in other places, 32K x 5120 with z: 751 -> 784 us).
 template <bool RUNNING, typename T, int CPL>
-__device__ __forceinline__ void load_steps(const View3 &v, int D, int64_t b, int t0, int rows, uint32_t lane_bytes, Raw<T, CPL> (&r)[kSteps]) {
-  const int step = (int)v.st * (int)sizeof(T);
-  const Buffer p = buffer_of(v.p, (b * v.sb + t0 * v.st) * (int64_t)sizeof(T), rows ? (rows - 1) * step + D * (int)sizeof(T) : 0);
+__device__ __forceinline__ void load_steps(const View3 &v, int D, int64_t b, int t0, int L, uint32_t lane_bytes, Raw<T, CPL> (&r)[kSteps]) {
+  const int step = (int)v.st * (int)sizeof(T), from = t0 < L ? t0 : L - 1, last = (rows_of(from, L) - 1) * step;
+  const Buffer p = buffer_of(v.p, (b * v.sb + from * v.st) * (int64_t)sizeof(T), last + D * (int)sizeof(T));
 #pragma unroll
-  for (int j = 0, at = 0; j < kSteps; ++j, at += step) {
+  for (int j = 0, at = 0; j < kSteps; ++j) {
     if constexpr (RUNNING) asm("" : "+s"(at));
     r[j].load(p, lane_bytes, at);
+    at = RUNNING ? (at + step < last ? at + step : last) : ((j + 1) * step < last ? (j + 1) * step : last);
   }
 }
 
@@ -219,11 +223,10 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
   int t0 = k * kRecurrenceChunk + w * kSteps;
   Raw<T, CPL> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps];
   auto load = [&] {
-    const int rows = rows_of(t0, L);
-    load_steps<true, T, CPL>(a.g, D, b, t0, rows, lane_bytes, rg);
-    if (IG) load_steps<true, T, CPL>(a.ig, D, b, t0, rows, lane_bytes, ri);
-    load_steps<true, T, CPL>(a.x, D, b, t0, rows, lane_bytes, rx);
-    if (Z) load_steps<true, T, CPL>(a.z, D, b, t0, rows, lane_bytes, rz);
+    load_steps<true, T, CPL>(a.g, D, b, t0, L, lane_bytes, rg);
+    if (IG) load_steps<true, T, CPL>(a.ig, D, b, t0, L, lane_bytes, ri);
+    load_steps<true, T, CPL>(a.x, D, b, t0, L, lane_bytes, rx);
+    if (Z) load_steps<true, T, CPL>(a.z, D, b, t0, L, lane_bytes, rz);
   };
   float rate2[CPL];
 #pragma unroll
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
     }
   }
   const int row = D * (int)sizeof(T);
-  const Buffer y = buffer_of(a.y, (b * L + t0) * row, uniform(rows_of(t0, L)) * row);
+  const Buffer y = buffer_of(a.y, (b * L + t0) * row, kSteps * row);
   const uint32_t out = on ? lane_bytes : kNoLane;
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
       o[q] = Z ? h[q] * silu_f(o[q]) : h[q];
       if (MARKS && j >= nv) o[q] = 0.0f;
     }
-    Raw<T, CPL>::put(y, out, j * row, o);
+    Raw<T, CPL>::put(y, t0 + j < L ? out : kNoLane, j * row, o);
   }
 }
 
@@ -355,12 +358,11 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
   int t0 = k * kRecurrenceChunk + w * kSteps;
   Raw<T, 1> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps], rd[kSteps];
   auto load = [&] {
-    const int rows = rows_of(t0, L);
-    load_steps<false, T, 1>(a.g, D, b, t0, rows, lane_bytes, rg);
-    if (IG) load_steps<false, T, 1>(a.ig, D, b, t0, rows, lane_bytes, ri);
-    load_steps<false, T, 1>(a.x, D, b, t0, rows, lane_bytes, rx);
-    load_steps<false, T, 1>(a.dy, D, b, t0, rows, lane_bytes, rd);
-    if (Z) load_steps<false, T, 1>(a.z, D, b, t0, rows, lane_bytes, rz);
+    load_steps<false, T, 1>(a.g, D, b, t0, L, lane_bytes, rg);
+    if (IG) load_steps<false, T, 1>(a.ig, D, b, t0, L, lane_bytes, ri);
+    load_steps<false, T, 1>(a.x, D, b, t0, L, lane_bytes, rx);
+    load_steps<false, T, 1>(a.dy, D, b, t0, L, lane_bytes, rd);
+    if (Z) load_steps<false, T, 1>(a.z, D, b, t0, L, lane_bytes, rz);
   };
   const float param = POWER ? a.decay[c] : 0.0f;
   load();
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
     in[j] = h;
     h = next;
   }
-  const int row = D * (int)sizeof(T), rows_bytes = uniform(rows_of(t0, L)) * row;
+  const int row = D * (int)sizeof(T), rows_bytes = kSteps * row;
   const int64_t row0 = (b * L + t0) * row;
   const Buffer bx = buffer_of(a.dx, row0, rows_bytes), bg = buffer_of(a.dg, row0, rows_bytes), bi = buffer_of(a.dig, row0, rows_bytes);
   const Buffer bz = buffer_of(a.dz, row0, rows_bytes);
@@ -473,10 +475,11 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
     }
     q = start ? 0.0f : flow;
     if (MARKS && j >= nv) dx[0] = dg[0] = di[0] = dz[0] = 0.0f;
-    Raw<T, 1>::put(bx, out, j * row, dx);
-    Raw<T, 1>::put(bg, out, j * row, dg);
-    if (IG) Raw<T, 1>::put(bi, out, j * row, di);
-    if (Z) Raw<T, 1>::put(bz, out, j * row, dz);
+    const uint32_t to = t0 + j < L ? out : kNoLane;
+    Raw<T, 1>::put(bx, to, j * row, dx);
+    Raw<T, 1>::put(bg, to, j * row, dg);
+    if (IG) Raw<T, 1>::put(bi, to, j * row, di);
+    if (Z) Raw<T, 1>::put(bz, to, j * row, dz);
   }
   if constexpr (POWER) {  // the chunk's part of ddecay, waves in order
     __syncthreads();
