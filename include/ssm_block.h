@@ -269,7 +269,7 @@ int ssm_gated_recurrence_update(int64_t batch, int64_t dim, int io_dtype, float 
  *   state_final: as state0: the last width - 1 inputs of each row, zero where
  *            they are not of the row's last document; NULL = not wanted
  *
- * dim: a multiple of 8 up to 2^23; batch <= 2^16; batch * dim / 8 *
+ * dim: a multiple of 8 up to 2^23; batch <= 2^16; seqlen <= 2^30; batch * dim / 8 *
  * (ceil(seqlen / 32) + 1) <= 2^31 (and for one token the same with seqlen 1).
  */
 int ssm_causal_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int width, int io_dtype,

@@ -14,6 +14,11 @@ namespace {
 
 constexpr int kRows = 8;  // rows whose loads are under way together
 
+template <int X>
+struct Int {
+  static constexpr int v = X;
+};
+
 // 8 channels of a row as they lie in memory.
 template <typename T>
 struct Raw;
@@ -58,19 +63,19 @@ __device__ __forceinline__ void load_before(const ConvArgs &a, int64_t b, int64_
 
 // win[0 .. K-2] are the inputs before a step, oldest first; at a document's
 // start they are nothing.
-template <int K>
-__device__ __forceinline__ void clear(float (&win)[K][8]) {
+template <int K, int V>
+__device__ __forceinline__ void clear(float (&win)[K][V]) {
 #pragma unroll
   for (int k = 0; k + 1 < K; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) win[k][j] = 0.0f;
+    for (int j = 0; j < V; ++j) win[k][j] = 0.0f;
 }
-template <int K>
-__device__ __forceinline__ void shift(float (&win)[K][8]) {
+template <int K, int V>
+__device__ __forceinline__ void shift(float (&win)[K][V]) {
 #pragma unroll
   for (int k = 0; k + 1 < K; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) win[k][j] = win[k + 1][j];
+    for (int j = 0; j < V; ++j) win[k][j] = win[k + 1][j];
 }
 
 // The inputs before step t0, into win[0 .. K-2]; none behind the row's length.
@@ -118,7 +123,7 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int64_t nchun
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         if (t + r >= t1) break;
-        if (a.starts && a.starts[b * a.L + t + r]) clear<K>(win);
+        if (a.starts && a.starts[b * a.L + t + r]) clear<K, 8>(win);
         raw[r].get(win[K - 1]);
         float v[8];
 #pragma unroll
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int64_t nchun
           if (t + r >= len) v[j] = 0.0f;
         }
         store_vec(y + (t + r) * a.D, v);
-        shift<K>(win);
+        shift<K, 8>(win);
       }
     }
     return;
@@ -147,129 +152,187 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int64_t nchun
   }
 }
 
-// dpre_s = dy_s act'(pre_s);  dx_t = sum over taps `back` of w[K-1-back] dpre_{t+back}
-// where no document starts in (t, t+back];  dweight[k] = sum dpre_s x_{s-(K-1)+k}.
-// A workgroup takes CG groups of 8 channels and 256 / CG chunks at once; a chunk
-// of nrow steps s yields dx of nrow - (K-1) steps t and as much of the weights' sums.
-template <typename T, int K, int CG>
-__global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int64_t nchunk, int nrow, int ctiles, int64_t nruns, float *part) {
-  constexpr int R = 256 / CG;
-  __shared__ alignas(16) float lds[256 * 8];
-  const int64_t ct = blockIdx.x % ctiles, run = blockIdx.x / ctiles;
-  const int slot = threadIdx.x / CG;
-  const int64_t c = (ct * CG + threadIdx.x % CG) * 8;
-  const bool on = c < a.D;
-  const int own = nrow - (K - 1);
-  float w[K][8], bias[8], dw[K + 1][8];
+// Backward.  dpre_s = dy_s act'(pre_s);  dx_t = sum over taps `back` of w[K-1-back]
+// dpre_{t+back} where no document starts in (t, t+back];  dweight[k] = sum dpre_s x_{s-(K-1)+k}.
+//
+// A wave takes two channels per lane and walks over kBwdRows steps s with the inputs
+// under the taps and the unfinished dx of the last K steps in registers: it yields
+// dx of kBwdRows - (K-1) steps t and as much of the weights' sums, which stay in registers
+// over its chunks; a workgroup adds its waves' sums and a second kernel the workgroups', in order.
+// All of a wave is at the same step, so that steps, starts and lengths are scalar work.
+// Two channels and not eight: 74 registers' worth of sums and windows less, six waves per
+// SIMD instead of two (8 x 2048 x 2048 bf16: 101 us with eight).
+constexpr int kBwdRows = 64;  // as many starts of documents as a wave has lanes
+
+template <typename T>
+struct Raw2;
+template <>
+struct Raw2<float> {
+  uint32_t a, b;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t step) {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    const u2 v = __builtin_bit_cast(u2, __builtin_amdgcn_raw_buffer_load_b64(p, lane, step, 0));
+    a = v.x, b = v.y;
+  }
+  __device__ __forceinline__ void get(float (&v)[2]) const { v[0] = __uint_as_float(a), v[1] = __uint_as_float(b); }
+};
+template <>
+struct Raw2<bf16> {
+  uint32_t a;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t step) { a = __builtin_amdgcn_raw_buffer_load_b32(p, lane, step, 0); }
+  __device__ __forceinline__ void get(float (&v)[2]) const { v[0] = __uint_as_float(a << 16), v[1] = __uint_as_float(a & 0xffff0000u); }
+};
+__device__ __forceinline__ void load2(const float *p, float (&v)[2]) { v[0] = ((const float2 *)p)->x, v[1] = ((const float2 *)p)->y; }
+__device__ __forceinline__ void load2(const bf16 *p, float (&v)[2]) {
+  const uint32_t w = *(const uint32_t *)p;
+  v[0] = __uint_as_float(w << 16), v[1] = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void store2(float *p, const float (&v)[2]) { *(float2 *)p = make_float2(v[0], v[1]); }
+__device__ __forceinline__ void store2(bf16 *p, const float (&v)[2]) { *(uint32_t *)p = pack_bf16(v[0], v[1]); }
+
+__device__ __forceinline__ int uniform(int64_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
+// Bit i: a document starts at step t0 + i, of the steps from 0 to L.
+__device__ __forceinline__ uint64_t start_bits(const uint8_t *starts, int64_t b, int t0, int L) {
+  if (!starts) return 0;
+  const int t = t0 + (int)(threadIdx.x & 63);
+  return __ballot(t >= 0 && t < L && starts[b * L + t] != 0);
+}
+
+template <typename T, int K, bool MARKS>
+__global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nchunk, int ctiles, int nruns, float *part) {
+  constexpr int kOwn = kBwdRows - (K - 1), N = 2 * (K + 1);
+  __shared__ float sums[4][N][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int ct = uniform(blockIdx.x % ctiles), run = uniform(blockIdx.x / ctiles);
+  const int D = (int)a.D, L = (int)a.L;
+  const int c_lane = (ct * 64 + lane) * 2, c = c_lane < D ? c_lane : D - 2;
+  const bool on = c_lane < D;
+  const uint32_t lane_bytes = (uint32_t)(c * sizeof(T));
+  float w[K][2], bias[2] = {0.0f, 0.0f}, dw[K + 1][2];
 #pragma unroll
-  for (int k = 0; k <= K; ++k)
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
-  if (on) {
-    load_weights<K>(a, c, w, bias);
-    for (int64_t it = run * R + slot; it < a.B * nchunk; it += nruns * R) {
-      const int64_t b = it / nchunk, t0 = it % nchunk * own;
-      const int len = row_length(a.lengths, b, a.L);
-      float win[K][8], d[K][8];
-      load_window<T, K>(a, b, t0, len, c, win);
+    for (int k = 0; k < K; ++k) w[k][j] = a.weight[(int64_t)(c + j) * K + k];
+  if (a.bias) load2(a.bias + c, bias);
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+  for (int k = 0; k <= K; ++k) dw[k][0] = dw[k][1] = 0.0f;
+  const int items = (int)a.B * nchunk;
+  for (int it = run * 4 + wave; it < items; it += nruns * 4) {
+    const int b32 = uniform(it / nchunk), t0 = uniform(it - b32 * nchunk) * kOwn;
+    const int64_t b = b32;
+    const int len = MARKS ? uniform(row_length(a.lengths, b, L)) : L;
+    const int rows = L - t0 < kBwdRows ? L - t0 : kBwdRows;
+    const uint64_t first = MARKS ? start_bits(a.starts, b, t0, L) : 0;
+    const uint32_t xstep = (uint32_t)a.x.st * sizeof(T), ystep = (uint32_t)a.dy.st * sizeof(T);
+    auto buffer = [&](const View3 &v, uint32_t step) {
+      return __builtin_amdgcn_make_buffer_rsrc((char *)v.p + (b * v.sb + t0 * v.st) * (int64_t)sizeof(T), 0, (int)((rows - 1) * step + D * (uint32_t)sizeof(T)),
+                                               0x00027000);
+    };
+    const auto bx = buffer(a.x, xstep), by = buffer(a.dy, ystep);
+    float win[K][2], d[K][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[k][j] = 0.0f;
-      const T *x = (const T *)a.x.p + b * a.x.sb + c, *dy = (const T *)a.dy.p + b * a.dy.sb + c;
-      int age = K - 1;  // steps of this document before step s, as far as taps reach
-      if (a.starts)
+    for (int k = 0; k < K; ++k) win[k][0] = win[k][1] = d[k][0] = d[k][1] = 0.0f;
+    int age = K - 1;  // steps of this document before step s, as far as taps reach
+    if constexpr (K > 1) {
+      const uint64_t ahead = MARKS ? start_bits(a.starts, b, t0 - (K - 1), L) : 0;
 #pragma unroll
-        for (int k = 1; k < K; ++k) {
-          const int64_t t = t0 - K + k;
-          if (t >= 0 && a.starts[b * a.L + t]) age = K - 1 - k;
+      for (int k = 0; k + 1 < K; ++k) {
+        const int t = t0 - (K - 1) + k;
+        if (MARKS && (ahead >> k & 1)) {
+          clear<K, 2>(win);
+          age = K - 2 - k;
         }
-      for (int m0 = 0; m0 < nrow && t0 + m0 - (K - 1) < a.L; m0 += kRows) {
-        Raw<T> rx[kRows], ry[kRows];
+        if (t >= 0 && t < len)
+          load2((const T *)a.x.p + b * a.x.sb + t * a.x.st + c, win[k]);
+        else if (t < 0 && a.state0)
+          load2((const T *)a.state0 + (b * (K - 1) + t + (K - 1)) * a.D + c, win[k]);
+      }
+    }
+    T *dx = (T *)a.dx + (b * L + t0 - (K - 1)) * a.D + c;
+    for (int m0 = 0; m0 < kBwdRows && m0 - (K - 1) < rows; m0 += kRows) {
+      Raw2<T> rx[kRows], ry[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const uint32_t m = m0 + r < rows ? m0 + r : rows - 1;
+        rx[r].load(bx, lane_bytes, m * xstep);
+        ry[r].load(by, lane_bytes, m * ystep);
+      }
+      // EDGE: a document starts among these steps or just before, or the row ends
+      auto walk = [&](auto edge) {
+        constexpr bool EDGE = decltype(edge)::v;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-          const int64_t s = t0 + m0 + r < a.L ? t0 + m0 + r : a.L - 1;
-          rx[r].load(x + s * a.x.st);
-          ry[r].load(dy + s * a.dy.st);
-        }
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const int64_t s = t0 + m0 + r, t = s - (K - 1);
-          const bool live = s < len;
-          if (a.starts) {
+          const int m = m0 + r, t = t0 + m - (K - 1);
+          if constexpr (EDGE && MARKS && K > 1) {
             age = age + 1 < K - 1 ? age + 1 : K - 1;
-            if (s < a.L && a.starts[b * a.L + s]) {
-              clear<K>(win);
+            if (first >> m & 1) {
+              clear<K, 2>(win);
               age = 0;
             }
           }
-          float g[8];
+          float g[2];
           rx[r].get(win[K - 1]);
           ry[r].get(g);
+          if (a.silu)
 #pragma unroll
-          for (int k = K - 1; k > 0; --k)
+            for (int j = 0; j < 2; ++j) {
+              float z = bias[j];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[k][j] = d[k - 1][j];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (!live) win[K - 1][j] = 0.0f;
-            if (a.silu) {
-              float pre = bias[j], f, df;
-#pragma unroll
-              for (int k = 0; k < K; ++k) pre = fmaf(w[k][j], win[k][j], pre);
-              silu_both(pre, f, df);
-              g[j] *= df;
+              for (int k = 0; k < K; ++k) z = fmaf(w[k][j], win[k][j], z);
+              const float s = sigmoid_f(z);
+              g[j] *= fmaf(s, fmaf(-z, s, z), s);  // silu' = s + s z (1 - s)
             }
-            if (!live) g[j] = 0.0f;
-            d[0][j] = 0.0f;
+          if (EDGE && t0 + m >= len) win[K - 1][0] = win[K - 1][1] = g[0] = g[1] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-              if (!a.starts || k <= age) d[k][j] = fmaf(w[K - 1 - k][j], g[j], d[k][j]);
-            if (m0 + r < own) {
+          for (int k = K - 1; k > 0; --k) d[k][0] = d[k - 1][0], d[k][1] = d[k - 1][1];
+          d[0][0] = w[K - 1][0] * g[0], d[0][1] = w[K - 1][1] * g[1];
+#pragma unroll
+          for (int k = 1; k < K; ++k)
+            if (!EDGE || k <= age)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) d[k][j] = fmaf(w[K - 1 - k][j], g[j], d[k][j]);
+          if (m < kOwn)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
               for (int k = 0; k < K; ++k) dw[k][j] = fmaf(g[j], win[k][j], dw[k][j]);
               dw[K][j] += g[j];
             }
-          }
-          if (m0 + r >= K - 1 ? t < a.L : t < 0) {
-            if (K > 1 && a.dstate_final && t >= len - (K - 1) && t < len) {  // an input of the last state
+          if constexpr (EDGE)
+            if (K > 1 && a.dstate_final && t >= len - (K - 1) && t < len && (m >= K - 1 || t < 0)) {  // an input of the last state
               bool kept = true;
-              if (a.starts)
-                for (int64_t u = t < 0 ? 0 : t + 1; u < len; ++u) kept = kept && !a.starts[b * a.L + u];
+              if (MARKS && a.starts)
+                for (int u = t < 0 ? 0 : t + 1; u < len; ++u) kept = kept && !a.starts[b * L + u];
               if (kept) {
-                float f[8];
-                load_vec((const T *)a.dstate_final + (b * (K - 1) + t - len + (K - 1)) * a.D + c, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[K - 1][j] += f[j];
+                float f[2];
+                load2((const T *)a.dstate_final + (b * (K - 1) + t - len + (K - 1)) * a.D + c, f);
+                d[K - 1][0] += f[0], d[K - 1][1] += f[1];
               }
             }
-            if (t >= 0)
-              store_vec((T *)a.dx + (b * a.L + t) * a.D + c, d[K - 1]);
-            else if (a.dstate0)
-              store_vec((T *)a.dstate0 + (b * (K - 1) + t + (K - 1)) * a.D + c, d[K - 1]);
+          if (m >= K - 1) {
+            if (on && (!EDGE || t < L)) store2(dx + m * a.D, d[K - 1]);
+          } else if (K > 1 && t < 0 && a.dstate0) {
+            if (on) store2((T *)a.dstate0 + (b * (K - 1) + t + (K - 1)) * a.D + c, d[K - 1]);
           }
-          shift<K>(win);
+          shift<K, 2>(win);
         }
-      }
+      };
+      if ((MARKS && K > 1 && (age < K - 1 || (first >> m0 & ((1 << kRows) - 1)))) || t0 + m0 + kRows > len)
+        walk(Int<1>{});
+      else
+        walk(Int<0>{});
     }
   }
-  part += run * a.D * (K + 1);
 #pragma unroll
-  for (int k = 0; k <= K; ++k) {
-    __syncthreads();
-    store_vec(lds + threadIdx.x * 8, dw[k]);
-    __syncthreads();
-    if (slot == 0)
-      for (int r = 1; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[k][j] += lds[(r * CG + threadIdx.x) * 8 + j];
-    if (slot == 0 && on) {
-      if (k == K)
-        store_vec(part + a.D * K + c, dw[k]);
-      else
-#pragma unroll
-        for (int j = 0; j < 8; ++j) part[(c + j) * K + k] = dw[k][j];
-    }
+  for (int k = 0; k <= K; ++k) sums[wave][2 * k][lane] = dw[k][0], sums[wave][2 * k + 1][lane] = dw[k][1];
+  __syncthreads();
+  part += (int64_t)run * a.D * (K + 1);
+  for (int i = threadIdx.x; i < N * 64; i += 256) {
+    const int q = i >> 6, l = i & 63, k = q >> 1;
+    const int64_t ch = (ct * 64 + l) * 2 + (q & 1);
+    if (ch >= D) continue;
+    const float v = (sums[0][q][l] + sums[1][q][l]) + (sums[2][q][l] + sums[3][q][l]);
+    part[k == K ? (int64_t)D * K + ch : ch * K + k] = v;
   }
 }
 
@@ -296,30 +359,25 @@ __global__ void __launch_bounds__(256) conv_update_kernel(ConvArgs a) {
   for (int k = 0; k + 1 < K; ++k) store_vec(state + k * a.D, win[k + 1]);
 }
 
-template <int X>
-struct Int {
-  static constexpr int v = X;
-};
 template <typename F>
 hipError_t by_width(int width, F f) {
   return width == 1 ? f(Int<1>{}) : width == 2 ? f(Int<2>{}) : width == 3 ? f(Int<3>{}) : f(Int<4>{});
 }
 
-constexpr int kFwdSteps = 32, kBwdRows = 64;
+constexpr int kFwdSteps = 32;
+constexpr int64_t kBwdWorkgroups = 1280;  // resident at once: five of four waves per CU
 
 struct BwdPlan {
-  int cg;            // groups of 8 channels per workgroup
   int64_t ctiles, nchunk, nruns;
 };
 BwdPlan bwd_plan(int64_t B, int64_t L, int64_t D, int width) {
   BwdPlan p;
-  const int64_t n8 = D / 8;
-  p.cg = n8 >= 64 ? 64 : n8 >= 32 ? 32 : n8 >= 16 ? 16 : 8;
-  p.ctiles = (n8 + p.cg - 1) / p.cg;
   const int own = kBwdRows - (width - 1);
+  p.ctiles = (D + 127) / 128;
   p.nchunk = (L + own - 1) / own;
-  const int64_t need = (B * p.nchunk + 256 / p.cg - 1) / (256 / p.cg), most = p.ctiles < 1024 ? 1024 / p.ctiles : 1;
-  p.nruns = need < most ? need : most;
+  // equal numbers of chunks for all waves, of as many workgroups as are resident
+  const int64_t need = (B * p.nchunk + 3) / 4, most = p.ctiles < kBwdWorkgroups ? kBwdWorkgroups / p.ctiles : 1, each = (need + most - 1) / most;
+  p.nruns = (need + each - 1) / each;
   return p;
 }
 
@@ -333,19 +391,18 @@ hipError_t fwd(const ConvArgs &a, hipStream_t s) {
   });
 }
 
-template <typename T, int CG>
-hipError_t bwd_cg(const ConvArgs &a, const BwdPlan &p, hipStream_t s) {
-  return by_width(a.width, [&](auto k) {
-    hipLaunchKernelGGL((conv_bwd_kernel<T, decltype(k)::v, CG>), dim3((unsigned)(p.ctiles * p.nruns)), dim3(256), 0, s, a, p.nchunk, kBwdRows,
-                       (int)p.ctiles, p.nruns, (float *)a.workspace);
-    return hipGetLastError();
-  });
-}
-
 template <typename T>
 hipError_t bwd(const ConvArgs &a, hipStream_t s) {
   const BwdPlan p = bwd_plan(a.B, a.L, a.D, a.width);
-  const hipError_t e = p.cg == 64 ? bwd_cg<T, 64>(a, p, s) : p.cg == 32 ? bwd_cg<T, 32>(a, p, s) : p.cg == 16 ? bwd_cg<T, 16>(a, p, s) : bwd_cg<T, 8>(a, p, s);
+  const hipError_t e = by_width(a.width, [&](auto k) {
+    constexpr int K = decltype(k)::v;
+    const dim3 grid((unsigned)(p.ctiles * p.nruns));
+    if (a.starts || a.lengths)
+      hipLaunchKernelGGL((conv_bwd_kernel<T, K, true>), grid, dim3(256), 0, s, a, (int)p.nchunk, (int)p.ctiles, (int)p.nruns, (float *)a.workspace);
+    else
+      hipLaunchKernelGGL((conv_bwd_kernel<T, K, false>), grid, dim3(256), 0, s, a, (int)p.nchunk, (int)p.ctiles, (int)p.nruns, (float *)a.workspace);
+    return hipGetLastError();
+  });
   if (e != hipSuccess) return e;
   return launch_sum_rows((const float *)a.workspace, p.nruns, a.D * (a.width + 1), a.D * a.width, a.dweight, a.dbias, s);
 }

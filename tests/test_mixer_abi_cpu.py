@@ -84,7 +84,7 @@ def conv_fwd(lib, B=2, L=16, D=64, K=4, io=0, x=None, w=FAKE, b=None, s0=None, l
 
 
 @pytest.mark.parametrize("kw,want", SIZES + [
-    (dict(K=0), UNSUPPORTED), (dict(K=5), UNSUPPORTED), (dict(w=None), NULL_ARG), (dict(w=FAKE + 4), ALIGNMENT), (dict(b=FAKE + 4), ALIGNMENT),
+    (dict(B=1, D=8, L=(1 << 30) + 1), UNSUPPORTED), (dict(B=65536, D=1 << 15, L=1 << 9), UNSUPPORTED), (dict(K=0), UNSUPPORTED), (dict(K=5), UNSUPPORTED), (dict(w=None), NULL_ARG), (dict(w=FAKE + 4), ALIGNMENT), (dict(b=FAKE + 4), ALIGNMENT),
     (dict(s0=FAKE + 8), ALIGNMENT), (dict(y=None), NULL_ARG), (dict(y=FAKE + 8), ALIGNMENT), (dict(fin=FAKE + 8), ALIGNMENT), (dict(ln=FAKE + 1), ALIGNMENT),
     (dict(K=1, s0=FAKE), NULL_ARG), (dict(K=1, fin=FAKE), NULL_ARG)])
 def test_conv_refusals(lib, kw, want):
