@@ -155,14 +155,14 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int64_t nchun
 // Backward.  dpre_s = dy_s act'(pre_s);  dx_t = sum over taps `back` of w[K-1-back]
 // dpre_{t+back} where no document starts in (t, t+back];  dweight[k] = sum dpre_s x_{s-(K-1)+k}.
 //
-// A wave takes two channels per lane and walks over kBwdRows steps s with the inputs
+// A wave takes two channels per lane and walks over nrow steps s with the inputs
 // under the taps and the unfinished dx of the last K steps in registers: it yields
-// dx of kBwdRows - (K-1) steps t and as much of the weights' sums, which stay in registers
+// dx of nrow - (K-1) steps t and as much of the weights' sums, which stay in registers
 // over its chunks; a workgroup adds its waves' sums and a second kernel the workgroups', in order.
 // All of a wave is at the same step, so that steps, starts and lengths are scalar work.
 // Two channels and not eight: 74 registers' worth of sums and windows less, six waves per
 // SIMD instead of two (8 x 2048 x 2048 bf16: 101 us with eight).
-constexpr int kBwdRows = 64;  // as many starts of documents as a wave has lanes
+constexpr int kBwdRows = 120;  // at most: two words of starts of documents, offsets below 2^32 bytes
 
 template <typename T>
 struct Raw2;
@@ -199,8 +199,9 @@ __device__ __forceinline__ uint64_t start_bits(const uint8_t *starts, int64_t b,
 }
 
 template <typename T, int K, bool MARKS>
-__global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nchunk, int ctiles, int nruns, float *part) {
-  constexpr int kOwn = kBwdRows - (K - 1), N = 2 * (K + 1);
+__global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nrow, int nchunk, int ctiles, int nruns, float *part) {
+  constexpr int N = 2 * (K + 1);
+  const int own = nrow - (K - 1);
   __shared__ float sums[4][N][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int ct = uniform(blockIdx.x % ctiles), run = uniform(blockIdx.x / ctiles);
@@ -218,11 +219,11 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nchunk, i
   for (int k = 0; k <= K; ++k) dw[k][0] = dw[k][1] = 0.0f;
   const int items = (int)a.B * nchunk;
   for (int it = run * 4 + wave; it < items; it += nruns * 4) {
-    const int b32 = uniform(it / nchunk), t0 = uniform(it - b32 * nchunk) * kOwn;
+    const int b32 = uniform(it / nchunk), t0 = uniform(it - b32 * nchunk) * own;
     const int64_t b = b32;
     const int len = MARKS ? uniform(row_length(a.lengths, b, L)) : L;
-    const int rows = L - t0 < kBwdRows ? L - t0 : kBwdRows;
-    const uint64_t first = MARKS ? start_bits(a.starts, b, t0, L) : 0;
+    const int rows = L - t0 < nrow ? L - t0 : nrow;
+    const uint64_t first = MARKS ? start_bits(a.starts, b, t0, L) : 0, first2 = MARKS ? start_bits(a.starts, b, t0 + 64, L) : 0;
     const uint32_t xstep = (uint32_t)a.x.st * sizeof(T), ystep = (uint32_t)a.dy.st * sizeof(T);
     auto buffer = [&](const View3 &v, uint32_t step) {
       return __builtin_amdgcn_make_buffer_rsrc((char *)v.p + (b * v.sb + t0 * v.st) * (int64_t)sizeof(T), 0, (int)((rows - 1) * step + D * (uint32_t)sizeof(T)),
@@ -249,14 +250,21 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nchunk, i
       }
     }
     T *dx = (T *)a.dx + (b * L + t0 - (K - 1)) * a.D + c;
-    for (int m0 = 0; m0 < kBwdRows && m0 - (K - 1) < rows; m0 += kRows) {
-      Raw2<T> rx[kRows], ry[kRows];
+    Raw2<T> rx[kRows], ry[kRows], nx[kRows], ny[kRows];
+    auto load = [&](int m0) {  // the last row again behind it
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         const uint32_t m = m0 + r < rows ? m0 + r : rows - 1;
-        rx[r].load(bx, lane_bytes, m * xstep);
-        ry[r].load(by, lane_bytes, m * ystep);
+        nx[r].load(bx, lane_bytes, m * xstep);
+        ny[r].load(by, lane_bytes, m * ystep);
       }
+    };
+    load(0);
+    for (int m0 = 0; m0 < nrow && m0 - (K - 1) < rows; m0 += kRows) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) rx[r] = nx[r], ry[r] = ny[r];
+      if (m0 + kRows < nrow) load(m0 + kRows);  // on its way while these rows are walked over
+      const uint32_t firsts = MARKS ? (uint32_t)((m0 < 64 ? first >> m0 : first2 >> (m0 - 64)) & ((1 << kRows) - 1)) : 0;
       // EDGE: a document starts among these steps or just before, or the row ends
       auto walk = [&](auto edge) {
         constexpr bool EDGE = decltype(edge)::v;
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nchunk, i
           const int m = m0 + r, t = t0 + m - (K - 1);
           if constexpr (EDGE && MARKS && K > 1) {
             age = age + 1 < K - 1 ? age + 1 : K - 1;
-            if (first >> m & 1) {
+            if (firsts >> r & 1) {
               clear<K, 2>(win);
               age = 0;
             }
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nchunk, i
             if (!EDGE || k <= age)
 #pragma unroll
               for (int j = 0; j < 2; ++j) d[k][j] = fmaf(w[K - 1 - k][j], g[j], d[k][j]);
-          if (m < kOwn)
+          if (m < own)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -317,7 +325,7 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nchunk, i
           shift<K, 2>(win);
         }
       };
-      if ((MARKS && K > 1 && (age < K - 1 || (first >> m0 & ((1 << kRows) - 1)))) || t0 + m0 + kRows > len)
+      if ((MARKS && K > 1 && (age < K - 1 || firsts)) || t0 + m0 + kRows > len)
         walk(Int<1>{});
       else
         walk(Int<0>{});
@@ -365,20 +373,25 @@ hipError_t by_width(int width, F f) {
 }
 
 constexpr int kFwdSteps = 32;
-constexpr int64_t kBwdWorkgroups = 1280;  // resident at once: five of four waves per CU
 
+// Steps per wave and chunk, from 16 to kBwdRows: the workgroups that are resident at
+// once (four of four waves per CU in bf16, three in fp32) take equal numbers of chunks, and
+// the fewest steps in all are walked over, with the K-1 that a chunk shares with the next
+// and about 6 for its start (8 x 2048 x 2048 bf16 packed: 58 us with 64 steps, of which
+// 1088 workgroups are not all resident).
 struct BwdPlan {
   int64_t ctiles, nchunk, nruns;
+  int nrow;
 };
-BwdPlan bwd_plan(int64_t B, int64_t L, int64_t D, int width) {
-  BwdPlan p;
-  const int own = kBwdRows - (width - 1);
-  p.ctiles = (D + 127) / 128;
-  p.nchunk = (L + own - 1) / own;
-  // equal numbers of chunks for all waves, of as many workgroups as are resident
-  const int64_t need = (B * p.nchunk + 3) / 4, most = p.ctiles < kBwdWorkgroups ? kBwdWorkgroups / p.ctiles : 1, each = (need + most - 1) / most;
-  p.nruns = (need + each - 1) / each;
-  return p;
+BwdPlan bwd_plan(int64_t B, int64_t L, int64_t D, int width, int es) {
+  const int64_t ctiles = (D + 127) / 128, resident = es == 2 ? 1024 : 768, most = ctiles < resident ? resident / ctiles : 1;
+  BwdPlan best{};
+  int64_t least = -1;
+  for (int nrow = 16; nrow <= kBwdRows; nrow += kRows) {
+    const int64_t nchunk = (L + nrow - width) / (nrow - width + 1), need = (B * nchunk + 3) / 4, each = (need + most - 1) / most;
+    if (least < 0 || each * (nrow + 6) < least) least = each * (nrow + 6), best = {ctiles, nchunk, (need + each - 1) / each, nrow};
+  }
+  return best;
 }
 
 template <typename T>
@@ -393,14 +406,14 @@ hipError_t fwd(const ConvArgs &a, hipStream_t s) {
 
 template <typename T>
 hipError_t bwd(const ConvArgs &a, hipStream_t s) {
-  const BwdPlan p = bwd_plan(a.B, a.L, a.D, a.width);
+  const BwdPlan p = bwd_plan(a.B, a.L, a.D, a.width, sizeof(T));
   const hipError_t e = by_width(a.width, [&](auto k) {
     constexpr int K = decltype(k)::v;
     const dim3 grid((unsigned)(p.ctiles * p.nruns));
     if (a.starts || a.lengths)
-      hipLaunchKernelGGL((conv_bwd_kernel<T, K, true>), grid, dim3(256), 0, s, a, (int)p.nchunk, (int)p.ctiles, (int)p.nruns, (float *)a.workspace);
+      hipLaunchKernelGGL((conv_bwd_kernel<T, K, true>), grid, dim3(256), 0, s, a, p.nrow, (int)p.nchunk, (int)p.ctiles, (int)p.nruns, (float *)a.workspace);
     else
-      hipLaunchKernelGGL((conv_bwd_kernel<T, K, false>), grid, dim3(256), 0, s, a, (int)p.nchunk, (int)p.ctiles, (int)p.nruns, (float *)a.workspace);
+      hipLaunchKernelGGL((conv_bwd_kernel<T, K, false>), grid, dim3(256), 0, s, a, p.nrow, (int)p.nchunk, (int)p.ctiles, (int)p.nruns, (float *)a.workspace);
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
@@ -417,7 +430,10 @@ hipError_t update(const ConvArgs &a, hipStream_t s) {
 
 }  // namespace
 
-int64_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int width) { return bwd_plan(B, L, D, width).nruns * D * (width + 1) * 4; }
+int64_t conv_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int width) {
+  const int64_t a = bwd_plan(B, L, D, width, 2).nruns, b = bwd_plan(B, L, D, width, 4).nruns;
+  return (a > b ? a : b) * D * (width + 1) * 4;
+}
 
 hipError_t launch_conv_fwd(const ConvArgs &a, int io_dtype, hipStream_t s) { return io_dtype == 0 ? fwd<float>(a, s) : fwd<bf16>(a, s); }
 hipError_t launch_conv_bwd(const ConvArgs &a, int io_dtype, hipStream_t s) { return io_dtype == 0 ? bwd<float>(a, s) : bwd<bf16>(a, s); }
