@@ -248,7 +248,7 @@ int ssm_gated_recurrence_bwd(int64_t batch, int64_t seqlen, int64_t dim, int io_
 
 /*
  * One token: state (batch, dim) fp32 is updated in place; y (batch, dim)
- * contiguous, io_dtype.  batch * dim <= 2^33.
+ * contiguous, io_dtype.  batch * dim <= 2^32.
  */
 int ssm_gated_recurrence_update(int64_t batch, int64_t dim, int io_dtype, float *state, const ssm_view3 *x,
                                 const ssm_view3 *decay_gate, const ssm_view3 *input_gate,
@@ -270,7 +270,7 @@ int ssm_gated_recurrence_update(int64_t batch, int64_t dim, int io_dtype, float 
  *            they are not of the row's last document; NULL = not wanted
  *
  * dim: a multiple of 8 up to 2^23; batch <= 2^16; seqlen <= 2^30; batch * dim / 8 *
- * (ceil(seqlen / 32) + 1) <= 2^31 (and for one token the same with seqlen 1).
+ * (ceil(seqlen / 32) + 1) <= 2^30 (and for one token the same with seqlen 1).
  */
 int ssm_causal_conv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int width, int io_dtype,
                         const ssm_view3 *x, const float *weight, const float *bias, const void *state0,

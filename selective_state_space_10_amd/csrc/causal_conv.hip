@@ -2,7 +2,7 @@
 // with a state of the last inputs, gradients, one token.
 //
 // Every tensor is read and written once but for the rows that chunks share: a
-// lane owns 8 adjacent channels and walks over a chunk of steps with the last
+// lane owns a few adjacent channels and walks over a chunk of steps with the last
 // width - 1 inputs in registers; the rows before its chunk (and in the backward
 // those after it, whose outputs its inputs reach) are read again, mostly from L2.
 #include "mixer_device.hpp"
@@ -19,33 +19,33 @@ struct Int {
   static constexpr int v = X;
 };
 
-// 8 channels of a row as they lie in memory.
+// 4 channels of a row as they lie in memory.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) { a = ((const float4 *)p)[0], b = ((const float4 *)p)[1]; }
-  __device__ __forceinline__ void get(float (&v)[8]) const { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w; }
+  float4 a;
+  __device__ __forceinline__ void load(const float *p) { a = ((const float4 *)p)[0]; }
+  __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w; }
 };
 template <>
 struct Raw<bf16> {
-  uint4 a;
-  __device__ __forceinline__ void load(const bf16 *p) { a = *(const uint4 *)p; }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  uint2 a;
+  __device__ __forceinline__ void load(const bf16 *p) { a = *(const uint2 *)p; }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    const uint32_t w[2] = {a.x, a.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 2; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 };
 
-// weights of 8 channels, w[k][j], and their bias
+// weights of 4 channels, w[k][j], and their bias
 template <int K>
-__device__ __forceinline__ void load_weights(const ConvArgs &a, int64_t c, float (&w)[K][8], float (&bias)[8]) {
-  float flat[8 * K];
+__device__ __forceinline__ void load_weights(const ConvArgs &a, int64_t c, float (&w)[K][4], float (&bias)[4]) {
+  float flat[4 * K];
   load_vec(a.weight + c * K, flat);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     bias[j] = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) w[k][j] = flat[j * K + k];
@@ -55,9 +55,9 @@ __device__ __forceinline__ void load_weights(const ConvArgs &a, int64_t c, float
 
 // The input at step t < 0 of the state, zero without one and at other steps.
 template <typename T, int K>
-__device__ __forceinline__ void load_before(const ConvArgs &a, int64_t b, int64_t t, int64_t c, float (&v)[8]) {
+__device__ __forceinline__ void load_before(const ConvArgs &a, int64_t b, int64_t t, int64_t c, float (&v)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  for (int j = 0; j < 4; ++j) v[j] = 0.0f;
   if (K > 1 && t < 0 && a.state0) load_vec((const T *)a.state0 + (b * (K - 1) + t + (K - 1)) * a.D + c, v);
 }
 
@@ -80,7 +80,7 @@ __device__ __forceinline__ void shift(float (&win)[K][V]) {
 
 // The inputs before step t0, into win[0 .. K-2]; none behind the row's length.
 template <typename T, int K>
-__device__ __forceinline__ void load_window(const ConvArgs &a, int64_t b, int64_t t0, int len, int64_t c, float (&win)[K][8]) {
+__device__ __forceinline__ void load_window(const ConvArgs &a, int64_t b, int64_t t0, int len, int64_t c, float (&win)[K][4]) {
 #pragma unroll
   for (int k = 0; k + 1 < K; ++k) {
     const int64_t t = t0 - (K - 1) + k;
@@ -97,21 +97,21 @@ __device__ __forceinline__ void load_window(const ConvArgs &a, int64_t b, int64_
 #pragma unroll
         for (int m = 0; m < k; ++m)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) win[m][j] = 0.0f;
+          for (int j = 0; j < 4; ++j) win[m][j] = 0.0f;
     }
 }
 
-// Threads: (batch row, chunk, 8 channels), channels fastest; behind them one for
-// every 8 channels of the last states.
+// Threads: (batch row, chunk, 4 channels), channels fastest; behind them one for
+// every 4 channels of the last states.
 template <typename T, int K>
 __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int64_t nchunk, int steps, int64_t main_threads) {
-  const int64_t n8 = a.D / 8;
+  const int64_t n4 = a.D / 4;
   int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i < main_threads) {
-    const int64_t c = i % n8 * 8, bc = i / n8, b = bc / nchunk, t0 = bc % nchunk * steps;
+    const int64_t c = i % n4 * 4, bc = i / n4, b = bc / nchunk, t0 = bc % nchunk * steps;
     const int len = row_length(a.lengths, b, a.L);
     const int64_t t1 = t0 + steps < a.L ? t0 + steps : a.L;
-    float w[K][8], bias[8], win[K][8];
+    float w[K][4], bias[4], win[K][4];
     load_weights<K>(a, c, w, bias);
     load_window<T, K>(a, b, t0, len, c, win);
     const T *x = (const T *)a.x.p + b * a.x.sb + c;
@@ -123,11 +123,11 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int64_t nchun
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         if (t + r >= t1) break;
-        if (a.starts && a.starts[b * a.L + t + r]) clear<K, 8>(win);
+        if (a.starts && a.starts[b * a.L + t + r]) clear<K, 4>(win);
         raw[r].get(win[K - 1]);
-        float v[8];
+        float v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           v[j] = bias[j];
 #pragma unroll
           for (int k = 0; k < K; ++k) v[j] = fmaf(w[k][j], win[k][j], v[j]);
@@ -135,17 +135,17 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int64_t nchun
           if (t + r >= len) v[j] = 0.0f;
         }
         store_vec(y + (t + r) * a.D, v);
-        shift<K, 8>(win);
+        shift<K, 4>(win);
       }
     }
     return;
   }
   if constexpr (K > 1) {
     i -= main_threads;
-    if (!a.state_final || i >= a.B * n8) return;
-    const int64_t b = i / n8, c = i % n8 * 8;
+    if (!a.state_final || i >= a.B * n4) return;
+    const int64_t b = i / n4, c = i % n4 * 4;
     const int len = row_length(a.lengths, b, a.L);
-    float win[K][8];
+    float win[K][4];
     load_window<T, K>(a, b, len, len, c, win);
 #pragma unroll
     for (int k = 0; k + 1 < K; ++k) store_vec((T *)a.state_final + (b * (K - 1) + k) * a.D + c, win[k]);
@@ -346,17 +346,17 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nrow, int
 
 template <typename T, int K>
 __global__ void __launch_bounds__(256) conv_update_kernel(ConvArgs a) {
-  const int64_t n8 = a.D / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.B * n8) return;
-  const int64_t b = i / n8, c = i % n8 * 8;
+  const int64_t n4 = a.D / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.B * n4) return;
+  const int64_t b = i / n4, c = i % n4 * 4;
   T *state = (T *)a.state + b * (K - 1) * a.D + c;
-  float w[K][8], bias[8], win[K][8], v[8];
+  float w[K][4], bias[4], win[K][4], v[4];
 #pragma unroll
   for (int k = 0; k + 1 < K; ++k) load_vec(state + k * a.D, win[k]);
   load_vec((const T *)a.x.p + b * a.x.sb + c, win[K - 1]);
   load_weights<K>(a, c, w, bias);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     v[j] = bias[j];
 #pragma unroll
     for (int k = 0; k < K; ++k) v[j] = fmaf(w[k][j], win[k][j], v[j]);
@@ -396,8 +396,8 @@ BwdPlan bwd_plan(int64_t B, int64_t L, int64_t D, int width, int es) {
 
 template <typename T>
 hipError_t fwd(const ConvArgs &a, hipStream_t s) {
-  const int64_t nchunk = (a.L + kFwdSteps - 1) / kFwdSteps, n8 = a.D / 8, main = a.B * nchunk * n8;
-  const int64_t threads = main + (a.state_final ? a.B * n8 : 0);
+  const int64_t nchunk = (a.L + kFwdSteps - 1) / kFwdSteps, n4 = a.D / 4, main = a.B * nchunk * n4;
+  const int64_t threads = main + (a.state_final ? a.B * n4 : 0);
   return by_width(a.width, [&](auto k) {
     hipLaunchKernelGGL((conv_fwd_kernel<T, decltype(k)::v>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, nchunk, kFwdSteps, main);
     return hipGetLastError();
@@ -423,7 +423,7 @@ hipError_t bwd(const ConvArgs &a, hipStream_t s) {
 template <typename T>
 hipError_t update(const ConvArgs &a, hipStream_t s) {
   return by_width(a.width, [&](auto k) {
-    hipLaunchKernelGGL((conv_update_kernel<T, decltype(k)::v>), dim3((unsigned)((a.B * (a.D / 8) + 255) / 256)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((conv_update_kernel<T, decltype(k)::v>), dim3((unsigned)((a.B * (a.D / 4) + 255) / 256)), dim3(256), 0, s, a);
     return hipGetLastError();
   });
 }

@@ -37,14 +37,27 @@ __device__ __forceinline__ float2 cos_sin(double turns) {
   return make_float2(n == 1 || n == 2 ? -u : u, n >= 2 ? -v : v);
 }
 
-// The elements one[i], two[i] of a lane are a pair; x holds its two pieces.
-__device__ __forceinline__ void to_pairs(const float (&x)[8], bool interleaved, float (&one)[4], float (&two)[4]) {
+// A lane's two pieces of a head as they lie in memory; the elements one[i], two[i]
+// are a pair.
+template <typename T>
+struct Pieces {
+  typename Vec4<T>::raw lo, hi;
+  __device__ __forceinline__ void load(const T *p, int o1, int o2) { lo = Vec4<T>::load(p, o1), hi = Vec4<T>::load(p, o2); }
+  template <bool INTER>
+  __device__ __forceinline__ void get(float (&one)[4], float (&two)[4]) const {
+    const float4 a = Vec4<T>::cvt(lo), b = Vec4<T>::cvt(hi);
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) one[i] = interleaved ? x[2 * i] : x[i], two[i] = interleaved ? x[2 * i + 1] : x[4 + i];
-}
-__device__ __forceinline__ void from_pairs(const float (&one)[4], const float (&two)[4], bool interleaved, float (&x)[8]) {
+    for (int i = 0; i < 4; ++i) one[i] = x[INTER ? 2 * i : i], two[i] = x[INTER ? 2 * i + 1 : 4 + i];
+  }
+};
+template <bool INTER>
+__device__ __forceinline__ void split(const float (&one)[4], const float (&two)[4], float (&lo)[4], float (&hi)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = interleaved ? (i & 1 ? two[i / 2] : one[i / 2]) : (i < 4 ? one[i] : two[i - 4]);
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = INTER ? (i & 1 ? two[i / 2] : one[i / 2]) : one[i];
+    hi[i] = INTER ? (i & 1 ? two[2 + i / 2] : one[2 + i / 2]) : two[i];
+  }
 }
 
 template <int TPR>
@@ -64,70 +77,68 @@ __device__ __forceinline__ void fill_table(const HeadNormArgs &a, int64_t b, int
   }
 }
 
-template <typename T, int TPR, bool BWD>
+template <typename T, int TPR, bool BWD, bool INTER>
 __global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadNormArgs a, Plan plan, float *part) {
   __shared__ alignas(16) float2 table[kMaxTable];
   const int half = a.rot / 2, HT = a.Hq + a.Hk;
   const int blk = (int)(blockIdx.x % plan.nblk), grp = threadIdx.x / TPR, p = threadIdx.x % TPR;
   const int64_t run = blockIdx.x / plan.nblk;
   const int hl = grp % plan.hb, sub = grp / plan.hb, h = blk * plan.hb + hl;
-  const bool mine = sub < plan.tsub && h < HT && hl < plan.hb, on = mine && p < a.d / 8;
-  const bool is_q = h < a.Hq;
-  const int hh = is_q ? h : h - a.Hq;
+  const bool mine = sub < plan.tsub && h < HT, on = mine && p < a.d / 8;
+  const bool is_q = h < a.Hq, rotated = p < a.rot / 8;
+  const int hh = is_q ? h : h - a.Hq, nh = is_q ? a.Hq : a.Hk;
   const HeadView &src = is_q ? a.q : a.k, &up = is_q ? a.dq_out : a.dk_out;
   T *dst = (T *)(BWD ? (is_q ? a.dq : a.dk) : (is_q ? a.q_out : a.k_out));
-  const int nh = is_q ? a.Hq : a.Hk;
-  const bool rotated = p < a.rot / 8, inter = a.interleaved && rotated;
   // where the lane's two pieces begin
-  const int o1 = rotated && !inter ? 4 * p : 8 * p, o2 = rotated && !inter ? 4 * p + half : 8 * p + 4;
-  float x[8], w1[4], w2[4], acc1[4], acc2[4];
+  const int o1 = rotated && !INTER ? 4 * p : 8 * p, o2 = rotated && !INTER ? 4 * p + half : 8 * p + 4;
+  float w1[4], w2[4], acc1[4], acc2[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w1[i] = w2[i] = 1.0f, acc1[i] = acc2[i] = 0.0f;
-  auto load_row = [&](const T *q, float (&v)[8]) {
-    float lo[4], hi[4];
-    load_vec(q + o1, lo);
-    load_vec(q + o2, hi);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
-  };
   const float *wp = is_q ? a.wq : a.wk;
   if (on && wp) {
-    float lo[4], hi[4];
-    load_vec(wp + hh * a.w_h + o1, lo);
-    load_vec(wp + hh * a.w_h + o2, hi);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
-    to_pairs(x, inter, w1, w2);
+    Pieces<float> w;
+    w.load(wp + hh * a.w_h, o1, o2);
+    w.template get<INTER>(w1, w2);
   }
+  const float over_d = 1.0f / (float)a.d;
   const int tt = plan.tsub * plan.rows;  // tokens of a chunk
   const int64_t row_chunks = (a.L + tt - 1) / tt;
   for (int64_t ch = run; ch < plan.nchunk; ch += plan.nruns) {
     const int64_t b = ch / row_chunks, t0 = ch % row_chunks * tt;
     const int n = (int)(a.L - t0 < tt ? a.L - t0 : tt);
-    const T *xp = (const T *)src.p + b * src.sb + t0 * src.st + hh * src.sh;
-    const T *up_p = BWD ? (const T *)up.p + b * up.sb + t0 * up.st + hh * up.sh : nullptr;
-    T *out = dst + ((b * a.L + t0) * nh + hh) * a.d;
+    const T *xp = (const T *)src.p + b * src.sb + (t0 + sub) * src.st + hh * src.sh;
+    const T *gp = BWD ? (const T *)up.p + b * up.sb + (t0 + sub) * up.st + hh * up.sh : nullptr;
+    T *out = dst + ((b * a.L + t0 + sub) * nh + hh) * a.d;
+    // a row is loaded while the one before it is worked on, the first while the angles are
+    Pieces<T> next, next_g;
+    const int mine_n = on ? n : 0;
+    if (sub < mine_n) {
+      next.load(xp, o1, o2);
+      if (BWD) next_g.load(gp, o1, o2);
+    }
     __syncthreads();  // the table's last readers are done
     fill_table(a, b, t0, n, table);
     __syncthreads();
-    for (int tok = sub; tok < n; tok += plan.tsub) {
-      if (!mine) break;
-      float one[4], two[4], g1[4], g2[4], ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) one[i] = two[i] = g1[i] = g2[i] = 0.0f;
+    for (int tok = sub; mine && tok < n; tok += plan.tsub) {
+      float one[4] = {}, two[4] = {}, g1[4] = {}, g2[4] = {};
       if (on) {
-        load_row(xp + tok * src.st, x);
-        to_pairs(x, inter, one, two);
-        if constexpr (BWD) {
-          load_row(up_p + tok * up.st, x);
-          to_pairs(x, inter, g1, g2);
+        next.template get<INTER>(one, two);
+        if (BWD) next_g.template get<INTER>(g1, g2);
+      }
+      if (tok + plan.tsub < mine_n) {
+        xp += plan.tsub * src.st;
+        next.load(xp, o1, o2);
+        if (BWD) {
+          gp += plan.tsub * up.st;
+          next_g.load(gp, o1, o2);
         }
       }
       float rstd = 1.0f;
       if (a.norm) {
+        float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) ss = fmaf(one[i], one[i], fmaf(two[i], two[i], ss));
-        rstd = rsqrtf(head_sum<TPR>(ss) / (float)a.d + a.eps);
+        rstd = rsqrtf(head_sum<TPR>(ss) * over_d + a.eps);
       }
       float2 cs[4];
       if (rotated)
@@ -135,38 +146,46 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadNormArgs a, Pla
         for (int i = 0; i < 4; ++i) cs[i] = table[tok * half + 4 * p + i];
       if constexpr (!BWD) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float n1 = one[i] * rstd * w1[i], n2 = two[i] * rstd * w2[i];
-          one[i] = rotated ? fmaf(n1, cs[i].x, -n2 * cs[i].y) : n1;
-          two[i] = rotated ? fmaf(n2, cs[i].x, n1 * cs[i].y) : n2;
-        }
+        for (int i = 0; i < 4; ++i) one[i] *= rstd * w1[i], two[i] *= rstd * w2[i];
+        if (rotated)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float n1 = one[i], n2 = two[i];
+            one[i] = fmaf(n1, cs[i].x, -n2 * cs[i].y);
+            two[i] = fmaf(n2, cs[i].x, n1 * cs[i].y);
+          }
       } else {
         // u = the gradient of n, turned back; with hat = x rstd: dx = rstd (u w - hat mean(u w hat))
         float s = 0.0f;
+        if (rotated)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float u1 = fmaf(g1[i], cs[i].x, g2[i] * cs[i].y), u2 = fmaf(g2[i], cs[i].x, -g1[i] * cs[i].y);
+            g1[i] = u1, g2[i] = u2;
+          }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float u1 = rotated ? fmaf(g1[i], cs[i].x, g2[i] * cs[i].y) : g1[i];
-          const float u2 = rotated ? fmaf(g2[i], cs[i].x, -g1[i] * cs[i].y) : g2[i];
           one[i] *= rstd, two[i] *= rstd;
-          acc1[i] = fmaf(u1, one[i], acc1[i]), acc2[i] = fmaf(u2, two[i], acc2[i]);
-          g1[i] = u1 * w1[i], g2[i] = u2 * w2[i];
+          acc1[i] = fmaf(g1[i], one[i], acc1[i]), acc2[i] = fmaf(g2[i], two[i], acc2[i]);
+          g1[i] *= w1[i], g2[i] *= w2[i];
           s = fmaf(g1[i], one[i], fmaf(g2[i], two[i], s));
         }
-        s = a.norm ? head_sum<TPR>(s) / (float)a.d : 0.0f;
+        if (a.norm) {
+          s = head_sum<TPR>(s) * over_d;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          one[i] = a.norm ? rstd * (g1[i] - one[i] * s) : g1[i];
-          two[i] = a.norm ? rstd * (g2[i] - two[i] * s) : g2[i];
+          for (int i = 0; i < 4; ++i) one[i] = rstd * fmaf(-one[i], s, g1[i]), two[i] = rstd * fmaf(-two[i], s, g2[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) one[i] = g1[i], two[i] = g2[i];
         }
       }
       if (on) {
-        from_pairs(one, two, inter, x);
         float lo[4], hi[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lo[i] = x[i], hi[i] = x[4 + i];
-        store_vec(out + (int64_t)tok * nh * a.d + o1, lo);
-        store_vec(out + (int64_t)tok * nh * a.d + o2, hi);
+        split<INTER>(one, two, lo, hi);
+        store_vec(out + o1, lo);
+        store_vec(out + o2, hi);
       }
+      out += (int64_t)plan.tsub * nh * a.d;
     }
   }
   if constexpr (BWD) {
@@ -177,10 +196,11 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadNormArgs a, Pla
     float *lds = (float *)table;
     static_assert(sizeof(table) >= kThreads * 8 * sizeof(float), "the sums fit where the angles were");
     __syncthreads();
-    from_pairs(acc1, acc2, inter, x);
+    float lo[4], hi[4];
+    split<INTER>(acc1, acc2, lo, hi);
     if (on) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lds[grp * a.d + o1 + i] = x[i], lds[grp * a.d + o2 + i] = x[4 + i];
+      for (int i = 0; i < 4; ++i) lds[grp * a.d + o1 + i] = lo[i], lds[grp * a.d + o2 + i] = hi[i];
     }
     __syncthreads();
     if (a.w_h) {
@@ -204,17 +224,28 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadNormArgs a, Pla
   }
 }
 
-constexpr int64_t kFwdWorkgroups = 2048, kBwdWorkgroups = 1024;
+constexpr int64_t kFwdWorkgroups = 65536, kBwdWorkgroups = 1024;
 
 int64_t most_runs(int nblk, int64_t workgroups) { return nblk < workgroups ? workgroups / nblk : 1; }
 
+int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
+int least_blocks(int HT, int tpr) { return (HT + kThreads / tpr - 1) / (kThreads / tpr); }
+constexpr int kMoreBlocks = 8;
+
 Plan plan_of(int64_t B, int64_t L, int HT, int d, int rot, int64_t workgroups) {
   Plan p;
-  p.tpr = d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32;
+  p.tpr = lanes_of(d);
+  // Blocks of heads: few, since each forms the angles of its tokens, and so that few groups
+  // of lanes are left over.  Per token: a row is about 120 instructions of a lane, an
+  // angle 50 of one of the workgroup's lanes (36 heads of 64 on 32 groups in 5 blocks of 8
+  // heads and 4 tokens, not in 2 of 18 and one).
   const int groups = kThreads / p.tpr;
-  p.nblk = (HT + groups - 1) / groups;
-  p.hb = (HT + p.nblk - 1) / p.nblk;
-  p.tsub = groups / p.hb;
+  double least = 0.0;
+  for (int nblk = least_blocks(HT, p.tpr); nblk <= HT && nblk <= least_blocks(HT, p.tpr) + kMoreBlocks; ++nblk) {
+    const int hb = (HT + nblk - 1) / nblk, tsub = groups / hb;
+    const double cost = 120.0 * nblk / tsub + 50.0 * nblk * (rot / 2) / kThreads;
+    if (least == 0.0 || cost < least) least = cost, p.nblk = (HT + hb - 1) / hb, p.hb = hb, p.tsub = tsub;
+  }
   p.rows = kMaxRows;
   while (p.rows > 1 && (p.tsub * p.rows * (rot / 2) > kMaxTable)) p.rows /= 2;
   const int64_t tt = p.tsub * p.rows;
@@ -234,20 +265,28 @@ HeadNormArgs merged(HeadNormArgs a, bool bwd) {
   return a;
 }
 
+template <typename T, int TPR, bool BWD>
+void launch_tpr(const HeadNormArgs &a, const Plan &p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.nblk * p.nruns));
+  if (a.interleaved)
+    hipLaunchKernelGGL((head_norm_kernel<T, TPR, BWD, true>), grid, dim3(kThreads), 0, s, a, p, (float *)a.workspace);
+  else
+    hipLaunchKernelGGL((head_norm_kernel<T, TPR, BWD, false>), grid, dim3(kThreads), 0, s, a, p, (float *)a.workspace);
+}
+
 template <typename T, bool BWD>
 hipError_t launch(const HeadNormArgs &given, hipStream_t s) {
   const HeadNormArgs a = merged(given, BWD);
   const Plan p = plan_of(a.B, a.L, a.Hq + a.Hk, a.d, a.rot, BWD ? kBwdWorkgroups : kFwdWorkgroups);
-  const dim3 grid((unsigned)(p.nblk * p.nruns));
-  float *part = (float *)a.workspace;
+  const float *part = (const float *)a.workspace;
   if (p.tpr == 4)
-    hipLaunchKernelGGL((head_norm_kernel<T, 4, BWD>), grid, dim3(kThreads), 0, s, a, p, part);
+    launch_tpr<T, 4, BWD>(a, p, s);
   else if (p.tpr == 8)
-    hipLaunchKernelGGL((head_norm_kernel<T, 8, BWD>), grid, dim3(kThreads), 0, s, a, p, part);
+    launch_tpr<T, 8, BWD>(a, p, s);
   else if (p.tpr == 16)
-    hipLaunchKernelGGL((head_norm_kernel<T, 16, BWD>), grid, dim3(kThreads), 0, s, a, p, part);
+    launch_tpr<T, 16, BWD>(a, p, s);
   else
-    hipLaunchKernelGGL((head_norm_kernel<T, 32, BWD>), grid, dim3(kThreads), 0, s, a, p, part);
+    launch_tpr<T, 32, BWD>(a, p, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !BWD || !a.dwq) return e;
   return a.w_h ? launch_sum_rows(part, p.nruns, (int64_t)(a.Hq + a.Hk) * a.d, (int64_t)a.Hq * a.d, a.dwq, a.dwk, s)
@@ -256,12 +295,12 @@ hipError_t launch(const HeadNormArgs &given, hipStream_t s) {
 
 }  // namespace
 
-// The largest that any rotation and any strides of these sizes need.
+// The largest that any rotation, any strides and either kind of weights of these sizes need.
 int64_t head_norm_bwd_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d) {
-  const Plan p = plan_of(1, 1, (int)(Hq + Hk), (int)d, 0, kBwdWorkgroups);
-  const int64_t most = most_runs(p.nblk, kBwdWorkgroups), runs = B * L < most ? B * L : most;
-  const int64_t row = 2 * p.nblk > Hq + Hk ? 2 * p.nblk : Hq + Hk;
-  return runs * row * d * 4;
+  const int64_t HT = Hq + Hk, N = B * L, few = least_blocks((int)HT, lanes_of((int)d)), many = few + kMoreBlocks;
+  const int64_t runs = most_runs((int)few, kBwdWorkgroups), per_head = (N < runs ? N : runs) * HT;
+  const int64_t all = many < kBwdWorkgroups ? kBwdWorkgroups : many, shared = 2 * (N < all / many ? N * many : all);
+  return (per_head > shared ? per_head : shared) * d * 4;
 }
 
 hipError_t launch_head_norm_fwd(const HeadNormArgs &a, int io_dtype, hipStream_t s) { return io_dtype == 0 ? launch<float, false>(a, s) : launch<bf16, false>(a, s); }

@@ -37,12 +37,12 @@ int check_recurrence(int64_t batch, int64_t seqlen, int64_t dim) {
   return SSM_OK;
 }
 
-// The same for threads of 8 channels and up to 32 steps, and of 8 channels of a last state.
+// The same for threads of 4 channels and up to 32 steps, and of 4 channels of a last state.
 int check_conv(int64_t batch, int64_t seqlen, int64_t dim) {
   SSM_TRY(check_seq(batch, seqlen, dim));
   if (seqlen > ((int64_t)1 << 30)) return api_fail(SSM_ERR_UNSUPPORTED, "seqlen=%lld exceeds 2^30", (long long)seqlen);
-  if (batch * (dim / 8) > ((int64_t)1 << 31) / ((seqlen + 31) / 32 + 1))
-    return api_fail(SSM_ERR_UNSUPPORTED, "batch * dim / 8 * (ceil(seqlen / 32) + 1) exceeds 2^31");
+  if (batch * (dim / 8) > ((int64_t)1 << 30) / ((seqlen + 31) / 32 + 1))
+    return api_fail(SSM_ERR_UNSUPPORTED, "batch * dim / 8 * (ceil(seqlen / 32) + 1) exceeds 2^30");
   return SSM_OK;
 }
 
