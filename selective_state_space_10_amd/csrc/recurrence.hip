@@ -498,13 +498,13 @@ __global__ void __launch_bounds__(256) recurrence_clear_kernel(uint4 *p, int64_t
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// One token: 8 channels per lane.
+// One token: 4 channels per lane.
 template <typename T, bool POWER>
 __global__ void __launch_bounds__(256) recurrence_update_kernel(RecurrenceUpdateArgs a) {
-  const int64_t n8 = a.D / 8, i8 = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i8 >= a.B * n8) return;
-  const int64_t b = i8 / n8, c = i8 % n8 * 8;
-  float x[8], g[8], i[8], z[8], h[8], l[8];
+  const int64_t n4 = a.D / 4, i4 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i4 >= a.B * n4) return;
+  const int64_t b = i4 / n4, c = i4 % n4 * 4;
+  float x[4], g[4], i[4], z[4], h[4], l[4];
   load_vec((const T *)a.x.p + b * a.x.sb + c, x);
   load_vec((const T *)a.g.p + b * a.g.sb + c, g);
   if (a.ig.p) load_vec((const T *)a.ig.p + b * a.ig.sb + c, i);
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(256) recurrence_update_kernel(RecurrenceUpdate
   if (POWER) load_vec(a.decay + c, l);
   load_vec(a.state + b * a.D + c, h);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     const Gate q = gate_of<POWER>(g[j], POWER ? rate_of(a.sharpness, l[j]) : 0.0f);
     h[j] = fmaf(q.a, h[j], q.s * (a.ig.p ? x[j] * sigmoid_f(i[j]) : x[j]));
     x[j] = a.z.p ? h[j] * silu_f(z[j]) : h[j];
@@ -600,7 +600,7 @@ hipError_t bwd(const RecurrenceArgs &a, hipStream_t s) {
 
 template <typename T>
 hipError_t update(const RecurrenceUpdateArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.B * (a.D / 8) + 255) / 256));
+  const dim3 grid((unsigned)((a.B * (a.D / 4) + 255) / 256));
   if (a.decay)
     hipLaunchKernelGGL((recurrence_update_kernel<T, true>), grid, dim3(256), 0, s, a);
   else
