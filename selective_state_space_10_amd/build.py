@@ -18,7 +18,7 @@ ARCH = "gfx950"
 SOURCES = ["ssm_api.cpp", "scan_fwd.hip", "scan_bwd.hip", "state_update.hip", "affine_scan.hip",
            "block_api.cpp", "decay_attn.hip", "decay_attn_f32.hip", "decay_attn_bf16.hip",
            "decay_update.hip", "block_norm.hip", "mixer_api.cpp", "recurrence.hip",
-           "causal_conv.hip", "head_norm.hip"]
+           "causal_conv.hip", "head_norm.hip", "sum_rows.hip"]
 # the vector-ALU rate probes (a measurement tool beside the library)
 PROBE_SOURCES = ["alu_probe.hip"]
 PROBE_LIB = os.path.join(HERE, "libssm_alu_probe.so")

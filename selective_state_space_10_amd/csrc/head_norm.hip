@@ -67,15 +67,26 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// The cosines and sines of tokens t0 .. t0 + n of a batch row.
-__device__ __forceinline__ void fill_table(const HeadNormArgs &a, int64_t b, int64_t t0, int n, float2 *table) {
-  const int half = a.rot / 2;
-  for (int i = threadIdx.x; i < n * half; i += kThreads) {
-    const int tok = i / half, p = i - tok * half;
-    const double turns = (double)a.pos[b * a.pos_b + t0 + tok] * (a.inv_freq[p] * 0.15915494309189535);
-    table[i] = cos_sin(turns - rint(turns));
+// One thread's angles of a chunk of tokens: one frequency, every `step`-th token.
+struct Angles {
+  int p, tok, step;
+  double turns;  // per position
+  __device__ __forceinline__ explicit Angles(const HeadNormArgs &a) {
+    const int half = a.rot / 2;
+    step = half ? kThreads / half : 0;
+    p = half ? threadIdx.x % half : 0, tok = half ? threadIdx.x / half : 0;
+    if (tok >= step) step = 0;  // (threads left over, or nothing to rotate)
+    turns = step ? a.inv_freq[p] * 0.15915494309189535 : 0.0;
   }
-}
+  // cosines and sines of tokens t0 .. t0 + n of a batch row
+  __device__ __forceinline__ void fill(const HeadNormArgs &a, int64_t b, int64_t t0, int n, float2 *table) const {
+    if (step == 0) return;
+    for (int t = tok; t < n; t += step) {
+      const double x = (double)a.pos[b * a.pos_b + t0 + t] * turns;
+      table[t * (a.rot / 2) + p] = cos_sin(x - rint(x));
+    }
+  }
+};
 
 template <typename T, int TPR, bool BWD, bool INTER>
 __global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadNormArgs a, Plan plan, float *part) {
@@ -101,6 +112,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadNormArgs a, Pla
     w.template get<INTER>(w1, w2);
   }
   const float over_d = 1.0f / (float)a.d;
+  const Angles angles(a);
   const int tt = plan.tsub * plan.rows;  // tokens of a chunk
   const int64_t row_chunks = (a.L + tt - 1) / tt;
   for (int64_t ch = run; ch < plan.nchunk; ch += plan.nruns) {
@@ -117,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadNormArgs a, Pla
       if (BWD) next_g.load(gp, o1, o2);
     }
     __syncthreads();  // the table's last readers are done
-    fill_table(a, b, t0, n, table);
+    angles.fill(a, b, t0, n, table);
     __syncthreads();
     for (int tok = sub; mine && tok < n; tok += plan.tsub) {
       float one[4] = {}, two[4] = {}, g1[4] = {}, g2[4] = {};

@@ -1,4 +1,19 @@
-// recurrence.hip -- the gated recurrence h_t = a_t h_{t-1} + s_t i_t x_t.
+// recurrence.hip -- the gated recurrence h_t = a_t h_{t-1} + s_t i_t x_t over whole
+// sequences, its gradients, and one token.
+//
+// Every input is read once and every output written once, and the bytes are the
+// floor; what keeps the kernels above it is that a workgroup loads, computes, waits for
+// the state before its chunk and stores in turn, and registers let only two workgroups
+// share a CU.  Vector units are active for half of the time (37 vector instructions
+// per element forward, 6 of them transcendental, and 63 with 7 backward), waves wait two fifths of it.
+// Measured, per call (a large copy moves 5.1 TB/s), bf16 in power form with an input gate:
+//   forward   8 x 2048 x 2048 (268 MB)            66 us, 4.0 TB/s (one lane per channel: 1782 us)
+//             4 x 4096 x 5120 (671 MB)           145 us, 4.6 TB/s
+//             1 x 32768 x 5120, z (1.68 GB)      377 us, 4.5 TB/s
+//             1 x 1048576 x 1024 (8.6 GB)        2.1 ms, 4.1 TB/s
+//   backward  8 x 2048 x 2048 (471 MB)           127 us, 3.7 TB/s (one lane per channel: 3298 us)
+//             1 x 32768 x 5120, z (3.0 GB)       740 us, 4.1 TB/s
+//   one token 256 x 5120, z (23 MB)              7.5 us
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
 
@@ -627,50 +642,6 @@ hipError_t launch_recurrence_bwd(const RecurrenceArgs &a, int io_dtype, hipStrea
 }
 hipError_t launch_recurrence_update(const RecurrenceUpdateArgs &a, int io_dtype, hipStream_t s) {
   return io_dtype == 0 ? update<float>(a, s) : update<bf16>(a, s);
-}
-
-// ---- sums over rows of partial sums
-
-namespace {
-
-// A workgroup takes 16 columns, 64 lanes' worth of rows each in turn; sums in a
-// fixed order.
-__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, int64_t rows, int64_t n, int64_t split, float *out, float *out2) {
-  __shared__ float s[64][17];
-  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const int64_t col = (int64_t)blockIdx.x * 16 + c;
-  float v = 0.0f;
-  if (col < n) {
-    constexpr int U = 4;  // loads under way
-    int64_t i = r;
-    for (; i + 64 * (U - 1) < rows; i += 64 * U) {
-      float x[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = part[(i + 64 * u) * n + col];
-#pragma unroll
-      for (int u = 0; u < U; ++u) v += x[u];
-    }
-    for (; i < rows; i += 64) v += part[i * n + col];
-  }
-  s[r][c] = v;
-  __syncthreads();
-  for (int m = 32; m >= 1; m >>= 1) {
-    if (r < m) s[r][c] += s[r + m][c];
-    __syncthreads();
-  }
-  if (r == 0 && col < n) {
-    if (col < split)
-      out[col] = s[0][c];
-    else if (out2)
-      out2[col - split] = s[0][c];
-  }
-}
-
-}  // namespace
-
-hipError_t launch_sum_rows(const float *part, int64_t rows, int64_t n, int64_t split, float *out, float *out2, hipStream_t stream) {
-  hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((n + 15) / 16)), dim3(1024), 0, stream, part, rows, n, split, out, out2);
-  return hipGetLastError();
 }
 
 }  // namespace ssm
