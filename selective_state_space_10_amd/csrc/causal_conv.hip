@@ -5,6 +5,12 @@
 // lane owns a few adjacent channels and walks over a chunk of steps with the last
 // width - 1 inputs in registers; the rows before its chunk (and in the backward
 // those after it, whose outputs its inputs reach) are read again, mostly from L2.
+//
+// Measured, width 4, per call: forward 4 x 4096 x 5120 bf16 (336 MB) 70 us, 4.8 TB/s, a
+// large copy 5.1; 8 x 2048 x 2048 fp32 (268 MB) 46 us; backward 8 x 2048 x 2048 bf16
+// (201 MB) on packed documents 55 us with 5 for the second kernel, 3.7 TB/s: one round of
+// four waves per SIMD, whose start and end nothing overlaps; 4 x 4096 x 5120 (503 MB) 120 us.
+// One token of 2048 channels takes 2.2 us, latency.
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
 
@@ -104,11 +110,12 @@ __device__ __forceinline__ void load_window(const ConvArgs &a, int64_t b, int64_
 // Threads: (batch row, chunk, 4 channels), channels fastest; behind them one for
 // every 4 channels of the last states.
 template <typename T, int K>
-__global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int64_t nchunk, int steps, int64_t main_threads) {
-  const int64_t n4 = a.D / 4;
-  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, uint32_t nchunk, int steps, uint32_t main_threads) {
+  const uint32_t n4 = (uint32_t)(a.D / 4);
+  uint32_t i = blockIdx.x * 256 + threadIdx.x;  // (a launch has fewer than 2^32 threads)
   if (i < main_threads) {
-    const int64_t c = i % n4 * 4, bc = i / n4, b = bc / nchunk, t0 = bc % nchunk * steps;
+    const uint32_t bc = i / n4, b32 = bc / nchunk;
+    const int64_t c = (i - bc * n4) * 4, b = b32, t0 = (int64_t)(bc - b32 * nchunk) * steps;
     const int len = row_length(a.lengths, b, a.L);
     const int64_t t1 = t0 + steps < a.L ? t0 + steps : a.L;
     float w[K][4], bias[4], win[K][4];
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nrow, int
 
 template <typename T, int K>
 __global__ void __launch_bounds__(256) conv_update_kernel(ConvArgs a) {
-  const int64_t n4 = a.D / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t n4 = (uint32_t)(a.D / 4), i = blockIdx.x * 256 + threadIdx.x;
   if (i >= a.B * n4) return;
   const int64_t b = i / n4, c = i % n4 * 4;
   T *state = (T *)a.state + b * (K - 1) * a.D + c;
@@ -399,7 +406,7 @@ hipError_t fwd(const ConvArgs &a, hipStream_t s) {
   const int64_t nchunk = (a.L + kFwdSteps - 1) / kFwdSteps, n4 = a.D / 4, main = a.B * nchunk * n4;
   const int64_t threads = main + (a.state_final ? a.B * n4 : 0);
   return by_width(a.width, [&](auto k) {
-    hipLaunchKernelGGL((conv_fwd_kernel<T, decltype(k)::v>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, nchunk, kFwdSteps, main);
+    hipLaunchKernelGGL((conv_fwd_kernel<T, decltype(k)::v>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, (uint32_t)nchunk, kFwdSteps, (uint32_t)main);
     return hipGetLastError();
   });
 }

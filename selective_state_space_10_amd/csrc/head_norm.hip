@@ -9,6 +9,12 @@
 // weights are in registers, and so are the sums for the weights' gradients.  The
 // cosines and sines of a few tokens are formed once per workgroup, into LDS, while
 // the tokens' rows are on their way.
+//
+// Bound by HBM.  Measured, per call, bf16 (a large copy moves 5.1 TB/s): forward 1 x
+// 32768, 40 and 8 heads of 128 (806 MB) 170 us, 4.7 TB/s; backward 8 x 2048, 16 and 16
+// heads of 128 (403 MB) 87 us with 5 for the second kernel, 4.6 TB/s; fp32 5.0 to 5.2
+// TB/s.  Heads of 64 (8 x 2048, 32 and 4: 151 and 227 MB) 41 and 62 us, 3.7 TB/s: blocks of 8
+// heads form the angles five times.  The forward runs six waves per SIMD (183 us with five).
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
 
@@ -89,7 +95,7 @@ struct Angles {
 };
 
 template <typename T, int TPR, bool BWD, bool INTER>
-__global__ void __launch_bounds__(kThreads) head_norm_kernel(HeadNormArgs a, Plan plan, float *part) {
+__global__ void __launch_bounds__(kThreads, BWD ? 1 : 6) head_norm_kernel(HeadNormArgs a, Plan plan, float *part) {
   __shared__ alignas(16) float2 table[kMaxTable];
   const int half = a.rot / 2, HT = a.Hq + a.Hk;
   const int blk = (int)(blockIdx.x % plan.nblk), grp = threadIdx.x / TPR, p = threadIdx.x % TPR;

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(256) recurrence_clear_kernel(uint4 *p, int64_t
 // One token: 4 channels per lane.
 template <typename T, bool POWER>
 __global__ void __launch_bounds__(256) recurrence_update_kernel(RecurrenceUpdateArgs a) {
-  const int64_t n4 = a.D / 4, i4 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t n4 = (uint32_t)(a.D / 4), i4 = blockIdx.x * 256 + threadIdx.x;  // (fewer than 2^32 threads)
   if (i4 >= a.B * n4) return;
   const int64_t b = i4 / n4, c = i4 % n4 * 4;
   float x[4], g[4], i[4], z[4], h[4], l[4];
