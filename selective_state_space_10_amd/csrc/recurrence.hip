@@ -72,7 +72,9 @@ __device__ __forceinline__ float rate_of(float sharpness, float v) { return -sha
 // once and every output written once.
 //
 // The state before a chunk comes from the workgroups of the chunks before it, all of
-// which have started: a workgroup draws its chunk of the tile from a counter.  It
+// which have started: a workgroup draws its chunk of the tile from a counter.  (Loads
+// for the chunk that it most likely is, before the draw is back, lose more when it is another
+// than the draw's two microseconds: 3 x 1537 x 1000 fp32 backward 56 against 45 us.)  It
 // waits for words that hold a value and say that they do, each published by one
 // 64-bit store.  Every `group` chunks a state is published; in between a workgroup
 // composes the maps of the chunks before its own since then, always in the same
@@ -196,19 +198,12 @@ __device__ __forceinline__ int rows_of(int t0, int L) { return L - t0 < 0 ? 0 : 
 
 // The wave's steps of a tensor, the sequence's last step again for those behind it; a
 // step's stride and 16 of them stay below 2^29 bytes.
-// RUNNING: one offset in a scalar register that moves on, instead of all steps' at once:
-// they do not fit beside each other (forward 8 x 2048 x 2048 bf16: 69.8 -> 68.1 us; the
-// backward, which waits for them in other places, 32K x 5120 with z: 751 -> 784 us).
-template <bool RUNNING, typename T, int CPL>
+template <typename T, int CPL>
 __device__ __forceinline__ void load_steps(const View3 &v, int D, int64_t b, int t0, int L, uint32_t lane_bytes, Raw<T, CPL> (&r)[kSteps]) {
   const int step = (int)v.st * (int)sizeof(T), from = t0 < L ? t0 : L - 1, last = (rows_of(from, L) - 1) * step;
   const Buffer p = buffer_of(v.p, (b * v.sb + from * v.st) * (int64_t)sizeof(T), last + D * (int)sizeof(T));
 #pragma unroll
-  for (int j = 0, at = 0; j < kSteps; ++j) {
-    if constexpr (RUNNING) asm("" : "+s"(at));
-    r[j].load(p, lane_bytes, at);
-    at = RUNNING ? (at + step < last ? at + step : last) : ((j + 1) * step < last ? (j + 1) * step : last);
-  }
+  for (int j = 0; j < kSteps; ++j) r[j].load(p, lane_bytes, j * step < last ? j * step : last);
 }
 
 // Bit j: a document starts at the wave's step j, before the row's length.
@@ -233,31 +228,21 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
   const bool chain = n.chunks > 1;
   const int D = (int)a.D, L = (int)a.L;  // (both below 2^30: a launch's workgroups)
   if (chain && threadIdx.x == 0) drawn = (int)atomicAdd(n.counter + tile * 16, 1u);
-  // loads for the chunk that it will almost always be
-  int k = uniform(blockIdx.x / n.tiles);
-  int t0 = k * kRecurrenceChunk + w * kSteps;
-  Raw<T, CPL> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps];
-  auto load = [&] {
-    load_steps<true, T, CPL>(a.g, D, b, t0, L, lane_bytes, rg);
-    if (IG) load_steps<true, T, CPL>(a.ig, D, b, t0, L, lane_bytes, ri);
-    load_steps<true, T, CPL>(a.x, D, b, t0, L, lane_bytes, rx);
-    if (Z) load_steps<true, T, CPL>(a.z, D, b, t0, L, lane_bytes, rz);
-  };
   float rate2[CPL];
 #pragma unroll
-  for (int q = 0; q < CPL; ++q) rate2[q] = POWER ? a.decay[c + q] : 0.0f;
-  load();
-#pragma unroll
-  for (int q = 0; q < CPL; ++q) rate2[q] = POWER ? rate_of(a.sharpness, rate2[q]) : 0.0f;
+  for (int q = 0; q < CPL; ++q) rate2[q] = POWER ? rate_of(a.sharpness, a.decay[c + q]) : 0.0f;
+  int k = 0;
   if (chain) {
     __syncthreads();
-    const int mine = uniform(drawn);
-    if ((uint32_t)mine >= (uint32_t)n.chunks) return;  // (the workspace was written to meanwhile)
-    if (mine != k) {
-      k = mine, t0 = k * kRecurrenceChunk + w * kSteps;
-      load();
-    }
+    k = uniform(drawn);
+    if ((uint32_t)k >= (uint32_t)n.chunks) return;  // (the workspace was written to meanwhile)
   }
+  const int t0 = k * kRecurrenceChunk + w * kSteps;
+  Raw<T, CPL> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps];
+  load_steps<T, CPL>(a.g, D, b, t0, L, lane_bytes, rg);
+  if (IG) load_steps<T, CPL>(a.ig, D, b, t0, L, lane_bytes, ri);
+  load_steps<T, CPL>(a.x, D, b, t0, L, lane_bytes, rx);
+  if (Z) load_steps<T, CPL>(a.z, D, b, t0, L, lane_bytes, rz);
   const int len = MARKS ? uniform(row_length(a.lengths, b, L)) : L, nv = rows_of(t0, len);
   const uint32_t first = MARKS ? start_bits(a.starts, b, t0, L, len, lane) : 0;
 
@@ -369,28 +354,21 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
   const bool chain = n.chunks > 1;
   const int D = (int)a.D, L = (int)a.L;  // (both below 2^30: a launch's workgroups)
   if (chain && threadIdx.x == 0) drawn = (int)atomicAdd(n.counter + tile * 16, 1u);
-  int kr = uniform(blockIdx.x / n.tiles), k = n.chunks - 1 - kr;
-  int t0 = k * kRecurrenceChunk + w * kSteps;
-  Raw<T, 1> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps], rd[kSteps];
-  auto load = [&] {
-    load_steps<false, T, 1>(a.g, D, b, t0, L, lane_bytes, rg);
-    if (IG) load_steps<false, T, 1>(a.ig, D, b, t0, L, lane_bytes, ri);
-    load_steps<false, T, 1>(a.x, D, b, t0, L, lane_bytes, rx);
-    load_steps<false, T, 1>(a.dy, D, b, t0, L, lane_bytes, rd);
-    if (Z) load_steps<false, T, 1>(a.z, D, b, t0, L, lane_bytes, rz);
-  };
   const float param = POWER ? a.decay[c] : 0.0f;
-  load();
   const float rate2 = POWER ? rate_of(a.sharpness, param) : 0.0f;
+  int kr = 0;
   if (chain) {
     __syncthreads();
-    const int mine = uniform(drawn);
-    if ((uint32_t)mine >= (uint32_t)n.chunks) return;  // (the workspace was written to meanwhile)
-    if (mine != kr) {
-      kr = mine, k = n.chunks - 1 - kr, t0 = k * kRecurrenceChunk + w * kSteps;
-      load();
-    }
+    kr = uniform(drawn);
+    if ((uint32_t)kr >= (uint32_t)n.chunks) return;  // (the workspace was written to meanwhile)
   }
+  const int k = n.chunks - 1 - kr, t0 = k * kRecurrenceChunk + w * kSteps;
+  Raw<T, 1> rx[kSteps], rg[kSteps], ri[kSteps], rz[kSteps], rd[kSteps];
+  load_steps<T, 1>(a.g, D, b, t0, L, lane_bytes, rg);
+  if (IG) load_steps<T, 1>(a.ig, D, b, t0, L, lane_bytes, ri);
+  load_steps<T, 1>(a.x, D, b, t0, L, lane_bytes, rx);
+  load_steps<T, 1>(a.dy, D, b, t0, L, lane_bytes, rd);
+  if (Z) load_steps<T, 1>(a.z, D, b, t0, L, lane_bytes, rz);
   const int len = MARKS ? uniform(row_length(a.lengths, b, L)) : L, nv = rows_of(t0, len);
   const uint32_t first = MARKS ? start_bits(a.starts, b, t0, L, len, lane) : 0;
   float h = a.states[(b * n.chunks + k) * a.D + c];
