@@ -11,10 +11,11 @@
 // the tokens' rows are on their way.
 //
 // Bound by HBM.  Measured, per call, bf16 (a large copy moves 5.1 TB/s): forward 1 x
-// 32768, 40 and 8 heads of 128 (806 MB) 170 us, 4.7 TB/s; backward 8 x 2048, 16 and 16
+// 32768, 40 and 8 heads of 128 (806 MB) 161 us, 5.0 TB/s; backward 8 x 2048, 16 and 16
 // heads of 128 (403 MB) 87 us with 5 for the second kernel, 4.6 TB/s; fp32 5.0 to 5.2
 // TB/s.  Heads of 64 (8 x 2048, 32 and 4: 151 and 227 MB) 41 and 62 us, 3.7 TB/s: blocks of 8
-// heads form the angles five times.  The forward runs six waves per SIMD (183 us with five).
+// heads form the angles five times.  The forward runs six waves per SIMD (with five the
+// first takes 7% longer).
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
 

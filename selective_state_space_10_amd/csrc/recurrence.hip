@@ -4,16 +4,16 @@
 // Every input is read once and every output written once, and the bytes are the
 // floor; what keeps the kernels above it is that a workgroup loads, computes, waits for
 // the state before its chunk and stores in turn, and registers let only two workgroups
-// share a CU.  Vector units are active for half of the time (37 vector instructions
-// per element forward, 6 of them transcendental, and 63 with 7 backward), waves wait two fifths of it.
+// share a CU.  Vector units are active for half of the time (34 vector instructions
+// per element forward, 6 of them transcendental, and 59 with 7 backward), waves wait two fifths of it.
 // Measured, per call (a large copy moves 5.1 TB/s), bf16 in power form with an input gate:
-//   forward   8 x 2048 x 2048 (268 MB)            66 us, 4.0 TB/s (one lane per channel: 1782 us)
-//             4 x 4096 x 5120 (671 MB)           145 us, 4.6 TB/s
-//             1 x 32768 x 5120, z (1.68 GB)      377 us, 4.5 TB/s
-//             1 x 1048576 x 1024 (8.6 GB)        2.1 ms, 4.1 TB/s
-//   backward  8 x 2048 x 2048 (471 MB)           127 us, 3.7 TB/s (one lane per channel: 3298 us)
-//             1 x 32768 x 5120, z (3.0 GB)       740 us, 4.1 TB/s
-//   one token 256 x 5120, z (23 MB)              7.5 us
+//   forward   8 x 2048 x 2048 (268 MB)            67 us, 4.0 TB/s (one lane per channel: 1782 us)
+//             4 x 4096 x 5120 (671 MB)           143 us, 4.7 TB/s
+//             1 x 32768 x 5120, z (1.68 GB)      346 us, 4.8 TB/s
+//             1 x 1048576 x 1024 (8.6 GB)        2.04 ms, 4.2 TB/s
+//   backward  8 x 2048 x 2048 (471 MB)           126 us, 3.7 TB/s (one lane per channel: 3298 us)
+//             1 x 32768 x 5120, z (3.0 GB)       735 us, 4.1 TB/s
+//   one token 256 x 5120, z (24 MB)              6 us (7.5 us at the profiler's lower clocks)
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
 
