@@ -6,10 +6,10 @@
 // width - 1 inputs in registers; the rows before its chunk (and in the backward
 // those after it, whose outputs its inputs reach) are read again, mostly from L2.
 //
-// Measured, width 4, per call: forward 4 x 4096 x 5120 bf16 (336 MB) 70 us, 4.8 TB/s, a
+// Measured, width 4, per call: forward 4 x 4096 x 5120 bf16 (336 MB) 72 us, 4.7 TB/s, a
 // large copy 5.1; 8 x 2048 x 2048 fp32 (268 MB) 46 us; backward 8 x 2048 x 2048 bf16
-// (201 MB) on packed documents 55 us with 5 for the second kernel, 3.7 TB/s: one round of
-// four waves per SIMD, whose start and end nothing overlaps; 4 x 4096 x 5120 (503 MB) 120 us.
+// (201 MB) on packed documents 52 us with 5 for the second kernel, 3.9 TB/s: one round of
+// four waves per SIMD, whose start and end nothing overlaps; 4 x 4096 x 5120 (503 MB) 108 us.
 // One token of 2048 channels takes 2.2 us, latency.
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
@@ -31,13 +31,13 @@ struct Raw;
 template <>
 struct Raw<float> {
   float4 a;
-  __device__ __forceinline__ void load(const float *p) { a = ((const float4 *)p)[0]; }
+  __device__ __forceinline__ void load(const float *p) { a = load_once((const float4 *)p); }
   __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w; }
 };
 template <>
 struct Raw<bf16> {
   uint2 a;
-  __device__ __forceinline__ void load(const bf16 *p) { a = *(const uint2 *)p; }
+  __device__ __forceinline__ void load(const bf16 *p) { a = load_once((const uint2 *)p); }
   __device__ __forceinline__ void get(float (&v)[4]) const {
     const uint32_t w[2] = {a.x, a.y};
 #pragma unroll
@@ -178,7 +178,7 @@ struct Raw2<float> {
   uint32_t a, b;
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t step) {
     typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-    const u2 v = __builtin_bit_cast(u2, __builtin_amdgcn_raw_buffer_load_b64(p, lane, step, 0));
+    const u2 v = __builtin_bit_cast(u2, __builtin_amdgcn_raw_buffer_load_b64(p, lane, step, kStream));
     a = v.x, b = v.y;
   }
   __device__ __forceinline__ void get(float (&v)[2]) const { v[0] = __uint_as_float(a), v[1] = __uint_as_float(b); }
@@ -186,7 +186,7 @@ struct Raw2<float> {
 template <>
 struct Raw2<bf16> {
   uint32_t a;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t step) { a = __builtin_amdgcn_raw_buffer_load_b32(p, lane, step, 0); }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t p, uint32_t lane, uint32_t step) { a = __builtin_amdgcn_raw_buffer_load_b32(p, lane, step, kStream); }
   __device__ __forceinline__ void get(float (&v)[2]) const { v[0] = __uint_as_float(a << 16), v[1] = __uint_as_float(a & 0xffff0000u); }
 };
 __device__ __forceinline__ void load2(const float *p, float (&v)[2]) { v[0] = ((const float2 *)p)->x, v[1] = ((const float2 *)p)->y; }

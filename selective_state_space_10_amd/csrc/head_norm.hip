@@ -12,8 +12,8 @@
 //
 // Bound by HBM.  Measured, per call, bf16 (a large copy moves 5.1 TB/s): forward 1 x
 // 32768, 40 and 8 heads of 128 (806 MB) 161 us, 5.0 TB/s; backward 8 x 2048, 16 and 16
-// heads of 128 (403 MB) 87 us with 5 for the second kernel, 4.6 TB/s; fp32 5.0 to 5.2
-// TB/s.  Heads of 64 (8 x 2048, 32 and 4: 151 and 227 MB) 41 and 62 us, 3.7 TB/s: blocks of 8
+// heads of 128 (403 MB) 81 us with 5 for the second kernel, 5.0 TB/s; the same in fp32
+// 85 and 135 us (537 and 805 MB; outputs stay in the last-level cache).  Heads of 64 (8 x 2048, 32 and 4: 151 and 227 MB) 41 and 62 us, 3.7 TB/s: blocks of 8
 // heads form the angles five times.  The forward runs six waves per SIMD (with five the
 // first takes 7% longer).
 #include "mixer_device.hpp"
@@ -50,6 +50,14 @@ template <typename T>
 struct Pieces {
   typename Vec4<T>::raw lo, hi;
   __device__ __forceinline__ void load(const T *p, int o1, int o2) { lo = Vec4<T>::load(p, o1), hi = Vec4<T>::load(p, o2); }
+  template <bool ONCE>
+  __device__ __forceinline__ void load_row(const T *p, int o1, int o2) {
+    using R = typename Vec4<T>::raw;
+    if constexpr (ONCE)
+      lo = load_once((const R *)(p + o1)), hi = load_once((const R *)(p + o2));
+    else
+      load(p, o1, o2);
+  }
   template <bool INTER>
   __device__ __forceinline__ void get(float (&one)[4], float (&two)[4]) const {
     const float4 a = Vec4<T>::cvt(lo), b = Vec4<T>::cvt(hi);
@@ -118,6 +126,11 @@ __global__ void __launch_bounds__(kThreads, BWD ? 1 : 6) head_norm_kernel(HeadNo
     w.load(wp + hh * a.w_h, o1, o2);
     w.template get<INTER>(w1, w2);
   }
+  // Rows past the caches' order where a piece's loads are whole 128-byte lines, and not in
+  // the bf16 forward: 8 x 2048, 16 and 16 heads of 128, fp32 forward 104 -> 85 us, backward 161 ->
+  // 135, bf16 88 -> 81; heads of 64 fp32 backward 102 -> 86.  Elsewhere it loses: heads of 64 bf16 41 -> 45 and
+  // 63 -> 67, the forward of heads of 128 in bf16 of which 32 are rotated 53 -> 59, of 64 in fp32 60 -> 67.
+  constexpr bool ONCE = sizeof(T) == 4 ? TPR >= (BWD ? 8 : 16) : BWD && TPR >= 16;
   const float over_d = 1.0f / (float)a.d;
   const Angles angles(a);
   const int tt = plan.tsub * plan.rows;  // tokens of a chunk
@@ -132,8 +145,8 @@ __global__ void __launch_bounds__(kThreads, BWD ? 1 : 6) head_norm_kernel(HeadNo
     Pieces<T> next, next_g;
     const int mine_n = on ? n : 0;
     if (sub < mine_n) {
-      next.load(xp, o1, o2);
-      if (BWD) next_g.load(gp, o1, o2);
+      next.template load_row<ONCE>(xp, o1, o2);
+      if (BWD) next_g.template load_row<ONCE>(gp, o1, o2);
     }
     __syncthreads();  // the table's last readers are done
     angles.fill(a, b, t0, n, table);
@@ -146,10 +159,10 @@ __global__ void __launch_bounds__(kThreads, BWD ? 1 : 6) head_norm_kernel(HeadNo
       }
       if (tok + plan.tsub < mine_n) {
         xp += plan.tsub * src.st;
-        next.load(xp, o1, o2);
+        next.template load_row<ONCE>(xp, o1, o2);
         if (BWD) {
           gp += plan.tsub * up.st;
-          next_g.load(gp, o1, o2);
+          next_g.template load_row<ONCE>(gp, o1, o2);
         }
       }
       float rstd = 1.0f;

@@ -7,12 +7,12 @@
 // share a CU.  Vector units are active for half of the time (34 vector instructions
 // per element forward, 6 of them transcendental, and 59 with 7 backward), waves wait two fifths of it.
 // Measured, per call (a large copy moves 5.1 TB/s), bf16 in power form with an input gate:
-//   forward   8 x 2048 x 2048 (268 MB)            67 us, 4.0 TB/s (one lane per channel: 1782 us)
-//             4 x 4096 x 5120 (671 MB)           143 us, 4.7 TB/s
-//             1 x 32768 x 5120, z (1.68 GB)      346 us, 4.8 TB/s
-//             1 x 1048576 x 1024 (8.6 GB)        2.04 ms, 4.2 TB/s
-//   backward  8 x 2048 x 2048 (471 MB)           126 us, 3.7 TB/s (one lane per channel: 3298 us)
-//             1 x 32768 x 5120, z (3.0 GB)       735 us, 4.1 TB/s
+//   forward   8 x 2048 x 2048 (268 MB)            62 us, 4.3 TB/s (one lane per channel: 1782 us)
+//             4 x 4096 x 5120 (671 MB)           134 us, 5.0 TB/s
+//             1 x 32768 x 5120, z (1.68 GB)      334 us, 5.0 TB/s
+//             1 x 1048576 x 1024 (8.6 GB)        2.00 ms, 4.3 TB/s
+//   backward  8 x 2048 x 2048 (471 MB)           124 us, 3.8 TB/s (one lane per channel: 3298 us)
+//             1 x 32768 x 5120, z (3.0 GB)       698 us, 4.3 TB/s
 //   one token 256 x 5120, z (24 MB)              6 us (7.5 us at the profiler's lower clocks)
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
@@ -168,7 +168,7 @@ struct Raw;
 template <>
 struct Raw<float, 1> {
   uint32_t v;
-  __device__ __forceinline__ void load(Buffer p, uint32_t lane, uint32_t step) { v = __builtin_amdgcn_raw_buffer_load_b32(p, lane, step, 0); }
+  __device__ __forceinline__ void load(Buffer p, uint32_t lane, uint32_t step) { v = __builtin_amdgcn_raw_buffer_load_b32(p, lane, step, kStream); }
   __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = __uint_as_float(v); }
   static __device__ __forceinline__ void put(Buffer p, uint32_t lane, uint32_t step, const float (&o)[1]) {
     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o[0]), p, lane, step, 0);
@@ -177,7 +177,7 @@ struct Raw<float, 1> {
 template <>
 struct Raw<bf16, 1> {
   uint16_t v;
-  __device__ __forceinline__ void load(Buffer p, uint32_t lane, uint32_t step) { v = __builtin_amdgcn_raw_buffer_load_b16(p, lane, step, 0); }
+  __device__ __forceinline__ void load(Buffer p, uint32_t lane, uint32_t step) { v = __builtin_amdgcn_raw_buffer_load_b16(p, lane, step, kStream); }
   __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = __uint_as_float((uint32_t)v << 16); }
   static __device__ __forceinline__ void put(Buffer p, uint32_t lane, uint32_t step, const float (&o)[1]) {
     __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(o[0], o[0]), p, lane, step, 0);
@@ -186,7 +186,7 @@ struct Raw<bf16, 1> {
 template <>
 struct Raw<bf16, 2> {
   uint32_t v;
-  __device__ __forceinline__ void load(Buffer p, uint32_t lane, uint32_t step) { v = __builtin_amdgcn_raw_buffer_load_b32(p, lane, step, 0); }
+  __device__ __forceinline__ void load(Buffer p, uint32_t lane, uint32_t step) { v = __builtin_amdgcn_raw_buffer_load_b32(p, lane, step, kStream); }
   __device__ __forceinline__ void get(float (&o)[2]) const { o[0] = __uint_as_float(v << 16), o[1] = __uint_as_float(v & 0xffff0000u); }
   static __device__ __forceinline__ void put(Buffer p, uint32_t lane, uint32_t step, const float (&o)[2]) {
     __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(o[0], o[1]), p, lane, step, 0);
