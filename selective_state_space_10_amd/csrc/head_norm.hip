@@ -12,9 +12,9 @@
 //
 // Bound by HBM.  Measured, per call, bf16 (a large copy moves 5.1 TB/s): forward 1 x
 // 32768, 40 and 8 heads of 128 (806 MB) 161 us, 5.0 TB/s; backward 8 x 2048, 16 and 16
-// heads of 128 (403 MB) 81 us with 5 for the second kernel, 5.0 TB/s; the same in fp32
-// 85 and 135 us (537 and 805 MB; outputs stay in the last-level cache).  Heads of 64 (8 x 2048, 32 and 4: 151 and 227 MB) 41 and 62 us, 3.7 TB/s: blocks of 8
-// heads form the angles five times.  The forward runs six waves per SIMD (with five the
+// heads of 128 (403 MB) 80 us with 5 for the second kernel, 5.0 TB/s; the same in fp32 85 and
+// 130 us (537 and 805 MB; outputs stay in the last-level cache).  Heads of 64 (8 x 2048, 32
+// and 4: 151 and 227 MB) 39 and 56 us, 3.9 and 4.0 TB/s: blocks of 8 heads form the angles five times.  The forward runs six waves per SIMD (with five the
 // first takes 7% longer).
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
@@ -25,7 +25,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTable = 2048;  // angles in LDS
-constexpr int kMaxRows = 8;      // rows of a group under way together
+// Rows of a group between two fillings of the table: few start sooner and leave more workgroups to
+// even out (8 x 2048, 32 and 4 heads of 64 bf16: forward 41 -> 39 us with 4 for 8, backward 62 -> 56; 16 and 16
+// of 128 fp32 backward 135 -> 130, interleaved forward 104 -> 96; 32K context backward 244 -> 236), but one
+// token at a time in the bf16 forward waits for each filling (40 and 8 heads of 128 176 against 172, 16 and
+// 16 interleaved 56 against 52; two rows lose 2 to 20% nearly everywhere).
+constexpr int max_rows(bool bwd, int es, int tpr) { return !bwd && es == 2 && tpr >= 16 ? 8 : 4; }
 
 struct Plan {
   int tpr, nblk, hb, tsub, rows;  // lanes per head, blocks of heads, heads per block, tokens at once, rows per group of a chunk of tokens
@@ -264,7 +269,8 @@ int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 int least_blocks(int HT, int tpr) { return (HT + kThreads / tpr - 1) / (kThreads / tpr); }
 constexpr int kMoreBlocks = 8;
 
-Plan plan_of(int64_t B, int64_t L, int HT, int d, int rot, int64_t workgroups) {
+Plan plan_of(int64_t B, int64_t L, int HT, int d, int rot, bool bwd, int es) {
+  const int64_t workgroups = bwd ? kBwdWorkgroups : kFwdWorkgroups;
   Plan p;
   p.tpr = lanes_of(d);
   // Blocks of heads: few, since each forms the angles of its tokens, and so that few groups
@@ -278,7 +284,7 @@ Plan plan_of(int64_t B, int64_t L, int HT, int d, int rot, int64_t workgroups) {
     const double cost = 120.0 * nblk / tsub + 50.0 * nblk * (rot / 2) / kThreads;
     if (least == 0.0 || cost < least) least = cost, p.nblk = (HT + hb - 1) / hb, p.hb = hb, p.tsub = tsub;
   }
-  p.rows = kMaxRows;
+  p.rows = max_rows(bwd, es, p.tpr);
   while (p.rows > 1 && (p.tsub * p.rows * (rot / 2) > kMaxTable)) p.rows /= 2;
   const int64_t tt = p.tsub * p.rows;
   p.nchunk = B * ((L + tt - 1) / tt);
@@ -309,7 +315,7 @@ void launch_tpr(const HeadNormArgs &a, const Plan &p, hipStream_t s) {
 template <typename T, bool BWD>
 hipError_t launch(const HeadNormArgs &given, hipStream_t s) {
   const HeadNormArgs a = merged(given, BWD);
-  const Plan p = plan_of(a.B, a.L, a.Hq + a.Hk, a.d, a.rot, BWD ? kBwdWorkgroups : kFwdWorkgroups);
+  const Plan p = plan_of(a.B, a.L, a.Hq + a.Hk, a.d, a.rot, BWD, sizeof(T));
   const float *part = (const float *)a.workspace;
   if (p.tpr == 4)
     launch_tpr<T, 4, BWD>(a, p, s);
