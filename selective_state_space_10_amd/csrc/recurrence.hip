@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
     float dx[1] = {ws * ii[j]}, di[1] = {dx[0] * (xs[j] - u)}, dg[1];
     if constexpr (POWER) {
       // with log2 a for log a: log 2 comes in with the sigmoid's slope and at the end
-      const float f = start ? 0.0f : flow * keep[j] * fmaf(-u * da[j], s > 0.0f ? fast_rcp(s) : 0.0f, h);
+      // (a step behind the row's length has no part in ddecay, not even 0 times a state that is not finite)
+      const float f = start || j >= nv ? 0.0f : flow * keep[j] * fmaf(-u * da[j], s > 0.0f ? fast_rcp(s) : 0.0f, h);
       sum += f;
       dg[0] = f * fmaf(-keep[j], over, kLn2);
     } else {

@@ -221,6 +221,28 @@ def test_nothing_crosses_a_start(ssm, form, bad):
     assert not d["dstate0"][:2].any()
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("L", [20, 150])
+@pytest.mark.parametrize("form", FORMS)
+def test_an_unused_row_is_not_in_ddecay(ssm, form, L, bad):
+    """A row of length 0 whose state, and what comes back for it, are not finite: they pass through, and the
+    gradients of all other rows and of the parameter that the rows share stay those without it."""
+    p = ref.recurrence_inputs(3, L, 72, form=form)
+    p["lengths"] = torch.tensor([L, 0, 7], dtype=torch.int32)
+    clean = {k: None if v is None else v.clone() for k, v in p.items()}
+    p["state0"][1] = p["dfinal"][1] = bad
+    g = ref.on_gpu(p)
+    y, final, states = forward(ssm, g)
+    d = backward(ssm, g, states)
+    ry, _, _, rg = ref.recurrence(clean)
+    assert ref.error(y, ry) <= tol(L) and torch.equal(final[1].cpu().isnan(), p["state0"][1].isnan())
+    for n in ("dx", "ddecay_gate", "dinput_gate", "dz", "ddecay"):
+        if d[n] is not None:
+            assert ref.error(d[n], rg[n]) <= 4 * tol(L), n
+    keep = [0, 2]
+    assert ref.error(d["dstate0"][keep], rg["dstate0"][keep]) <= 3 * tol(L)
+
+
 def test_a_bad_value_reaches_later_steps_of_its_document_alone(ssm):
     p = ref.recurrence_inputs(1, 400, 16)
     p["x"][0, 130, 5] = math.nan
