@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int nrow, int
             if (!EDGE || k <= age)
 #pragma unroll
               for (int j = 0; j < 2; ++j) d[k][j] = fmaf(w[K - 1 - k][j], g[j], d[k][j]);
-          if (m < own)
+          // (a step behind the row's length has no part in the sums, not even 0 times an unused state that is not finite)
+          if (m < own && !(EDGE && t0 + m >= len))
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll

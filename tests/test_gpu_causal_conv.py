@@ -158,6 +158,27 @@ def test_nothing_crosses_a_start(ssm, bad):
     assert ref.error(d[0][keep], rg["dx"][0][keep]) <= TOL
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("K", [2, 4])
+@pytest.mark.parametrize("L", [2, 70])
+def test_an_unused_row_is_not_in_the_weights_gradients(ssm, K, L, bad):
+    """A row of length 0 whose state, and what comes back for it, are not finite: they pass through, and the
+    gradients of all other rows and of the weights stay those without it."""
+    p = ref.conv_inputs(3, L, 24, K)
+    p["lengths"] = torch.tensor([L, 0, 1], dtype=torch.int32)
+    clean = {k: None if v is None else v.clone() for k, v in p.items()}
+    p["state0"][1] = p["dfinal"][1] = bad
+    g = ref.on_gpu(p)
+    y, final = forward(ssm, g)
+    d = backward(ssm, g)
+    ry, rf, rg = ref.conv(clean)
+    keep = [0, 2]
+    assert ref.error(y, ry) <= TOL and torch.equal(final[keep].cpu().double(), rf[keep]) and torch.equal(final[1].cpu().isnan(), p["state0"][1].isnan())
+    for n in ("dx", "dweight", "dbias"):
+        assert ref.error(d[n], rg[n]) <= (TOL if n == "dx" else SUMS), n
+    assert ref.error(d["dstate0"][keep], rg["dstate0"][keep]) <= TOL
+
+
 def test_strides(ssm):
     p = ref.conv_inputs(3, 70, 24, 4, dtype=BF16)
     g = ref.on_gpu(p)
