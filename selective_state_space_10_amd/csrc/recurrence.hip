@@ -26,7 +26,7 @@ namespace {
 // (1/8)^5 / 720 < 2^-24 relative, beyond it 1 - a^2 loses 2^-24 / (1 - e^-1/8) of
 // itself, half of that in s.  Logistic form: a = r, s = 1 - r.
 struct Gate {
-  float a, s, r, o, la2;  // o = 1 - r
+  float a, s, r, o;  // o = 1 - r
 };
 __device__ __forceinline__ float scale_of(float la2, float a) {
   const float v = 2.0f * kLn2 * la2;
@@ -38,11 +38,10 @@ __device__ __forceinline__ Gate gate_of(float g, float rate2) {
   Gate q;
   sigmoid_both(g, q.r, q.o);
   if constexpr (POWER) {
-    q.la2 = rate2 * q.r;
-    q.a = fast_exp2(q.la2);
-    q.s = scale_of(q.la2, q.a);
+    const float la2 = rate2 * q.r;
+    q.a = fast_exp2(la2);
+    q.s = scale_of(la2, q.a);
   } else {
-    q.la2 = 0.0f;
     q.a = q.r;
     q.s = q.o;
   }
@@ -334,8 +333,8 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
 // Backward: the chunks in reverse, w_t = e_t + a_{t+1} w_{t+1}.  What flows from step t
 // to t - 1 is q = a_t w_t, and a stretch of steps is q -> P q + Q with the P of the
 // forward map.  The states inside a chunk are formed again from the one before it, its
-// maps and those of the adjoint in one exchange.  For a step's gradients a lane keeps
-// log2 a (power form; its sigmoid is log2 a over rate2) or 1 - a, and s in LDS:
+// maps and those of the adjoint in one exchange.  For a step's gradients a lane keeps the
+// gate's sigmoid and its complement in one register (power form) or 1 - a, and s in LDS:
 //   log a da/d(log a) w (h_{t-1} - u a / s) = dLoss / d(log a) log a,  u = sigmoid(i) x.
 template <typename T, bool POWER, bool IG, bool Z, bool MARKS>
 __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(RecurrenceArgs a, Chain n, float *part) {
@@ -373,14 +372,14 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
   const uint32_t first = MARKS ? start_bits(a.starts, b, t0, L, len, lane) : 0;
   float h = a.states[(b * n.chunks + k) * a.D + c];
 
-  // keep: log2 a or 1 - a; steps behind the end: a = 1, nothing comes in
+  // keep: the folded gate or 1 - a; steps behind the end: a = 1, nothing comes in
   float da[kSteps], keep[kSteps], in[kSteps], ii[kSteps], xs[kSteps], es[kSteps];
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
     float g[1], v[1];
     rg[j].get(g);
     const Gate t = gate_of<POWER>(g[0], rate2);
-    da[j] = t.a, keep[j] = POWER ? t.la2 : t.o;
+    da[j] = t.a, keep[j] = POWER ? fold_gate(g[0], t.r, t.o) : t.o;
     rx[j].get(v), xs[j] = v[0];
     rd[j].get(v), es[j] = v[0];
     if (Z) {
@@ -401,7 +400,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
   if (nv < kSteps)
 #pragma unroll
     for (int j = 0; j < kSteps; ++j)
-      if (j >= nv) da[j] = 1.0f, keep[j] = in[j] = ii[j] = xs[j] = es[j] = 0.0f;
+      if (j >= nv) da[j] = 1.0f, keep[j] = POWER ? -0.0f : 0.0f, in[j] = ii[j] = xs[j] = es[j] = 0.0f;
   Map m = {1.0f, 0.0f};
   float q = 0.0f;
 #pragma unroll
@@ -447,8 +446,6 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
   const Buffer bx = buffer_of(a.dx, row0, rows_bytes), bg = buffer_of(a.dg, row0, rows_bytes), bi = buffer_of(a.dig, row0, rows_bytes);
   const Buffer bz = buffer_of(a.dz, row0, rows_bytes);
   const uint32_t out = on ? lane_bytes : kNoLane;
-  // (a rate whose reciprocal leaves fp32 has no gradient either)
-  const float over = POWER && rate2 < -0x1p-120f ? kLn2 * fast_rcp(rate2) : 0.0f;
   float sum = 0.0f;
 #pragma unroll
   for (int j = kSteps - 1; j >= 0; --j) {
@@ -461,9 +458,11 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
     if constexpr (POWER) {
       // with log2 a for log a: log 2 comes in with the sigmoid's slope and at the end
       // (a step behind the row's length has no part in ddecay, not even 0 times a state that is not finite)
-      const float f = start || j >= nv ? 0.0f : flow * keep[j] * fmaf(-u * da[j], s > 0.0f ? fast_rcp(s) : 0.0f, h);
+      float r, o;
+      unfold_gate(keep[j], r, o);
+      const float f = start || (MARKS && j >= nv) ? 0.0f : flow * (rate2 * r) * fmaf(-u * da[j], s > 0.0f ? fast_rcp(s) : 0.0f, h);
       sum += f;
-      dg[0] = f * fmaf(-keep[j], over, kLn2);
+      dg[0] = f * (kLn2 * o);
     } else {
       dg[0] = start ? 0.0f : flow * s * (h - u);
     }

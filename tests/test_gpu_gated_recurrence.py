@@ -148,6 +148,47 @@ def test_extreme_decays(ssm, decay):
     compare(ssm, p, ref.on_gpu(p))
 
 
+def gates(D, dtype, form, seed=0):
+    """One step whose factors do not cancel in any gradient: state and adjoints of one sign, inputs of the other."""
+    p = ref.recurrence_inputs(3, 1, D, form=form, z=False, dtype=dtype, seed=seed)
+    for n in ("x", "dy", "dfinal"):
+        p[n] = 0.5 + p[n].abs()
+    p["state0"] = -0.5 - p["state0"].abs()
+    p["decay_gate"], p["input_gate"] = (p[n].clamp(-1, 1) for n in ("decay_gate", "input_gate"))
+    return p
+
+
+def every_value(ssm, p, name):
+    """Each value of a gradient against its own size.  In units of 2^-24 of it: a gate's smaller side 21 (the exponent
+    v log2(e) up to 29, rounded to half of 2^-19 and with log2(e) itself off by 1.3e-8, makes 16, exponential 2,
+    reciprocal 2, product 1) and half of that again in s; the decay's rate 5, s 10, a 3, sigmoid(i) x 5, reciprocal 2,
+    the adjoint 3, products 6: 65, taken as 80."""
+    g = ref.on_gpu(p)
+    d = backward(ssm, g, forward(ssm, g)[2])[name].cpu().double()
+    want = ref.recurrence(p)[3]["d" + name[1:]]
+    u = torch.finfo(p["x"].dtype).eps / 2
+    off = float(((d - want).abs() / want.abs()).max())
+    assert off <= u + 80 * 2.0 ** -24, off  # (no reference value is 0: off would be NaN or infinite)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradient_of_far_decay_gates(ssm, form, dtype):
+    """Open and closed gates keep the digits of their gradients, which are e^-|v| of the others'."""
+    p = gates(136, dtype, form)
+    p["decay_gate"][:] = torch.linspace(-20, 20, 136)
+    every_value(ssm, p, "ddecay_gate")
+
+
+def test_gradient_of_gates_of_the_smallest_rates(ssm):
+    """softplus(decay) close to the end of fp32's range: 1 - sigmoid stays in the gate's gradient.  (The gate's
+    exponent is below 16, and log a, about 2^-120, has four bits to spare above the range's end.)"""
+    p = gates(136, F32, "power")
+    p["decay"][:] = -86.0
+    p["decay_gate"][:] = torch.linspace(-1, 8, 136)
+    every_value(ssm, p, "ddecay_gate")
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_tokens_are_the_sequence(ssm, dtype):
     for form in FORMS:
