@@ -392,7 +392,8 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
     ii[j] = 1.0f;
     if (IG) ri[j].get(v), ii[j] = sigmoid_f(v[0]);
     float s = t.s;
-    if (MARKS && (first >> j & 1)) da[j] = 0.0f, s = 1.0f;
+    // (at a start the gate is not used, whatever it holds)
+    if (MARKS && (first >> j & 1)) da[j] = 0.0f, s = 1.0f, keep[j] = POWER ? -0.0f : 0.0f;
     if (POWER) scale[w][j][lane] = s;
     in[j] = s * (ii[j] * xs[j]);
     if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (more steps at once do not fit registers)

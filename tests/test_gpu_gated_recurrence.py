@@ -263,6 +263,17 @@ def test_nothing_crosses_a_start(ssm, form, bad):
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("form", FORMS)
+def test_the_decay_gate_of_a_start_is_not_used(ssm, form, bad):
+    p = ref.recurrence_inputs(2, 150, 72, form=form)
+    p["starts"] = torch.zeros(2, 150, dtype=torch.bool)
+    p["starts"][:, [0, 17, 128, 149]] = True
+    clean = {k: None if v is None else v.clone() for k, v in p.items()}
+    p["decay_gate"][p["starts"]] = bad
+    compare(ssm, clean, ref.on_gpu(p))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("L", [20, 150])
 @pytest.mark.parametrize("form", FORMS)
 def test_an_unused_row_is_not_in_ddecay(ssm, form, L, bad):
