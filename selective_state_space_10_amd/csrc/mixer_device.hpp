@@ -85,15 +85,19 @@ __device__ __forceinline__ void sigmoid_both(float v, float &one, float &other) 
   other = v < -64.0f ? 1.0f : e * one;  // (e is infinite from about -88 on)
 }
 
-// sigmoid(v) and its complement in one register: the smaller of the two, with the sign
-// bit set (on zero too) if that is the sigmoid.  The larger is 1 minus it to half a
-// step; the smaller formed as 1 minus the larger has lost 3% of itself at v = 12 and all at 17.
-__device__ __forceinline__ float fold_gate(float v, float one, float other) { return v >= 0.0f ? other : -one; }
-__device__ __forceinline__ void unfold_gate(float k, float &one, float &other) {
-  const float less = fabsf(k), more = 1.0f - less;
-  const bool closed = (int)__float_as_uint(k) < 0;
-  one = closed ? less : more;
-  other = closed ? more : less;
+// sigmoid(v), and in one register what its derivative needs too: a sigmoid up to 1/2
+// itself, a larger one as minus its complement (so that the other side is the fraction
+// that is left to the next whole number; -2^-126 instead of nothing at all keeps the sign).  The
+// complement formed as 1 minus the sigmoid has lost 3% of itself at v = 12 and all at 17.
+__device__ __forceinline__ float sigmoid_folded(float v, float &folded) {
+  const float e = fast_exp2(-v * kLog2e), one = fast_rcp(1.0f + e);
+  folded = v >= 0.0f ? fmaf(-e, one, -0x1p-126f) : one;
+  return one;
+}
+// the sigmoid and its derivative, sigmoid times complement
+__device__ __forceinline__ void unfold(float folded, float &one, float &slope) {
+  one = __builtin_amdgcn_fractf(folded);
+  slope = fmaf(-fabsf(folded), fabsf(folded), fabsf(folded));
 }
 
 // z sigmoid(z) and its derivative

@@ -25,8 +25,9 @@ namespace {
 // by the series of -expm1(2 log a) where a is near 1: four terms up to 1/8 leave
 // (1/8)^5 / 720 < 2^-24 relative, beyond it 1 - a^2 loses 2^-24 / (1 - e^-1/8) of
 // itself, half of that in s.  Logistic form: a = r, s = 1 - r.
+// keep: of the gate, what its gradient needs: the folded sigmoid, or 1 - r.
 struct Gate {
-  float a, s, r, o;  // o = 1 - r
+  float a, s, keep;
 };
 __device__ __forceinline__ float scale_of(float la2, float a) {
   const float v = 2.0f * kLn2 * la2;
@@ -36,14 +37,13 @@ __device__ __forceinline__ float scale_of(float la2, float a) {
 template <bool POWER>
 __device__ __forceinline__ Gate gate_of(float g, float rate2) {
   Gate q;
-  sigmoid_both(g, q.r, q.o);
   if constexpr (POWER) {
-    const float la2 = rate2 * q.r;
+    const float la2 = rate2 * sigmoid_folded(g, q.keep);
     q.a = fast_exp2(la2);
     q.s = scale_of(la2, q.a);
   } else {
-    q.a = q.r;
-    q.s = q.o;
+    sigmoid_both(g, q.a, q.s);
+    q.keep = q.s;
   }
   return q;
 }
@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(64 * kWaves) recurrence_fwd_kernel(RecurrenceA
 // Backward: the chunks in reverse, w_t = e_t + a_{t+1} w_{t+1}.  What flows from step t
 // to t - 1 is q = a_t w_t, and a stretch of steps is q -> P q + Q with the P of the
 // forward map.  The states inside a chunk are formed again from the one before it, its
-// maps and those of the adjoint in one exchange.  For a step's gradients a lane keeps the
-// gate's sigmoid and its complement in one register (power form) or 1 - a, and s in LDS:
+// maps and those of the adjoint in one exchange.  For a step's gradients a lane keeps each
+// gate's sigmoid and complement in one register (of the logistic form's decay 1 - a), and s in LDS:
 //   log a da/d(log a) w (h_{t-1} - u a / s) = dLoss / d(log a) log a,  u = sigmoid(i) x.
 template <typename T, bool POWER, bool IG, bool Z, bool MARKS>
 __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(RecurrenceArgs a, Chain n, float *part) {
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
   const int D = (int)a.D, L = (int)a.L;  // (both below 2^30: a launch's workgroups)
   if (chain && threadIdx.x == 0) drawn = (int)atomicAdd(n.counter + tile * 16, 1u);
   const float param = POWER ? a.decay[c] : 0.0f;
-  const float rate2 = POWER ? rate_of(a.sharpness, param) : 0.0f;
+  const float rate2 = POWER ? rate_of(a.sharpness, param) : 0.0f, rate = kLn2 * rate2;
   int kr = 0;
   if (chain) {
     __syncthreads();
@@ -372,14 +372,14 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
   const uint32_t first = MARKS ? start_bits(a.starts, b, t0, L, len, lane) : 0;
   float h = a.states[(b * n.chunks + k) * a.D + c];
 
-  // keep: the folded gate or 1 - a; steps behind the end: a = 1, nothing comes in
+  // keep: the folded gate or 1 - a; ii: the folded input gate; steps behind the end: a = 1, nothing comes in
   float da[kSteps], keep[kSteps], in[kSteps], ii[kSteps], xs[kSteps], es[kSteps];
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
     float g[1], v[1];
     rg[j].get(g);
     const Gate t = gate_of<POWER>(g[0], rate2);
-    da[j] = t.a, keep[j] = POWER ? fold_gate(g[0], t.r, t.o) : t.o;
+    da[j] = t.a, keep[j] = t.keep;
     rx[j].get(v), xs[j] = v[0];
     rd[j].get(v), es[j] = v[0];
     if (Z) {
@@ -389,19 +389,20 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
       gate_grad[w][j][lane] = es[j] * df;
       es[j] *= f;
     }
-    ii[j] = 1.0f;
-    if (IG) ri[j].get(v), ii[j] = sigmoid_f(v[0]);
+    float i = 1.0f;
+    ii[j] = 0.0f;
+    if (IG) ri[j].get(v), i = sigmoid_folded(v[0], ii[j]);
     float s = t.s;
     // (at a start the gate is not used, whatever it holds)
-    if (MARKS && (first >> j & 1)) da[j] = 0.0f, s = 1.0f, keep[j] = POWER ? -0.0f : 0.0f;
+    if (MARKS && (first >> j & 1)) da[j] = 0.0f, s = 1.0f, keep[j] = 0.0f;
     if (POWER) scale[w][j][lane] = s;
-    in[j] = s * (ii[j] * xs[j]);
+    in[j] = s * (i * xs[j]);
     if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (more steps at once do not fit registers)
   }
   if (nv < kSteps)
 #pragma unroll
     for (int j = 0; j < kSteps; ++j)
-      if (j >= nv) da[j] = 1.0f, keep[j] = POWER ? -0.0f : 0.0f, in[j] = ii[j] = xs[j] = es[j] = 0.0f;
+      if (j >= nv) da[j] = 1.0f, keep[j] = in[j] = ii[j] = xs[j] = es[j] = 0.0f;
   Map m = {1.0f, 0.0f};
   float q = 0.0f;
 #pragma unroll
@@ -453,17 +454,18 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
     const bool start = MARKS && (first >> j & 1);
     float dz[1] = {Z ? gate_grad[w][j][lane] * h : 0.0f};
     h = in[j];
-    const float wt = es[j] + q, flow = wt * da[j], u = ii[j] * xs[j];
+    float i = 1.0f, di_v = 0.0f;
+    if (IG) unfold(ii[j], i, di_v);
+    const float wt = es[j] + q, flow = wt * da[j], u = i * xs[j];
     const float s = POWER ? scale[w][j][lane] : start ? 1.0f : keep[j], ws = wt * s;
-    float dx[1] = {ws * ii[j]}, di[1] = {dx[0] * (xs[j] - u)}, dg[1];
+    float dx[1] = {ws * i}, di[1] = {ws * (xs[j] * di_v)}, dg[1];
     if constexpr (POWER) {
-      // with log2 a for log a: log 2 comes in with the sigmoid's slope and at the end
       // (a step behind the row's length has no part in ddecay, not even 0 times a state that is not finite)
-      float r, o;
-      unfold_gate(keep[j], r, o);
-      const float f = start || (MARKS && j >= nv) ? 0.0f : flow * (rate2 * r) * fmaf(-u * da[j], s > 0.0f ? fast_rcp(s) : 0.0f, h);
-      sum += f;
-      dg[0] = f * (kLn2 * o);
+      float r, dr;
+      unfold(keep[j], r, dr);
+      const float f = start || (MARKS && j >= nv) ? 0.0f : flow * rate * fmaf(-u * da[j], s > 0.0f ? fast_rcp(s) : 0.0f, h);
+      sum = fmaf(f, r, sum);
+      dg[0] = f * dr;
     } else {
       dg[0] = start ? 0.0f : flow * s * (h - u);
     }
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) recurrence_bwd_kernel(Recurren
       sum = 0.0f;
       for (int i = 0; i < kWaves; ++i) sum += back[i][lane];
       // sigmoid / softplus goes to 1 where both vanish
-      part[(b * n.chunks + k) * a.D + c] = kLn2 * sum * (param < -40.0f ? 1.0f : sigmoid_f(param) / softplus_full(param));
+      part[(b * n.chunks + k) * a.D + c] = sum * (param < -40.0f ? 1.0f : sigmoid_f(param) / softplus_full(param));
     }
   }
 }

@@ -180,6 +180,14 @@ def test_gradient_of_far_decay_gates(ssm, form, dtype):
     every_value(ssm, p, "ddecay_gate")
 
 
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradient_of_far_input_gates(ssm, form, dtype):
+    p = gates(136, dtype, form)
+    p["input_gate"][:] = torch.linspace(-20, 20, 136)
+    every_value(ssm, p, "dinput_gate")
+
+
 def test_gradient_of_gates_of_the_smallest_rates(ssm):
     """softplus(decay) close to the end of fp32's range: 1 - sigmoid stays in the gate's gradient.  (The gate's
     exponent is below 16, and log a, about 2^-120, has four bits to spare above the range's end.)"""
