@@ -11,7 +11,7 @@ from torch.autograd.function import once_differentiable
 from torch.autograd.graph import increment_version
 
 from . import _lib
-from .ops import _IO, _io_code, _need, _ptr, _stream
+from .ops import _IO, _gradient, _io_code, _need, _ptr, _stream
 
 _F32 = torch.float32
 _View4 = _lib.View4
@@ -354,9 +354,8 @@ class DecayAttentionFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, do, dfinal):
         q, k, v, log_decay, state0 = ctx.saved_tensors
-        do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None else do.contiguous()
-        g = decay_attn_bwd(q, k, v, log_decay, do, ctx.scale, state0,
-                           None if dfinal is None else dfinal.contiguous(),
+        do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None else _gradient(do)
+        g = decay_attn_bwd(q, k, v, log_decay, do, ctx.scale, state0, _gradient(dfinal),
                            want_dlog_decay=ctx.needs_input_grad[3],
                            want_dstate0=ctx.needs_input_grad[5])
         return g["dq"], g["dk"], g["dv"], g["dlog_decay"], None, g["dstate0"]
@@ -383,8 +382,8 @@ class ResidualNormFn(torch.autograd.Function):
     def backward(ctx, dy, dh):
         x, h, rstd, weight, scale = ctx.saved_tensors
         shape, dtype, dev = ctx.x_like
-        dy = torch.zeros(shape, dtype=dtype, device=dev) if dy is None else dy.contiguous()
-        g = residual_norm_bwd(dy, None if dh is None else dh.contiguous(), h, rstd, weight, x, scale)
+        dy = torch.zeros(shape, dtype=dtype, device=dev) if dy is None else _gradient(dy)
+        g = residual_norm_bwd(dy, _gradient(dh), h, rstd, weight, x, scale)
         return g["dx"], g["dresidual"], g["dweight"], g["dscale"], None
 
 
@@ -407,7 +406,7 @@ class GatedNormFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, z, weight, rstd = ctx.saved_tensors
-        g = gated_norm_bwd(dy.contiguous(), x, z, weight, rstd, ctx.group, ctx.gate_first)
+        g = gated_norm_bwd(_gradient(dy), x, z, weight, rstd, ctx.group, ctx.gate_first)
         return g["dx"], g["dz"], g["dweight"], None, None, None
 
 

@@ -11,7 +11,7 @@ from torch.autograd.graph import increment_version
 
 from . import _lib
 from .block_ops import _call, _gpu, _is, _view, _want, _want_or_none, _workspace
-from .ops import _io_code, _ptr
+from .ops import _gradient, _io_code, _ptr
 
 _F32 = torch.float32
 _View3 = _lib.View3
@@ -287,11 +287,7 @@ def head_norm_rotary_bwd(dq_out, dk_out, q, k=None, q_weight=None, k_weight=None
 
 def _cotangent(dy, like):
     shape, dtype, dev = like
-    return torch.zeros(shape, dtype=dtype, device=dev) if dy is None else dy.contiguous()
-
-
-def _plain(t):
-    return None if t is None else t.contiguous()
+    return torch.zeros(shape, dtype=dtype, device=dev) if dy is None else _gradient(dy)
 
 
 class GatedRecurrenceFn(torch.autograd.Function):
@@ -313,7 +309,7 @@ class GatedRecurrenceFn(torch.autograd.Function):
     def backward(ctx, dy, dfinal):
         x, decay_gate, input_gate, decay, z, states, starts, lengths = ctx.saved_tensors
         g = gated_recurrence_bwd(_cotangent(dy, (x.shape, x.dtype, x.device)), x, decay_gate, input_gate, decay, z,
-                                 states, starts, lengths, ctx.sharpness, _plain(dfinal),
+                                 states, starts, lengths, ctx.sharpness, _gradient(dfinal),
                                  want_dstate0=ctx.needs_input_grad[5])
         return (g["dx"], g["ddecay_gate"], g["dinput_gate"], g["ddecay"], g["dz"], g["dstate0"], None, None, None)
 
@@ -340,7 +336,7 @@ class CausalConvFn(torch.autograd.Function):
     def backward(ctx, dy, dfinal):
         x, weight, bias, state0, starts, lengths = ctx.saved_tensors
         g = causal_conv_bwd(_cotangent(dy, (x.shape, x.dtype, x.device)), x, weight, bias, state0, starts, lengths,
-                            ctx.silu, _plain(dfinal))
+                            ctx.silu, _gradient(dfinal))
         return g["dx"], g["dweight"], g["dbias"], g["dstate0"], None, None, None
 
 

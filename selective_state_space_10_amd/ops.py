@@ -36,6 +36,15 @@ def _need(name, t, shape, dtype, device, optional=False):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _gradient(t: Optional[torch.Tensor]):
+    """A gradient that autograd hands in, as the kernels read it: contiguous, and on a
+    16-byte boundary, which a slice of a larger gradient need not be."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _io_code(u: torch.Tensor) -> int:
     if u.dtype not in _IO:
         raise TypeError(f"io dtype must be float32 or bfloat16, got {u.dtype}")
@@ -336,7 +345,7 @@ class SelectiveScanFn(torch.autograd.Function):
     def backward(ctx, dy, dhf):
         u, delta, A, B, C, D, z, delta_bias, h0, cs = ctx.saved_tensors
         g = scan_bwd(u, delta, A, B, C, D, z, delta_bias, ctx.delta_softplus, h0, cs,
-                     dy.contiguous(), None if dhf is None else dhf.contiguous(),
+                     _gradient(dy), _gradient(dhf),
                      want_ddelta_bias=delta_bias is not None, want_dh0=h0 is not None,
                      zoh=ctx.zoh, reverse=ctx.reverse)
         return (g["du"], g["ddelta"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"],
@@ -378,7 +387,7 @@ class ConvScanFn(torch.autograd.Function):
     def backward(ctx, dy, dhf):
         x, conv_w, conv_b, delta, A, B, C, D, z, delta_bias, h0, cs = ctx.saved_tensors
         g = scan_bwd_conv(x, conv_w, conv_b, delta, A, B, C, D, z, delta_bias, ctx.delta_softplus,
-                          h0, cs, dy.contiguous(), None if dhf is None else dhf.contiguous(),
+                          h0, cs, _gradient(dy), _gradient(dhf),
                           want_ddelta_bias=delta_bias is not None, want_dh0=h0 is not None,
                           zoh=ctx.zoh)
         return (g["dx"], g["dconv_w"], g["dconv_b"], g["ddelta"], g["dA"], g["dB"], g["dC"],
