@@ -355,9 +355,10 @@ class DecayAttentionFn(torch.autograd.Function):
     def backward(ctx, do, dfinal):
         q, k, v, log_decay, state0 = ctx.saved_tensors
         do = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if do is None else _gradient(do)
+        # (a slice: apply() may have been given fewer arguments)
         g = decay_attn_bwd(q, k, v, log_decay, do, ctx.scale, state0, _gradient(dfinal),
                            want_dlog_decay=ctx.needs_input_grad[3],
-                           want_dstate0=ctx.needs_input_grad[5])
+                           want_dstate0=any(ctx.needs_input_grad[5:6]))
         return g["dq"], g["dk"], g["dv"], g["dlog_decay"], None, g["dstate0"]
 
 

@@ -308,9 +308,10 @@ class GatedRecurrenceFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, dfinal):
         x, decay_gate, input_gate, decay, z, states, starts, lengths = ctx.saved_tensors
+        # (a slice: apply() may have been given fewer arguments)
         g = gated_recurrence_bwd(_cotangent(dy, (x.shape, x.dtype, x.device)), x, decay_gate, input_gate, decay, z,
                                  states, starts, lengths, ctx.sharpness, _gradient(dfinal),
-                                 want_dstate0=ctx.needs_input_grad[5])
+                                 want_dstate0=any(ctx.needs_input_grad[5:6]))
         return (g["dx"], g["ddecay_gate"], g["dinput_gate"], g["ddecay"], g["dz"], g["dstate0"], None, None, None)
 
 
