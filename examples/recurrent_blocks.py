@@ -9,7 +9,8 @@ served token by token.
     x = projection of o                              x = projection of gated_norm(decay_attention(q, k, v), z)
 
 A document starts where ``starts`` says so: convolution, recurrence and decay attention
-carry nothing over it, and positions begin anew.
+carry nothing over it, the recurrence takes its first input in full, and positions begin
+anew.  A prompt's first token is marked too, so that serving computes what was trained.
 
 ``python examples/recurrent_blocks.py`` checks on the GPU that a prompt taken at once, and
 the same prompt in one piece followed by single tokens, give the same outputs.
@@ -51,6 +52,13 @@ class RecurrentBlock(torch.nn.Module):
         u, conv1 = ssm.causal_conv(u, self.conv, self.conv_bias, conv0, starts, lengths)
         o, h1 = ssm.gated_recurrence(u, g, i, self.decay, z, h0, starts, lengths)
         return self.out(o), h, (conv1, h1)
+
+    def prompt(self, x, residual, lengths=None):
+        """The beginnings of documents, which forward or step go on from: the first tokens are
+        marked, as packed documents' are in training."""
+        starts = torch.zeros(x.shape[:2], dtype=torch.bool, device=x.device)
+        starts[:, 0] = True
+        return self(x, residual, None, starts, lengths)
 
     @torch.no_grad()
     def step(self, x, residual, state):
@@ -129,10 +137,10 @@ def served(dtype=torch.bfloat16, batch=3, length=150, width=128, seed=0):
     residual = torch.randn(batch, length, width, device="cuda")
     positions = torch.arange(length, device="cuda").expand(batch, -1).contiguous()
     with torch.no_grad():
-        y, h, _ = one(x, residual)
+        y, h, _ = one.prompt(x, residual)
         whole, _, _ = two(y, h, positions)
         cut = length - 5
-        y, h, state1 = one(x[:, :cut].contiguous(), residual[:, :cut].contiguous())
+        y, h, state1 = one.prompt(x[:, :cut].contiguous(), residual[:, :cut].contiguous())
         _, _, state2 = two(y, h, positions[:, :cut].contiguous())
         tail = []
         for t in range(cut, length):

@@ -198,8 +198,11 @@ typedef struct ssm_view3 {
  *   decay:     (dim) fp32; sharpness > 0 and finite (not used without decay)
  *   state0:    (batch, dim) fp32 or NULL
  *   starts:    (batch, seqlen) bytes, NULL = none: where not zero, a document
- *              starts: a = 0 and s = 1.  Nothing crosses it, infinities and NaN
- *              included, in either direction.
+ *              starts: a = 0 and s = 1 in both forms, whatever the gate holds.
+ *              Nothing crosses it, infinities and NaN included, in either
+ *              direction.  A first step without a mark has the gate's s, so a
+ *              document gives the same in a packed row and in one of its own if
+ *              its first step is marked in both
  *   lengths:   (batch), NULL = seqlen: the rows' lengths in a padded batch
  *              (taken as 0 below 0 and as seqlen above).  Inputs behind a row's
  *              length are not used, y is zero there, and the state stays that
@@ -248,7 +251,8 @@ int ssm_gated_recurrence_bwd(int64_t batch, int64_t seqlen, int64_t dim, int io_
 
 /*
  * One token: state (batch, dim) fp32 is updated in place; y (batch, dim)
- * contiguous, io_dtype.  batch * dim <= 2^32.
+ * contiguous, io_dtype.  batch * dim <= 2^32.  It has no mark: the first token of
+ * a document is a sequence of one marked step.
  */
 int ssm_gated_recurrence_update(int64_t batch, int64_t dim, int io_dtype, float *state, const ssm_view3 *x,
                                 const ssm_view3 *decay_gate, const ssm_view3 *input_gate,

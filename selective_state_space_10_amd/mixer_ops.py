@@ -84,7 +84,10 @@ def gated_recurrence_fwd(x, decay_gate, input_gate=None, decay=None, z=None, sta
     and s = sqrt(1 - a^2); without, a = sigmoid(decay_gate) and s = 1 - a.
     x, decay_gate, input_gate, z (batch, seqlen, dim), strided views allowed; state0
     (batch, dim) fp32; ``starts`` (batch, seqlen) bool marks the first step of a
-    document: nothing crosses it; ``lengths`` (batch,) int32 are the rows' lengths
+    document: there a = 0 and so s = 1, in both forms and whatever the gate holds: nothing
+    crosses it, and its input counts in full.  A first step without a mark has the gate's s;
+    a document is the same in a packed row and in a row of its own if its first step is
+    marked in both.  ``lengths`` (batch,) int32 are the rows' lengths
     in a padded batch: behind them inputs are not used, y is zero, and the
     state stays.  Returns (y, final state or None, states or None): states
     (batch, ceil(seqlen / 128), dim), before every 128th step, are what the backward needs."""
@@ -127,7 +130,8 @@ def gated_recurrence_bwd(dy, x, decay_gate, input_gate, decay, z, states, starts
 
 def gated_recurrence_update(state, x, decay_gate, input_gate=None, decay=None, z=None, sharpness=8.0):
     """One token of gated_recurrence_fwd; ``state`` (batch, dim) fp32 is updated in
-    place.  x, decay_gate, input_gate, z (batch, dim).  Returns y."""
+    place.  x, decay_gate, input_gate, z (batch, dim).  Returns y.  It goes on in a document:
+    the first token of one is a gated_recurrence_fwd of one marked step."""
     dev, io, (B, D), views = _recurrence(x, decay_gate, input_gate, decay, z, 2)
     _want("state", state, (B, D), _F32, dev)
     y = torch.empty_like(x, memory_format=torch.contiguous_format)

@@ -270,6 +270,36 @@ def test_nothing_crosses_a_start(ssm, form, bad):
     assert not d["dstate0"][:2].any()
 
 
+@pytest.mark.parametrize("form", FORMS)
+def test_packed_documents_are_the_documents_alone(ssm, form):
+    """A document in a packed row and in a call of its own, its first step marked in both: outputs, last state and
+    gradients.  A first step without a mark has the gate's s instead of 1."""
+    p = ref.recurrence_inputs(1, 300, 24, form=form, z=False, state0=False)
+    p["starts"] = torch.zeros(1, 300, dtype=torch.bool)
+    ends = (0, 1, 140, 300)
+    p["starts"][0, list(ends[:-1])] = True
+    p["dfinal"].zero_()
+    g = ref.on_gpu(p)
+    y, final, states = forward(ssm, g)
+    d = backward(ssm, g, states)
+    for a, b in zip(ends, ends[1:]):
+        one = {n: t[:, a:b] if t is not None and t.dim() == 3 else t for n, t in g.items()}
+        one["starts"] = g["starts"][:, a:b].contiguous()
+        y1, final1, states1 = forward(ssm, one)
+        d1 = backward(ssm, one, states1)
+        assert ref.error(y1, y[:, a:b].cpu()) <= 2 * tol(b - a)
+        assert all(ref.error(d1[n], d[n][:, a:b].cpu()) <= 6 * tol(b - a) for n in ("dx", "dinput_gate", "ddecay_gate"))
+    assert ref.error(final1, final.cpu()) <= 2 * tol(b - a)
+    one["starts"] = None
+    gate = p["decay_gate"][:, a].double()
+    if form == "power":
+        rate = 8 * torch.nn.functional.softplus(p["decay"].double()) * torch.sigmoid(gate)
+        s = torch.sqrt(-torch.expm1(-2 * rate))
+    else:
+        s = torch.sigmoid(-gate)
+    assert ref.error(forward(ssm, one)[0][:, 0], s * y[:, a].cpu()) <= 2 * tol(1)
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("form", FORMS)
 def test_the_decay_gate_of_a_start_is_not_used(ssm, form, bad):

@@ -135,6 +135,31 @@ def test_serving(blocks, dtype, tol):
     assert blocks.served(dtype) <= tol
 
 
+@pytest.mark.parametrize("documents", [(1, 40, 59), (100,)])
+def test_packed_training_is_what_is_served(blocks, documents):
+    """Documents packed into one training row, and each served by itself, as a prompt of a part of it and single
+    tokens.  fp32: as in test_serving, products in another order."""
+    torch.manual_seed(4)
+    block = blocks.RecurrentBlock(64, 72, dtype=torch.float32)
+    gen = torch.Generator().manual_seed(5)
+    x, residual = torch.randn(1, 100, 64, generator=gen).cuda(), torch.randn(1, 100, 64, generator=gen).cuda()
+    starts = torch.zeros(1, 100, dtype=torch.bool, device="cuda")
+    at = 0
+    for n in documents:
+        starts[:, at] = True
+        at += n
+    with torch.no_grad():
+        want = block(x, residual, starts=starts)[0]
+        got, at = [], 0
+        for n in documents:
+            cut = max(1, n // 2)
+            y, _, state = block.prompt(x[:, at:at + cut], residual[:, at:at + cut])
+            got.append(y)
+            got += [block.step(x[:, t], residual[:, t], state)[0][:, None] for t in range(at + cut, at + n)]
+            at += n
+    assert error(torch.cat(got, 1), want.cpu()) <= 1e-4
+
+
 def test_training_steps_in_a_graph(blocks):
     """Forward, backward and gradients of both blocks captured once and replayed on other
     inputs, with eager steps of the same blocks between; all eager graphs are gone
