@@ -262,6 +262,8 @@ def head_norm_rotary_fwd(q, k=None, q_weight=None, k_weight=None, positions=None
     for both, fp32, None = 1; norm=False leaves the norm out.  positions int64, (batch,
     seqlen) or (seqlen,), for single tokens (batch,); inv_freq (rotary / 2,) fp64; without them
     nothing is rotated.  Pair p is (p, p + rotary / 2), or with interleaved (2p, 2p + 1).
+    Every row is one by itself, those of padding too: for the weights' gradients they should be
+    finite, since 0 times what they hold is in the sum.
     Returns (q, k) normed and rotated, contiguous."""
     dev, io, sizes, views, rest = _heads(q, k, q_weight, k_weight, positions, inv_freq, norm)
     q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
