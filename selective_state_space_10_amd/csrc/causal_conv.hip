@@ -16,9 +16,9 @@
 
 namespace ssm {
 
-namespace {
+using namespace conv;
 
-constexpr int kRows = 8;  // rows whose loads are under way together
+namespace {
 
 template <int X>
 struct Int {
@@ -169,8 +169,6 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, uint32_t nchu
 // All of a wave is at the same step, so that steps, starts and lengths are scalar work.
 // Two channels and not eight: 74 registers' worth of sums and windows less, six waves per
 // SIMD instead of two (8 x 2048 x 2048 bf16: 101 us with eight).
-constexpr int kBwdRows = 120;  // at most: two words of starts of documents, offsets below 2^32 bytes
-
 template <typename T>
 struct Raw2;
 template <>
@@ -381,26 +379,6 @@ hipError_t by_width(int width, F f) {
 }
 
 constexpr int kFwdSteps = 32;
-
-// Steps per wave and chunk, from 16 to kBwdRows: the workgroups that are resident at
-// once (four of four waves per CU in bf16, three in fp32) take equal numbers of chunks, and
-// the fewest steps in all are walked over, with the K-1 that a chunk shares with the next
-// and about 6 for its start (8 x 2048 x 2048 bf16 packed: 58 us with 64 steps, of which
-// 1088 workgroups are not all resident).
-struct BwdPlan {
-  int64_t ctiles, nchunk, nruns;
-  int nrow;
-};
-BwdPlan bwd_plan(int64_t B, int64_t L, int64_t D, int width, int es) {
-  const int64_t ctiles = (D + 127) / 128, resident = es == 2 ? 1024 : 768, most = ctiles < resident ? resident / ctiles : 1;
-  BwdPlan best{};
-  int64_t least = -1;
-  for (int nrow = 16; nrow <= kBwdRows; nrow += kRows) {
-    const int64_t nchunk = (L + nrow - width) / (nrow - width + 1), need = (B * nchunk + 3) / 4, each = (need + most - 1) / most;
-    if (least < 0 || each * (nrow + 6) < least) least = each * (nrow + 6), best = {ctiles, nchunk, (need + each - 1) / each, nrow};
-  }
-  return best;
-}
 
 template <typename T>
 hipError_t fwd(const ConvArgs &a, hipStream_t s) {

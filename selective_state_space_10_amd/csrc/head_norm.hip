@@ -21,21 +21,9 @@
 
 namespace ssm {
 
+using namespace heads;
+
 namespace {
-
-constexpr int kThreads = 256;
-constexpr int kMaxTable = 2048;  // angles in LDS
-// Rows of a group between two fillings of the table: few start sooner and leave more workgroups to
-// even out (8 x 2048, 32 and 4 heads of 64 bf16: forward 41 -> 39 us with 4 for 8, backward 62 -> 56; 16 and 16
-// of 128 fp32 backward 135 -> 130, interleaved forward 104 -> 96; 32K context backward 244 -> 236), but one
-// token at a time in the bf16 forward waits for each filling (40 and 8 heads of 128 176 against 172, 16 and
-// 16 interleaved 56 against 52; two rows lose 2 to 20% nearly everywhere).
-constexpr int max_rows(bool bwd, int es, int tpr) { return !bwd && es == 2 && tpr >= 16 ? 8 : 4; }
-
-struct Plan {
-  int tpr, nblk, hb, tsub, rows;  // lanes per head, blocks of heads, heads per block, tokens at once, rows per group of a chunk of tokens
-  int64_t nchunk, nruns;
-};
 
 // cos and sin of 2 pi turns, |turns| <= 1/2: to the nearest quarter, then the
 // series of an angle up to pi / 4; what they leave out is below 2^-28.
@@ -261,38 +249,6 @@ __global__ void __launch_bounds__(kThreads, BWD ? 1 : 6) head_norm_kernel(HeadNo
   }
 }
 
-constexpr int64_t kFwdWorkgroups = 65536, kBwdWorkgroups = 1024;
-
-int64_t most_runs(int nblk, int64_t workgroups) { return nblk < workgroups ? workgroups / nblk : 1; }
-
-int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
-int least_blocks(int HT, int tpr) { return (HT + kThreads / tpr - 1) / (kThreads / tpr); }
-constexpr int kMoreBlocks = 8;
-
-Plan plan_of(int64_t B, int64_t L, int HT, int d, int rot, bool bwd, int es) {
-  const int64_t workgroups = bwd ? kBwdWorkgroups : kFwdWorkgroups;
-  Plan p;
-  p.tpr = lanes_of(d);
-  // Blocks of heads: few, since each forms the angles of its tokens, and so that few groups
-  // of lanes are left over.  Per token: a row is about 120 instructions of a lane, an
-  // angle 50 of one of the workgroup's lanes (36 heads of 64 on 32 groups in 5 blocks of 8
-  // heads and 4 tokens, not in 2 of 18 and one).
-  const int groups = kThreads / p.tpr;
-  double least = 0.0;
-  for (int nblk = least_blocks(HT, p.tpr); nblk <= HT && nblk <= least_blocks(HT, p.tpr) + kMoreBlocks; ++nblk) {
-    const int hb = (HT + nblk - 1) / nblk, tsub = groups / hb;
-    const double cost = 120.0 * nblk / tsub + 50.0 * nblk * (rot / 2) / kThreads;
-    if (least == 0.0 || cost < least) least = cost, p.nblk = (HT + hb - 1) / hb, p.hb = hb, p.tsub = tsub;
-  }
-  p.rows = max_rows(bwd, es, p.tpr);
-  while (p.rows > 1 && (p.tsub * p.rows * (rot / 2) > kMaxTable)) p.rows /= 2;
-  const int64_t tt = p.tsub * p.rows;
-  p.nchunk = B * ((L + tt - 1) / tt);
-  const int64_t most = most_runs(p.nblk, workgroups);
-  p.nruns = p.nchunk < most ? p.nchunk : most;
-  return p;
-}
-
 // Batch rows that follow each other evenly are one row; so are rows of one token.
 HeadNormArgs merged(HeadNormArgs a, bool bwd) {
   auto even = [&](const HeadView &v) { return a.L == 1 || v.sb == v.st * a.L; };
@@ -333,13 +289,7 @@ hipError_t launch(const HeadNormArgs &given, hipStream_t s) {
 
 }  // namespace
 
-// The largest that any rotation, any strides and either kind of weights of these sizes need.
-int64_t head_norm_bwd_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d) {
-  const int64_t HT = Hq + Hk, N = B * L, few = least_blocks((int)HT, lanes_of((int)d)), many = few + kMoreBlocks;
-  const int64_t runs = most_runs((int)few, kBwdWorkgroups), per_head = (N < runs ? N : runs) * HT;
-  const int64_t all = many < kBwdWorkgroups ? kBwdWorkgroups : many, shared = 2 * (N < all / many ? N * many : all);
-  return (per_head > shared ? per_head : shared) * d * 4;
-}
+int64_t head_norm_bwd_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d) { return bwd_workspace_bytes(B, L, Hq, Hk, d); }
 
 hipError_t launch_head_norm_fwd(const HeadNormArgs &a, int io_dtype, hipStream_t s) { return io_dtype == 0 ? launch<float, false>(a, s) : launch<bf16, false>(a, s); }
 hipError_t launch_head_norm_bwd(const HeadNormArgs &a, int io_dtype, hipStream_t s) { return io_dtype == 0 ? launch<float, true>(a, s) : launch<bf16, true>(a, s); }

@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mixer_plans.hpp"
+
 namespace ssm {
 
 // (batch, step, channel) tensor, strides in elements, channels adjacent.
@@ -14,8 +16,6 @@ struct View3 {
   const void *p;
   int64_t sb, st;
 };
-
-constexpr int kRecurrenceChunk = 128;  // SSM_RECURRENCE_CHUNK
 
 struct RecurrenceArgs {
   int64_t B, L, D;

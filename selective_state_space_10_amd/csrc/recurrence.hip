@@ -19,6 +19,8 @@
 
 namespace ssm {
 
+using namespace recurrence;
+
 namespace {
 
 // The decay's gate.  Power form: r = sigmoid(g), log2 a = rate2 r, s^2 = 1 - a^2,
@@ -79,10 +81,6 @@ __device__ __forceinline__ float rate_of(float sharpness, float v) { return -sha
 // composes the maps of the chunks before its own since then, always in the same
 // order, so that results do not depend on who was first.  A wait that is not served
 // within about a second (a workspace written to meanwhile) ends with NaN.
-
-constexpr int kWaves = 8, kSteps = 16;
-static_assert(kWaves * kSteps == kRecurrenceChunk, "a wave takes kSteps steps of a chunk");
-constexpr int kMaxGroup = 2 * kWaves;  // two words per wave: a state and the maps of 15 chunks
 
 // A value that is the same in all lanes, in a scalar register.
 __device__ __forceinline__ int uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
@@ -528,17 +526,6 @@ hipError_t by_switches(bool power, bool ig, bool z, bool marks, F f) {
   auto l = [&](auto p, auto i) { return z ? m(p, i, Int<1>{}) : m(p, i, Int<0>{}); };
   auto o = [&](auto p) { return ig ? l(p, Int<1>{}) : l(p, Int<0>{}); };
   return power ? o(Int<1>{}) : o(Int<0>{});
-}
-
-// Chunks per published state.  A state's way from one workgroup to the next takes
-// about 1.25 us, and the maps between states are words to read in every workgroup
-// behind: as few maps as keep the states' way through the sequence below 2/5 of the
-// time that the tensors need (x, both gates and y at 4 TB/s).
-int group_of(int64_t B, int64_t L, int64_t D, int es) {
-  const double us = (double)(B * L) * (double)(4 * D * es) / 4e6, way = (double)((L + kRecurrenceChunk - 1) / kRecurrenceChunk) * 1.25;
-  int g = 1;
-  while (g < kMaxGroup && way > 0.4 * us * g) g *= 2;
-  return g;
 }
 
 // cpl: channels per lane, es: bytes of an element
