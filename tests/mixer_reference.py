@@ -172,3 +172,29 @@ def heads(p, eps=1e-6, norm=True, interleaved=False, grads=True):
 
 def on_gpu(p):
     return {n: None if t is None else t.cuda() for n, t in p.items()}
+
+
+# ---- the convolution at sizes of training, all steps at once
+
+
+def conv_at_once(p, silu=True):
+    """As conv, on the inputs' device: every tap as a shifted tensor, masked where a document starts between."""
+    v = {n: None if p[n] is None else p[n].detach().to(F64).clone().requires_grad_() for n in CONV_INPUTS}
+    B, L, D = p["x"].shape
+    K, dev = p["weight"].shape[1], p["x"].device
+    end = torch.full((B,), L, device=dev) if p["lengths"] is None else p["lengths"].long()
+    on = (torch.arange(L, device=dev) < end[:, None])[..., None]
+    doc = torch.zeros(B, L, dtype=torch.int64, device=dev) if p["starts"] is None else p["starts"].long().cumsum(1)
+    doc = torch.cat([doc.new_zeros(B, K - 1), doc], 1)  # a state's inputs belong to the row's first document
+    head = v["x"].new_zeros(B, K - 1, D) if v["state0"] is None else v["state0"]
+    xs = torch.cat([head, torch.where(on, v["x"], 0.0)], 1)
+    pre = torch.zeros_like(v["x"]) if v["bias"] is None else v["bias"].expand(B, L, D)
+    for k in range(K):
+        pre = pre + v["weight"][:, k] * torch.where((doc[:, k:k + L] == doc[:, K - 1:])[..., None], xs[:, k:k + L], 0.0)
+    y = torch.where(on, pre * torch.sigmoid(pre) if silu else pre, 0.0)
+    at = end[:, None] + torch.arange(K - 1, device=dev)  # the last K - 1 inputs; at - (K - 1) is a step
+    last = doc.gather(1, (end + K - 2).clamp(min=0)[:, None])
+    final = torch.where((doc.gather(1, at) == last)[..., None], xs.gather(1, at[..., None].expand(-1, -1, D)), 0.0)
+    names = [n for n in CONV_INPUTS if v[n] is not None]
+    gr = torch.autograd.grad((y * p["dy"].to(F64)).sum() + (final * p["dfinal"].to(F64)).sum(), [v[n] for n in names], allow_unused=True)
+    return y.detach(), final.detach(), {"d" + n: torch.zeros_like(v[n]) if t is None else t for n, t in zip(names, gr)}

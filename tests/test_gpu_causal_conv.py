@@ -12,6 +12,7 @@ import pytest
 import torch
 
 from tests import mixer_reference as ref
+from tests.test_mixer_plans import CONV
 
 pytestmark = pytest.mark.gpu
 
@@ -91,6 +92,28 @@ def test_dense_starts(ssm, L):
 @pytest.mark.parametrize("B,L", [(1, 5000), (40, 300), (300, 20)])
 def test_many_rows(ssm, B, L):
     check(ssm, B, L, 16, 4, starts=True, lengths=True)
+
+
+@pytest.mark.parametrize("sizes", CONV, ids=str)
+@pytest.mark.parametrize("marks", [False, True])
+def test_training_sizes(ssm, sizes, marks):
+    """Chunks of more than 64 steps, and several of them to a wave, with and without starts and lengths."""
+    B, L, D, K, es = sizes
+    print("conv", sizes, marks, flush=True)
+    gen = torch.Generator("cuda").manual_seed(L + D)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    dtype = BF16 if es == 2 else F32
+    g = dict(x=r(B, L, D).to(dtype), weight=r(D, K) * K ** -0.5, bias=r(D), state0=r(B, K - 1, D).to(dtype), dy=r(B, L, D).to(dtype),
+             dfinal=r(B, K - 1, D).to(dtype), starts=None, lengths=None)
+    if marks:
+        g["starts"] = torch.rand(B, L, generator=gen, device="cuda") < 0.02
+        g["lengths"] = torch.tensor([L, L - 3, 0, 70, 1, L // 2, L, L - 40][:B], dtype=torch.int32, device="cuda")
+    y, final = forward(ssm, g)
+    d = backward(ssm, g)
+    ry, rf, rg = ref.conv_at_once(g)
+    assert ref.error(y, ry.cpu()) <= TOL and torch.equal(final.double(), rf)
+    for n, got in d.items():
+        assert ref.error(got, rg[n].cpu()) <= (TOL if n in ("dx", "dstate0") else SUMS), n
 
 
 @pytest.mark.parametrize("seed", range(16))

@@ -1,0 +1,35 @@
+"""How the gated recurrence, the convolution and the heads are split over workgroups: the plans of the
+sizes that the GPU tests of training sizes rest on, so that another rule cannot move those
+tests off the paths that they are for.  And the convolution's reference at once against the one step by step."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests import mixer_plans as plans
+from tests import mixer_reference as ref
+
+
+@pytest.mark.parametrize("K", [1, 2, 4])
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("seed", range(8))
+def test_convolution_at_once(K, silu, seed):
+    coin = lambda i: bool(seed >> i & 1)  # noqa: E731
+    p = ref.conv_inputs(4, 1 + 7 * seed, 8, K, bias=coin(0), state0=coin(1), starts=coin(2), lengths=not coin(0), seed=seed)
+    if p["starts"] is not None:
+        p["starts"] = torch.rand(p["starts"].shape, generator=torch.Generator().manual_seed(seed)) < 0.3
+    y, final, g = ref.conv_at_once(p, silu)
+    y1, final1, g1 = ref.conv(p, silu)
+    assert torch.allclose(y, y1) and torch.equal(final, final1) and g.keys() == g1.keys()
+    assert all(torch.allclose(g[n], g1[n]) for n in g)
+
+
+# B, L, D, width, bytes of an element: (more than 64 steps of a chunk, several chunks of a wave)
+CONV = {(8, 2048, 2048, 4, 2): (True, False), (8, 2048, 2048, 4, 4): (True, False), (2, 257, 65672, 4, 2): (True, True),
+        (3, 333, 32776, 4, 4): (True, True), (1, 1000, 32776, 3, 4): (True, True), (1, 700, 65672, 2, 2): (True, True)}
+
+
+@pytest.mark.parametrize("sizes", CONV, ids=str)
+def test_convolution_backward(sizes):
+    p = plans.conv_backward(*sizes)
+    assert (p["nrow"] > 64, sizes[0] * p["nchunk"] > 4 * p["nruns"]) == CONV[sizes], p
