@@ -16,6 +16,7 @@ import pytest
 import torch
 
 from tests import mixer_reference as ref
+from tests.test_mixer_plans import RECURRENCE
 
 pytestmark = pytest.mark.gpu
 
@@ -52,14 +53,14 @@ def check(ssm, B, L, D, sharpness=8.0, **kw):
     compare(ssm, p, ref.on_gpu(p), sharpness)
 
 
-def compare(ssm, p, g, sharpness=8.0):
+def compare(ssm, p, g, sharpness=8.0, t=None, want=None):
     L = p["x"].shape[1]
     y, final, states = forward(ssm, g, sharpness)
     d = backward(ssm, g, states, sharpness)
-    ry, rf, rb, rg = ref.recurrence(p, sharpness)
+    ry, rf, rb, rg = want or ref.recurrence(p, sharpness)
     normal = lambda w: torch.where(w.abs() < 2.0 ** -126, 0.0, w)  # noqa: E731
     rg = {n: normal(w) for n, w in rg.items()}
-    t = tol(L)
+    t = tol(L) if t is None else t
     assert y.dtype == p["x"].dtype and final.dtype == states.dtype == F32
     for n, got, want, most in [("y", y, ry, t), ("final", final, rf, t), ("states", states, rb[:, ::128], t)]:
         assert ref.error(got, want) <= most, (n, ref.error(got, want), most)
@@ -98,6 +99,62 @@ def test_widths(ssm, D, dtype):
 @pytest.mark.parametrize("lengths", [True, False])
 def test_options(ssm, form, input_gate, z, state0, starts, lengths):
     check(ssm, 4, 150, 40, form=form, input_gate=input_gate, z=z, state0=state0, starts=starts, lengths=lengths, dtype=BF16 if z else F32)
+
+
+@pytest.mark.parametrize("sizes", RECURRENCE, ids=str)
+@pytest.mark.parametrize("marks", [False, True])
+@pytest.mark.parametrize("form", FORMS)
+def test_states_handed_on(ssm, sizes, marks, form):
+    """Decays so close to 1 that a state is felt over many chunks, at sizes where states are published every 1, 2, 4, 8
+    and 16 chunks, and more than once.
+
+    The tolerance: a decay next to 1 is off by up to 2^-24 from its exponential (1 step of numbers in [1/2, 1)), and not
+    of either sign alike: over 65536 decays between 1 - 1e-4 and 1 the instruction is off by -0.116 of that on average
+    (as torch's fp32 exponential is), where rounding would be off by 0.00.  What a state keeps of a step k steps
+    back is then off by up to k of these at once, and a state by up to L: L 2^-24 more than tol(L), which has the
+    random part.  (tol(L) alone failed by 6% at 2 x 2100 x 520.)"""
+    B, L, D, es = sizes
+    print("recurrence", sizes, marks, form, flush=True)
+    p = ref.recurrence_inputs(B, L, D, form=form, dtype=BF16 if es == 2 else F32, seed=L)
+    u = torch.rand(D, generator=torch.Generator().manual_seed(D))
+    if form == "power":
+        p["decay"] = torch.log(torch.expm1(-torch.log(0.99 + 0.0099 * u) / 8.0))
+    else:
+        p["decay_gate"] += 3.0  # (a mean of 5)
+    if marks:
+        p["starts"] = torch.rand(B, L, generator=torch.Generator().manual_seed(L)) < 0.002
+        p["starts"][:, 300] = True
+        p["lengths"] = torch.tensor([L, L - 130, L, 0, L, 290, L, L - 1][:B], dtype=torch.int32)
+    g = ref.on_gpu(p)
+    with torch.device("cuda"):  # (the reference's many small steps are quicker there)
+        y, final, before, grads = ref.recurrence(g)
+    want = y.cpu(), final.cpu(), before.cpu(), {n: t.cpu() for n, t in grads.items()}
+    compare(ssm, p, g, t=tol(L) + L * 2.0 ** -24, want=want)
+
+
+def test_states_handed_on_over_the_longest_rows(ssm):
+    """More than 2^31 elements of output, a state felt over many chunks: every row of a batch, whose states are published
+    after each chunk, against a row by itself, published after every second, and against 64 bits.  Gates of 6 forget
+    in 404 steps, of which each has the same error in its decay, of up to 2 units (the reciprocal's 1, the sum's
+    and the exponential's parts in 1 + e^-6): 2 x 404 units of 2^-24 over tol(404).  Between the two calls, whose decays
+    are the same, twice tol(404)."""
+    B, L, D = 3, 87500, 8192
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    row = torch.randn(1, L, D, generator=gen, device="cuda").to(BF16)
+    gate = torch.full((1, 1, D), 6.0, dtype=BF16, device="cuda")
+    y, f, _ = ssm.gated_recurrence_fwd(row.expand(B, L, D), gate.expand(B, L, D), return_final_state=True)
+    y1, f1, _ = ssm.gated_recurrence_fwd(row, gate.expand(1, L, D), return_final_state=True)
+    t = tol(404) + 808 * 2.0 ** -24
+    some = slice(5, None, 127)
+    a, h, d = torch.full((L, 1), 1 / (1 + math.exp(-6.0)), dtype=torch.float64, device="cuda"), row[0, :, some].double() / (1 + math.exp(6.0)), 1
+    while d < L:  # each step's sum of the 2 d steps up to it
+        h[d:] += a[d:] * h[:-d]
+        a[d:] = a[d:] * a[:-d]
+        d *= 2
+    for b in range(B):
+        assert ref.error(y[b][:, some], h.cpu()) <= t
+        assert float((f[b] - f1[0]).abs().max() / f1.abs().max()) <= 2 * tol(404)
+    assert ref.error(y1[0][:, some], h.cpu()) <= t
 
 
 @pytest.mark.parametrize("L", [4095, 4097, 4500, 8200])

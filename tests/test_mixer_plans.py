@@ -33,3 +33,18 @@ CONV = {(8, 2048, 2048, 4, 2): (True, False), (8, 2048, 2048, 4, 4): (True, Fals
 def test_convolution_backward(sizes):
     p = plans.conv_backward(*sizes)
     assert (p["nrow"] > 64, sizes[0] * p["nchunk"] > 4 * p["nruns"]) == CONV[sizes], p
+
+
+# B, L, D, bytes of an element: chunks per published state, fewer than the sequence has
+RECURRENCE = {(8, 515, 2056, 2): 1, (2, 700, 4104, 2): 2, (3, 700, 2056, 2): 4, (2, 1100, 1000, 2): 8, (2, 2100, 520, 2): 16,
+              (8, 700, 1000, 4): 1, (4, 700, 1000, 4): 2, (3, 1537, 1000, 4): 4, (2, 1537, 712, 4): 8}
+
+
+@pytest.mark.parametrize("sizes", RECURRENCE, ids=str)
+def test_recurrence(sizes):
+    group = plans.recurrence_group(*sizes)
+    assert group == RECURRENCE[sizes] and -(-sizes[1] // 128) > group
+
+
+def test_recurrence_of_the_longest_rows():
+    assert (plans.recurrence_group(3, 87500, 8192, 2), plans.recurrence_group(1, 87500, 8192, 2)) == (1, 2)
