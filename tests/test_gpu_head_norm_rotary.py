@@ -12,6 +12,7 @@ import pytest
 import torch
 
 from tests import mixer_reference as ref
+from tests.test_mixer_plans import HEADS
 
 pytestmark = pytest.mark.gpu
 
@@ -132,6 +133,27 @@ def test_zero_and_bad_heads_stay_by_themselves(ssm):
         assert torch.isnan(got[0, t, h]).any()
         got[0, t, h] = want[0, t, h].float()
         assert ref.error(got, want) <= TOL
+
+
+@pytest.mark.parametrize("sizes", sorted(HEADS), ids=str)
+@pytest.mark.parametrize("weights,interleaved,strided", [("shared", False, False), ("per head", True, False), ("shared", True, True), ("per head", False, True)])
+def test_training_sizes(ssm, sizes, weights, interleaved, strided):
+    """Several chunks of tokens to a workgroup: the angles filled again, sums carried on, batch rows apart or as one."""
+    B, L, Hq, Hk, d, es = sizes
+    print("heads", sizes, weights, interleaved, strided, flush=True)
+    p = ref.head_inputs(B, L, Hq, Hk, d, d, weights=weights, dtype=BF16 if es == 2 else F32, seed=L)
+    g = ref.on_gpu(p)
+    if strided:  # heads before steps: no row of the batch follows the one before it
+        for n in ("q", "k", "dq_out", "dk_out"):
+            g[n] = g[n].transpose(1, 2).contiguous().transpose(1, 2)
+    out = dict(zip(("q", "k"), forward(ssm, g, interleaved=interleaved)))
+    got = backward(ssm, g, interleaved=interleaved)
+    with torch.device("cuda"):
+        want, grads = ref.heads(g, interleaved=interleaved)
+    for n, t in out.items():
+        assert ref.error(t, want[n].cpu()) <= TOL, n
+    for n, t in got.items():
+        assert ref.error(t, grads[n].cpu()) <= (SUMS if n.endswith("weight") else TOL), n
 
 
 @pytest.mark.parametrize("seed", range(20))

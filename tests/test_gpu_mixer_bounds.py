@@ -95,3 +95,21 @@ def test_heads(ssm, guards, dtype, weights, B, L, Hq, Hk, d, rot):
     guards()
     ssm.head_norm_rotary_bwd(g["dq_out"], g["dk_out"], *args)
     guards()
+
+
+@pytest.mark.parametrize("weights", ["shared", "per head"])
+@pytest.mark.parametrize("B,L,Hq,Hk,d,rot", [(1, 9000, 16, 16, 128, 128), (1, 9000, 20, 5, 80, 40), (1, 70000, 1, 0, 8, 8), (1, 300, 300, 20, 128, 64)])
+def test_heads_with_all_workgroups(ssm, guards, weights, B, L, Hq, Hk, d, rot):
+    """The workspace of as many workgroups as there are at most, and of blocks of heads beyond that."""
+    print("heads", weights, B, L, Hq, Hk, d, rot, flush=True)
+    g = ref.on_gpu(ref.head_inputs(B, L, Hq, Hk, d, rot, dtype=BF16, weights=weights))
+    ssm.head_norm_rotary_bwd(g["dq_out"], g["dk_out"], *(g[n] for n in ("q", "k", "q_weight", "k_weight", "positions", "inv_freq")))
+    guards()
+
+
+@pytest.mark.parametrize("K,D,B,L,dtype", [(4, 65672, 2, 257, BF16), (3, 32776, 1, 1000, F32), (2, 2056, 8, 500, BF16)])
+def test_conv_with_all_workgroups(ssm, guards, K, D, B, L, dtype):
+    print("conv", K, D, B, L, dtype, flush=True)
+    g = ref.on_gpu(ref.conv_inputs(B, L, D, K, dtype=dtype, starts=True, lengths=True))
+    ssm.causal_conv_bwd(g["dy"], g["x"], g["weight"], g["bias"], g["state0"], g["starts"], g["lengths"], dstate_final=g["dfinal"])
+    guards()

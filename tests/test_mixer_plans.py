@@ -48,3 +48,14 @@ def test_recurrence(sizes):
 
 def test_recurrence_of_the_longest_rows():
     assert (plans.recurrence_group(3, 87500, 8192, 2), plans.recurrence_group(1, 87500, 8192, 2)) == (1, 2)
+
+
+# B, L, q heads, k heads, dim, bytes of an element: several chunks of tokens per workgroup in the backward
+HEADS = {(1, 9000, 16, 16, 128, 2), (3, 3000, 16, 16, 128, 4), (2, 4500, 32, 4, 64, 2), (1, 9000, 20, 5, 80, 4)}
+
+
+@pytest.mark.parametrize("sizes", sorted(HEADS), ids=str)
+def test_heads_backward(sizes):
+    B, L, Hq, Hk, d, es = sizes
+    p = plans.heads(1, B * L, Hq + Hk, d, d, 1, es)  # (contiguous rows of a batch follow each other as one)
+    assert p["nchunk"] > 2 * p["nruns"], p
