@@ -32,7 +32,7 @@ __device__ __forceinline__ float4 load_once(const float4 *p) {
   return __builtin_bit_cast(float4, __builtin_nontemporal_load((const f4 *)p));
 }
 
-// N adjacent elements, a multiple of 4, at a 16-byte aligned address (8-byte for 4 of bf16).
+// Adjacent elements at an address aligned to 16 bytes, 8 in bf16: 4 of them, of fp32 any multiple of 4.
 template <int N>
 __device__ __forceinline__ void load_vec(const float *p, float (&v)[N]) {
 #pragma unroll
@@ -41,41 +41,14 @@ __device__ __forceinline__ void load_vec(const float *p, float (&v)[N]) {
     v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
   }
 }
-template <int N>
-__device__ __forceinline__ void load_vec(const bf16 *p, float (&v)[N]) {
-  uint32_t w[N / 2];
-  if constexpr (N == 4) {
-    const uint2 a = *(const uint2 *)p;
-    w[0] = a.x, w[1] = a.y;
-  } else {
+__device__ __forceinline__ void load_vec(const bf16 *p, float (&v)[4]) {
+  const uint2 a = *(const uint2 *)p;
+  const uint32_t w[2] = {a.x, a.y};
 #pragma unroll
-    for (int i = 0; i < N; i += 8) {
-      const uint4 a = *(const uint4 *)(p + i);
-      w[i / 2] = a.x, w[i / 2 + 1] = a.y, w[i / 2 + 2] = a.z, w[i / 2 + 3] = a.w;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  for (int i = 0; i < 2; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
 }
-template <int N>
-__device__ __forceinline__ void store_vec(float *p, const float (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 4) *(float4 *)(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-}
-template <int N>
-__device__ __forceinline__ void store_vec(bf16 *p, const float (&v)[N]) {
-  uint32_t w[N / 2];
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-  if constexpr (N == 4) {
-    *(uint2 *)p = make_uint2(w[0], w[1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 8) *(uint4 *)(p + i) = make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
-  }
-}
-__device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_one(bf16 *p, float v) { p->bits = (uint16_t)pack_bf16(v, v); }
+__device__ __forceinline__ void store_vec(float *p, const float (&v)[4]) { *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void store_vec(bf16 *p, const float (&v)[4]) { *(uint2 *)p = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])); }
 
 // sigmoid(v) and 1 - sigmoid(v), neither from the other by a subtraction: e^-v
 // over 1 + e^-v keeps the digits of a nearly open gate's complement.

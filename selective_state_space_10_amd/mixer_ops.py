@@ -10,7 +10,7 @@ from torch.autograd.function import once_differentiable
 from torch.autograd.graph import increment_version
 
 from . import _lib
-from .block_ops import _call, _gpu, _is, _view, _want, _want_or_none, _workspace
+from .block_ops import _call, _gpu, _view, _want, _want_or_none, _workspace
 from .ops import _gradient, _io_code, _ptr
 
 _F32 = torch.float32
