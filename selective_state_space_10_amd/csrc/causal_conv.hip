@@ -6,11 +6,12 @@
 // width - 1 inputs in registers; the rows before its chunk (and in the backward
 // those after it, whose outputs its inputs reach) are read again, mostly from L2.
 //
-// Measured, width 4, per call: forward 4 x 4096 x 5120 bf16 (336 MB) 72 us, 4.7 TB/s, a
-// large copy 5.1; 8 x 2048 x 2048 fp32 (268 MB) 46 us; backward 8 x 2048 x 2048 bf16
-// (201 MB) on packed documents 52 us with 5 for the second kernel, 3.9 TB/s: one round of
-// four waves per SIMD, whose start and end nothing overlaps; 4 x 4096 x 5120 (503 MB) 108 us.
-// One token of 2048 channels takes 2.2 us, latency.
+// Measured, width 4, per call: forward 4 x 4096 x 5120 bf16 (336 MB) 69 us, 4.9 TB/s, a
+// large copy 5.1; 8 x 2048 x 2048 fp32 (268 MB) 46 us; 1 x 2048 x 2048 bf16 (17 MB) 13 us, four loads'
+// latency of 32 steps in 130 workgroups; backward 8 x 2048 x 2048 bf16
+// (201 MB) on packed documents 50 us with 4 for the second kernel, 4.0 TB/s: one round of
+// four waves per SIMD, whose start and end nothing overlaps; 4 x 4096 x 5120 (503 MB) 107 us.
+// One token of 2048 channels takes 2.4 us, latency.
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
 
@@ -167,8 +168,8 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, uint32_t nchu
 // dx of nrow - (K-1) steps t and as much of the weights' sums, which stay in registers
 // over its chunks; a workgroup adds its waves' sums and a second kernel the workgroups', in order.
 // All of a wave is at the same step, so that steps, starts and lengths are scalar work.
-// Two channels and not eight: 74 registers' worth of sums and windows less, six waves per
-// SIMD instead of two (8 x 2048 x 2048 bf16: 101 us with eight).
+// Two channels and not eight: 74 registers' worth of sums and windows less, four waves per
+// SIMD in bf16 (three in fp32) instead of two (8 x 2048 x 2048 bf16: 101 us with eight).
 template <typename T>
 struct Raw2;
 template <>

@@ -12,10 +12,13 @@
 //
 // Bound by HBM.  Measured, per call, bf16 (a large copy moves 5.1 TB/s): forward 1 x
 // 32768, 40 and 8 heads of 128 (806 MB) 161 us, 5.0 TB/s; backward 8 x 2048, 16 and 16
-// heads of 128 (403 MB) 80 us with 5 for the second kernel, 5.0 TB/s; the same in fp32 85 and
+// heads of 128 (403 MB) 80 us with 4 for the second kernel, 5.0 TB/s; the same in fp32 85 and
 // 130 us (537 and 805 MB; outputs stay in the last-level cache).  Heads of 64 (8 x 2048, 32
-// and 4: 151 and 227 MB) 39 and 56 us, 3.9 and 4.0 TB/s: blocks of 8 heads form the angles five times.  The forward runs six waves per SIMD (with five the
-// first takes 7% longer).
+// and 4: 151 and 227 MB) 39 and 56 us, 3.9 and 4.0 TB/s: blocks of 8 heads form the angles five times.  Heads of
+// 80 and 160, which leave 6 of 16 and 12 of 32 lanes idle (8 x 2048, 16 and 16): 50 and 100 us forward, 72 and 141
+// backward, 3.4 to 3.6 TB/s.  Single tokens, 40 and 8 heads of 128: 3.4 us for one, 8.4 for 256 (6 MB in 96
+// workgroups), since a group of lanes takes its rows one after the other however few there are.  The forward
+// runs six waves per SIMD (with five the first takes 7% longer).
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
 

@@ -5,15 +5,18 @@
 // floor; what keeps the kernels above it is that a workgroup loads, computes, waits for
 // the state before its chunk and stores in turn, and registers let only two workgroups
 // share a CU.  Vector units are active for half of the time (34 vector instructions
-// per element forward, 6 of them transcendental, and 59 with 7 backward), waves wait two fifths of it.
+// per element forward, 6 of them transcendental, and 68 with 7 backward), waves wait two fifths of it.
 // Measured, per call (a large copy moves 5.1 TB/s), bf16 in power form with an input gate:
 //   forward   8 x 2048 x 2048 (268 MB)            62 us, 4.3 TB/s (one lane per channel: 1782 us)
 //             4 x 4096 x 5120 (671 MB)           134 us, 5.0 TB/s
 //             1 x 32768 x 5120, z (1.68 GB)      334 us, 5.0 TB/s
 //             1 x 1048576 x 1024 (8.6 GB)        2.00 ms, 4.3 TB/s
-//   backward  8 x 2048 x 2048 (471 MB)           124 us, 3.8 TB/s (one lane per channel: 3298 us)
+//   backward  8 x 2048 x 2048 (471 MB)           116 to 125 us, 3.8 to 4.0 TB/s (one lane per channel: 3298 us)
 //             1 x 32768 x 5120, z (3.0 GB)       698 us, 4.3 TB/s
-//   one token 256 x 5120, z (24 MB)              6 us (7.5 us at the profiler's lower clocks)
+//   one token 256 x 5120, z (24 MB)              6 us
+//   narrow and long, where the states' way through the chunks is what takes the time:
+//             1 x 32768 x 256                    54 us forward, 47 backward (67 and 118 MB)
+//             1 x 32768 x 1024                   72 and 122 us (268 and 471 MB)
 #include "mixer_device.hpp"
 #include "mixer_kernels.hpp"
 

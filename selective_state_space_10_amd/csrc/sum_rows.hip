@@ -1,7 +1,7 @@
 // sum_rows.hip -- the sums over rows of partial sums that end the backward passes of the
 // gated recurrence, the causal convolution and the norm of heads: a workgroup takes
 // 16 columns, 64 lanes' worth of rows each in turn, all in a fixed order.  A launch
-// of its own takes about 4.5 us, latency for the most part (128 rows x 2048 and 60 rows x 10240).
+// of its own takes about 4 us, latency for the most part (128 rows x 2048 and 60 rows x 10240).
 #include "mixer_kernels.hpp"
 
 namespace ssm {
