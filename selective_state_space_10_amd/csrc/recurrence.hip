@@ -55,8 +55,9 @@ __device__ __forceinline__ Gate gate_of(float g, float rate2) {
 
 // softplus to fp32's rounding: e^-|v| by the exponent's rounded product and what that
 // leaves out, log1p by the logarithm of the rounded 1 + w and what that leaves out.
+// (Below -200, -infinity too, e^-|v| is zero; a comparison, which lets NaN through.)
 __device__ __forceinline__ float softplus_full(float v) {
-  const float m = -fabsf(v), t = m * kLog2e;
+  const float m = fabsf(v) > 200.0f ? -200.0f : -fabsf(v), t = m * kLog2e;
   const float rest = fmaf(m, kLog2e, -t) + m * 1.9259629911266175e-8f;  // log2 e = kLog2e + 1.93e-8
   float w = fast_exp2(t);
   w = fmaf(w, rest * kLn2, w);

@@ -205,6 +205,22 @@ def test_extreme_decays(ssm, decay):
     compare(ssm, p, ref.on_gpu(p))
 
 
+def test_infinite_decays(ssm):
+    """softplus(-inf) = 0: nothing is forgotten and nothing comes in; softplus(inf) = inf: every step forgets all."""
+    p = ref.recurrence_inputs(2, 130, 16)
+    p["decay"][::2] = -math.inf
+    compare(ssm, p, ref.on_gpu(p))
+    p["decay"][::2] = math.inf
+    y, final, _, _ = ref.recurrence(p, grads=False)
+    got = forward(ssm, ref.on_gpu(p))
+    assert ref.error(got[0], y) <= tol(130) and ref.error(got[1], final) <= tol(130)
+    state = p["state0"].cuda()
+    ssm.gated_recurrence_update(state, *(p[n][:, 0].cuda() for n in ("x", "decay_gate", "input_gate")), p["decay"].cuda())
+    assert ref.error(state[:, ::2], (torch.sigmoid(p["input_gate"]) * p["x"])[:, 0, ::2].double()) <= tol(1)
+    p["decay"][3] = math.nan
+    assert torch.isnan(forward(ssm, ref.on_gpu(p))[1][:, 3]).all()
+
+
 def gates(D, dtype, form, seed=0):
     """One step whose factors do not cancel in any gradient: state and adjoints of one sign, inputs of the other."""
     p = ref.recurrence_inputs(3, 1, D, form=form, z=False, dtype=dtype, seed=seed)
