@@ -318,7 +318,7 @@ int ssm_causal_conv_update(int64_t batch, int64_t dim, int width, int io_dtype, 
  *   q_out, k_out: contiguous, io_dtype
  *
  * dim: a multiple of 8 from 8 to 256; rotary: a multiple of 8 up to dim; heads
- * in all <= 65536; batch * seqlen <= 2^40.
+ * in all <= 65536; batch * seqlen * heads in all * dim <= 2^40.
  */
 int ssm_head_norm_rotary_fwd(int64_t batch, int64_t seqlen, int64_t q_heads, int64_t k_heads, int64_t dim,
                              int64_t rotary, int io_dtype, const ssm_view4 *q, const ssm_view4 *k,

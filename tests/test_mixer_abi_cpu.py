@@ -125,6 +125,13 @@ def test_head_refusals(lib, kw, want):
     assert lib.ssm_last_error()
 
 
+def test_head_elements(lib):
+    """2^40 elements of queries and keys together, by the workspace's query, which has the same limits."""
+    need = lib.ssm_head_norm_rotary_bwd_workspace_bytes
+    assert need(1, 1 << 32, 3, 1, 64) > 0 and need(1, (1 << 32) + 1, 3, 1, 64) == -1
+    assert heads_fwd(lib, B=1 << 16, L=(1 << 16) + 1, Hq=3, Hk=1) == BAD_SHAPE
+
+
 @pytest.mark.parametrize("name", ["q", "k"])
 @pytest.mark.parametrize("kw,want", [(dict(ptr=0), NULL_ARG), (dict(ptr=FAKE + 8), ALIGNMENT), (dict(sh=34), ALIGNMENT), (dict(st=-64), BAD_SHAPE)])
 def test_head_views(lib, name, kw, want):
